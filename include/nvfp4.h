@@ -198,6 +198,172 @@ int nvfp4_gemm(const uint8_t *codes, const uint8_t *scales, const float *alpha, 
                int64_t cols, const void *x, int batch, float *y, cudaStream_t stream);
 
 /*
+ * nvfp4_linear -- the W4A16 product with its epilogue, for a decoder layer's
+ *   projections:
+ *     y[b][r] = bf16_rne( residual[b][r] + gate[b][r] * act(
+ *                         alpha * sum_c q[r][c] Delta[r][c/16] x[b][c] + bias[r] ) )
+ *   with fp32 accumulation and an fp32 epilogue, rounded once.  Unlike
+ *   nvfp4_gemv and nvfp4_gemm the weights are not rounded to bf16 first:
+ *   q * Delta has at most six significant bits, so it enters the products
+ *   exactly, and alpha multiplies the finished sum.  The order of the
+ *   additions is fixed by the shape and the device, so results repeat bit for
+ *   bit.  (The method's pages quantize weights for such products; this is a
+ *   consumer of the path.)
+ * Arguments:
+ *   codes, scales, alpha, rows, cols  a quantized tensor as nvfp4_quantize
+ *          writes it (device; codes 8-byte aligned).
+ *   x      device, bf16, 16-byte aligned, [batch, cols], consecutive rows
+ *          x_stride elements apart (>= cols, a multiple of 8).  Finite.
+ *   batch  >= 0 vectors (0: nothing is enqueued).  More than 256 run in slices
+ *          of 256.
+ *   epilogue  host struct (read during the call only), or NULL for none:
+ *          bias [rows], gate and residual [batch, rows] with rows gate_stride
+ *          and residual_stride elements apart; each device, bf16, 2-byte
+ *          aligned, or NULL; activation an nvfp4_activation.
+ *   y      device, bf16, 2-byte aligned, [batch, rows] with rows y_stride
+ *          elements apart (>= rows).  y may be the residual or the gate
+ *          itself (same address and stride).
+ *   workspace  device, 256-byte aligned, nvfp4_linear_workspace_bytes(rows,
+ *          cols, batch) bytes, or NULL: then the library's pool provides it.
+ *          A caller's workspace must be all zero before its first use; each
+ *          call leaves it ready for the next one of any shape that it is
+ *          large enough for.  Calls that may overlap on the GPU need
+ *          workspaces of their own.
+ *   stream cudaStream_t.
+ * Returns an nvfp4_status.  nvfp4_linear_workspace_bytes returns -1 for an
+ * invalid shape or without a supported device.
+ */
+enum nvfp4_activation {
+  NVFP4_ACT_NONE = 0,
+  NVFP4_ACT_RELU = 1,       /* max(v, 0) */
+  NVFP4_ACT_GELU = 2,       /* v/2 (1 + erf(v / sqrt 2)) */
+  NVFP4_ACT_GELU_TANH = 3,  /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+  NVFP4_ACT_SILU = 4        /* v / (1 + exp(-v)) */
+};
+typedef struct nvfp4_epilogue {
+  const void *bias;
+  const void *gate;
+  int64_t gate_stride;
+  const void *residual;
+  int64_t residual_stride;
+  int activation;
+} nvfp4_epilogue;
+int64_t nvfp4_linear_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
+int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows,
+                 int64_t cols, const void *x, int64_t x_stride, int64_t batch,
+                 const nvfp4_epilogue *epilogue, void *y, int64_t y_stride, void *workspace,
+                 cudaStream_t stream);
+
+/*
+ * A paged key-value cache: `pages` pages of page_size tokens; page p holds
+ * keys [kv_heads][page_size][head_dim] at k + p * k_page_stride elements
+ * (contiguous inside a page) and values likewise at v.  Token t of a sequence
+ * lives in row t % page_size of the page that entry t / page_size of the
+ * sequence's row of the page table names.
+ *   k, v        device, 16-byte aligned.  dtype NVFP4_DTYPE_BF16 or
+ *               NVFP4_DTYPE_E4M3.
+ *   *_page_stride  elements between pages, >= kv_heads * page_size * head_dim,
+ *               a multiple of 16 bytes (keys and values may share one
+ *               allocation).
+ *   page_size   a power of two, 8 .. 65536.  head_dim 64, 128 or 256.
+ *               pages and kv_heads * page_size below 2^31.
+ *   k_scale, v_scale  E4M3 only: device, [kv_heads] fp32 > 0, the value of one
+ *               unit of that head's codes (value = code * scale), or NULL for
+ *               1.  Must be NULL for bf16.
+ */
+enum nvfp4_dtype { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_FP32 = 1, NVFP4_DTYPE_E4M3 = 2 };
+typedef struct nvfp4_kv_cache {
+  void *k;
+  void *v;
+  int64_t k_page_stride;
+  int64_t v_page_stride;
+  int64_t pages;
+  int page_size;
+  int kv_heads;
+  int head_dim;
+  int dtype;
+  const float *k_scale;
+  const float *v_scale;
+} nvfp4_kv_cache;
+
+/*
+ * nvfp4_kv_append -- writes the keys and values of new tokens into a paged
+ *   cache, rotating queries and keys by position on the way:
+ *     (a, b) -> (a cos - b sin, b cos + a sin), every product and sum rounded
+ *   to fp32, for the pairs (i, i + rotary_dim/2) or, interleaved, (2i, 2i + 1)
+ *   of each head's first rotary_dim dimensions; the others pass unchanged.
+ *   bf16 caches store bf16_rne; E4M3 caches store e4m3_rne(value * (1 / scale))
+ *   saturating at +-448, the reciprocal rounded to fp32.
+ * Arguments:
+ *   cache   host struct, see above.
+ *   qkv     device, 16-byte aligned, bf16 or fp32 (qkv_dtype): one row per
+ *           token, qkv_stride elements apart (a multiple of 16 bytes):
+ *           q_heads query heads, kv_heads key heads, kv_heads value heads of
+ *           head_dim each.
+ *   tokens  >= 0.  q_heads >= 0.
+ *   seq, pos  device, [tokens] int32: each token's sequence and position.  Two
+ *           tokens of one call must not name the same slot.
+ *   table   device, int32, [sequences] rows of table_width page numbers,
+ *           table_stride entries apart.
+ *   cos_sin device, fp32, 16-byte aligned, [positions][rotary_dim]: per
+ *           position rotary_dim/2 cosines, then as many sines.
+ *   rotary_dim  0 .. head_dim, a multiple of 16 (0: no rotation, cos_sin
+ *           unused).
+ *   interleaved  0 or 1.
+ *   q_out   device, bf16, 16-byte aligned, [tokens][q_heads][head_dim]
+ *           (written: the rotated queries).  Unused with q_heads 0.
+ * A token is skipped (q_out zeros, nothing stored) when its seq is outside
+ * [0, sequences), its pos is negative, past the table's width or (with
+ * rotation) not below `positions`, or its page is not in [0, pages): padding
+ * tokens of a captured batch carry pos = -1.
+ * Returns an nvfp4_status.
+ */
+int nvfp4_kv_append(const nvfp4_kv_cache *cache, const void *qkv, int qkv_dtype, int64_t qkv_stride,
+                    int64_t tokens, int q_heads, const int32_t *seq, const int32_t *pos,
+                    const int32_t *table, int64_t sequences, int64_t table_width,
+                    int64_t table_stride, const float *cos_sin, int64_t positions, int rotary_dim,
+                    int interleaved, void *q_out, cudaStream_t stream);
+
+/*
+ * nvfp4_paged_attention -- attention of one new token per sequence over a
+ *   paged cache.  With n = lengths[s], query head h reads cache head
+ *   h / (q_heads / kv_heads) at the tokens t in [max(0, n - window), n)
+ *   ([0, n) with window 0):
+ *     s_t = scale * k_scale * (q . k_t),  m = max s_t,  l = sum exp(s_t - m),
+ *     out = v_scale / l * sum exp(s_t - m) v_t,   lse = m + ln l.
+ *   Scores, maxima, sums and outputs are fp32; the weights exp(s_t - m) enter
+ *   the products with V rounded to the 16-bit type of the products.  The order
+ *   of the additions depends on the lengths and the device only, so results
+ *   repeat bit for bit.  An empty row (n <= 0) gives out = 0, lse = -inf, as
+ *   does a row whose scores are all -inf.
+ * Arguments:
+ *   cache   host struct, see above.
+ *   q       device, bf16, 16-byte aligned, [sequences][q_heads][head_dim],
+ *           sequences q_stride elements apart (a multiple of 8).
+ *   sequences 0 .. 65535.  q_heads a multiple of kv_heads, at most 1024.
+ *   lengths device, [sequences] int32: tokens in the cache, the new one
+ *           included; clipped to [0, table_width * page_size].
+ *   table   as for nvfp4_kv_append.  Entries behind a sequence's last page are
+ *           not read; an entry outside [0, pages) reads as zeros.
+ *   scale   the score's factor (finite).  window >= 0.
+ *   out     device, bf16, 16-byte aligned, [sequences][q_heads][head_dim]
+ *           (written).
+ *   lse     device, fp32, 4-byte aligned, [sequences][q_heads] (written), or
+ *           NULL.
+ *   workspace  as for nvfp4_linear, nvfp4_paged_attention_workspace_bytes(
+ *           cache, q_heads) bytes whatever the sequences and lengths; or NULL.
+ * Returns an nvfp4_status.  Stored keys and values behind a sequence's length
+ * may hold anything.  Every wait inside the kernel is bounded: should a copy
+ * never complete, the affected outputs are NaN.
+ */
+int64_t nvfp4_paged_attention_workspace_bytes(const nvfp4_kv_cache *cache, int q_heads);
+int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_stride,
+                          int64_t sequences, int q_heads, const int32_t *lengths,
+                          const int32_t *table, int64_t table_width, int64_t table_stride,
+                          float scale, int64_t window, void *out, float *lse, void *workspace,
+                          cudaStream_t stream);
+
+/*
  * nvfp4_swizzle_scales -- the E4M3 block scales of a quantized [rows, cols]
  *   tensor, from the linear [rows, cols/16] layout that nvfp4_quantize
  *   writes to the layout block-scaled tensor-core matrix multiplies read

@@ -22,7 +22,27 @@ MODES = {"max": MAX, "four_over_six": FOUR_OVER_SIX, "cjso": CJSO, "cjso_decoupl
 NVFP4_OK = 0
 NVFP4_GROUP_MAX = 256
 
+# activations of the product's epilogue
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
+               "silu": ACT_SILU}
+DTYPE_BF16, DTYPE_FP32, DTYPE_E4M3 = 0, 1, 2
+
 _lib = None
+
+
+class nvfp4_epilogue(ctypes.Structure):
+    """The epilogue of nvfp4_linear (include/nvfp4.h)."""
+    _fields_ = [("bias", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64), ("activation", ctypes.c_int)]
+
+
+class nvfp4_kv_cache(ctypes.Structure):
+    """A paged key-value cache (include/nvfp4.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_page_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class nvfp4_tensor(ctypes.Structure):
@@ -62,6 +82,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_gemv.restype = ci
     L.nvfp4_gemm.argtypes = [vp, vp, vp, i64, i64, vp, ci, vp, vp]
     L.nvfp4_gemm.restype = ci
+    L.nvfp4_linear_workspace_bytes.argtypes = [i64, i64, i64]
+    L.nvfp4_linear_workspace_bytes.restype = i64
+    L.nvfp4_linear.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, ctypes.POINTER(nvfp4_epilogue), vp, i64, vp, vp]
+    L.nvfp4_linear.restype = ci
+    L.nvfp4_kv_append.argtypes = [ctypes.POINTER(nvfp4_kv_cache), vp, ci, i64, i64, ci, vp, vp, vp, i64, i64, i64,
+                                  vp, i64, ci, ci, vp, vp]
+    L.nvfp4_kv_append.restype = ci
+    L.nvfp4_paged_attention_workspace_bytes.argtypes = [ctypes.POINTER(nvfp4_kv_cache), ci]
+    L.nvfp4_paged_attention_workspace_bytes.restype = i64
+    L.nvfp4_paged_attention.argtypes = [ctypes.POINTER(nvfp4_kv_cache), vp, i64, i64, ci, vp, vp, i64, i64,
+                                        ctypes.c_float, i64, vp, vp, vp, vp]
+    L.nvfp4_paged_attention.restype = ci
     L.nvfp4_swizzled_scales_bytes.argtypes = [i64, i64]
     L.nvfp4_swizzled_scales_bytes.restype = i64
     L.nvfp4_swizzle_scales.argtypes = [vp, i64, i64, vp, vp]
@@ -132,6 +164,35 @@ def nvfp4_gemv(codes, scales, alpha, rows, cols, x, batch, y, stream) -> int:
 
 def nvfp4_gemm(codes, scales, alpha, rows, cols, x, batch, y, stream) -> int:
     return load().nvfp4_gemm(codes, scales, alpha, rows, cols, x, batch, y, stream)
+
+
+def nvfp4_linear_workspace_bytes(rows, cols, batch) -> int:
+    return load().nvfp4_linear_workspace_bytes(rows, cols, batch)
+
+
+def nvfp4_linear(codes, scales, alpha, rows, cols, x, x_stride, batch, epilogue, y, y_stride, workspace,
+                 stream) -> int:
+    """`epilogue`: an nvfp4_epilogue (passed by reference) or None."""
+    return load().nvfp4_linear(codes, scales, alpha, rows, cols, x, x_stride, batch, epilogue, y, y_stride,
+                               workspace, stream)
+
+
+def nvfp4_kv_append(cache, qkv, qkv_dtype, qkv_stride, tokens, q_heads, seq, pos, table, sequences, table_width,
+                    table_stride, cos_sin, positions, rotary_dim, interleaved, q_out, stream) -> int:
+    """`cache`: an nvfp4_kv_cache (passed by reference)."""
+    return load().nvfp4_kv_append(cache, qkv, qkv_dtype, qkv_stride, tokens, q_heads, seq, pos, table, sequences,
+                                  table_width, table_stride, cos_sin, positions, rotary_dim, interleaved, q_out,
+                                  stream)
+
+
+def nvfp4_paged_attention_workspace_bytes(cache, q_heads) -> int:
+    return load().nvfp4_paged_attention_workspace_bytes(cache, q_heads)
+
+
+def nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table, table_width, table_stride, scale,
+                          window, out, lse, workspace, stream) -> int:
+    return load().nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table, table_width,
+                                        table_stride, scale, window, out, lse, workspace, stream)
 
 
 def nvfp4_swizzled_scales_bytes(rows, cols) -> int:
@@ -353,6 +414,208 @@ def gemm(codes, scales, alpha, rows: int, cols: int, x, out=None, stream=None):
     _check(nvfp4_gemm(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, x.data_ptr(), batch,
                       y.data_ptr(), _stream_ptr(stream)), "nvfp4_gemm")
     return y
+
+
+def _on(stream, *tensors):
+    """The stream to launch on; tensors made here for a stream other than the
+    current one are kept from reuse until that stream has passed this point."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _workspace(nbytes: int, device):
+    """A zeroed workspace (zeroed on the current stream, like any new tensor)."""
+    import torch
+    if nbytes < 0:
+        raise ValueError("invalid shape, or no supported device")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def _rows_of(t, batch: int, width: int, what: str):
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.shape != (batch, width) or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a bf16 CUDA tensor [{batch}, {width}] with contiguous rows")
+    return t.data_ptr(), t.stride(0) if batch > 1 and width > 0 else 8 * ((width + 7) // 8)
+
+
+def linear_workspace(rows: int, cols: int, batch: int, device="cuda"):
+    """A workspace for linear() of this shape or smaller batches, kept by the
+    caller from call to call (one per stream that such calls run on)."""
+    return _workspace(nvfp4_linear_workspace_bytes(rows, cols, batch), device)
+
+
+def linear(codes, scales, alpha, rows: int, cols: int, x, bias=None, activation=None, gate=None, residual=None,
+           out=None, workspace=None, stream=None):
+    """The W4A16 product with its epilogue: bf16 y [batch, rows] =
+    residual + gate * activation(W x + bias), W = q * Delta * alpha, for bf16 x
+    [batch, cols]; bias [rows], gate and residual [batch, rows] bf16 or None.
+    x, gate, residual and out may have rows further apart than their width;
+    out may be the residual.  See nvfp4_linear in include/nvfp4.h."""
+    import torch
+    if x.dim() == 1:
+        x = x.unsqueeze(0)
+    batch = x.shape[0]
+    xp, xs = _rows_of(x, batch, cols, "x")
+    if codes.numel() * 2 != rows * cols or scales.numel() * 16 != rows * cols or not codes.is_contiguous() or \
+            not scales.is_contiguous():
+        raise ValueError("codes and scales must be contiguous and hold [rows, cols] elements")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)}")
+    ep = nvfp4_epilogue(activation=ACTIVATIONS[activation])
+    if bias is not None:
+        if bias.dtype != torch.bfloat16 or not bias.is_cuda or bias.shape != (rows,) or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous bf16 CUDA tensor [rows]")
+        ep.bias = bias.data_ptr()
+    if gate is not None:
+        ep.gate, ep.gate_stride = _rows_of(gate, batch, rows, "gate")
+    if residual is not None:
+        ep.residual, ep.residual_stride = _rows_of(residual, batch, rows, "residual")
+    made = None
+    if out is None:
+        out = made = torch.empty((batch, rows), dtype=torch.bfloat16, device=x.device)
+    yp, ys = _rows_of(out, batch, rows, "out")
+    if workspace is not None and (not workspace.is_cuda or
+                                  workspace.nbytes < nvfp4_linear_workspace_bytes(rows, cols, batch)):
+        raise ValueError("workspace too small: make it with linear_workspace(rows, cols, batch)")
+    _check(nvfp4_linear(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, xp, xs, batch,
+                        ctypes.byref(ep), yp, ys, None if workspace is None else workspace.data_ptr(),
+                        _on(stream, made)), "nvfp4_linear")
+    return out
+
+
+class KVCache:
+    """A paged key-value cache: k and v bf16 or float8_e4m3fn CUDA tensors
+    [pages, kv_heads, page_size, head_dim], contiguous inside a page (the pages
+    may lie further apart); k_scale and v_scale [kv_heads] fp32 give the value
+    of one unit of an E4M3 cache (None: 1).  The tensors stay the caller's;
+    this object is the handle that kv_append and paged_attention take."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        kinds = {torch.bfloat16: DTYPE_BF16, torch.float8_e4m3fn: DTYPE_E4M3}
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in kinds or not k.is_cuda or \
+                k.device != v.device:
+            raise ValueError("k and v must be alike: bf16 or float8_e4m3fn CUDA tensors "
+                             "[pages, kv_heads, page_size, head_dim]")
+        pages, heads, size, dim = k.shape
+        for t in (k, v):
+            if pages > 0 and not t[0].is_contiguous():
+                raise ValueError("keys and values must be contiguous inside a page")
+        for t in (k_scale, v_scale):
+            if t is not None and (k.dtype == torch.bfloat16 or t.dtype != torch.float32 or t.device != k.device or
+                                  t.shape != (heads,) or not t.is_contiguous()):
+                raise ValueError("scales are for E4M3 caches: contiguous fp32 CUDA tensors [kv_heads]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, dim
+        page = heads * size * dim
+        self.desc = nvfp4_kv_cache(k.data_ptr(), v.data_ptr(), k.stride(0) if pages > 1 else page,
+                                   v.stride(0) if pages > 1 else page, pages, size, heads, dim, kinds[k.dtype],
+                                   None if k_scale is None else k_scale.data_ptr(),
+                                   None if v_scale is None else v_scale.data_ptr())
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=None, device="cuda", k_scale=None,
+              v_scale=None):
+        """A cache of uninitialised pages (dtype: torch.bfloat16, the default, or torch.float8_e4m3fn)."""
+        import torch
+        shape = (pages, kv_heads, page_size, head_dim)
+        make = lambda: torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)  # noqa: E731
+        return cls(make(), make(), k_scale, v_scale)
+
+
+def _ints(t, shape, what: str):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 CUDA tensor {list(shape)}")
+    return t.data_ptr()
+
+
+def _table_of(table):
+    import torch
+    if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or \
+            (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be an int32 CUDA tensor [sequences, pages of a sequence] with contiguous rows")
+    n, width = table.shape
+    return table.data_ptr(), n, width, table.stride(0) if n > 1 else width
+
+
+def kv_append(cache: KVCache, qkv, q_heads: int, seq, pos, table, cos_sin=None, interleaved: bool = False, out=None,
+              stream=None):
+    """Writes the keys and values of new tokens into the cache and returns the
+    queries, bf16 [tokens, q_heads, head_dim]; queries and keys are rotated by
+    position on the way.  qkv: bf16 or fp32 CUDA [tokens, (q_heads + 2 kv_heads)
+    * head_dim]; seq, pos: int32 [tokens] (pos -1: padding); table: int32
+    [sequences, pages]; cos_sin: fp32 [positions, rotary_dim], cosines then
+    sines (None: no rotation).  See nvfp4_kv_append in include/nvfp4.h."""
+    import torch
+    width = (q_heads + 2 * cache.kv_heads) * cache.head_dim
+    if qkv.dtype not in (torch.bfloat16, torch.float32) or not qkv.is_cuda or qkv.dim() != 2 or \
+            qkv.shape[1] != width or qkv.stride(1) != 1:
+        raise ValueError(f"qkv must be a bf16 or fp32 CUDA tensor [tokens, {width}] with contiguous rows")
+    tokens = qkv.shape[0]
+    sp, pp = _ints(seq, (tokens,), "seq"), _ints(pos, (tokens,), "pos")
+    tp, sequences, pages, stride = _table_of(table)
+    positions = rotary = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
+        positions, rotary = cos_sin.shape
+    shape, made = (tokens, q_heads, cache.head_dim), None
+    if out is None:
+        out = made = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
+    elif out.dtype != torch.bfloat16 or not out.is_cuda or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bf16 CUDA tensor {list(shape)}")
+    _check(nvfp4_kv_append(cache.desc, qkv.data_ptr(), DTYPE_FP32 if qkv.dtype == torch.float32 else DTYPE_BF16,
+                           qkv.stride(0) if tokens > 1 else width, tokens, q_heads, sp, pp, tp, sequences, pages,
+                           stride, None if cos_sin is None else cos_sin.data_ptr(), positions, rotary,
+                           int(interleaved), out.data_ptr(), _on(stream, made)), "nvfp4_kv_append")
+    return out
+
+
+def attention_workspace(cache: KVCache, q_heads: int):
+    """A workspace for paged_attention() over this cache, whatever the batch
+    and the lengths, kept by the caller from call to call (one per stream)."""
+    return _workspace(nvfp4_paged_attention_workspace_bytes(cache.desc, q_heads), cache.k.device)
+
+
+def paged_attention(cache: KVCache, q, table, lengths, scale=None, window: int = 0, out=None, return_lse: bool = False,
+                    workspace=None, stream=None):
+    """Attention of one new token per sequence over the cache: bf16 out like q
+    [sequences, q_heads, head_dim], with return_lse also the fp32 log-sum-exp
+    [sequences, q_heads].  lengths: int32 [sequences], tokens in the cache with
+    the new one (0: an empty row); window: only the last `window` tokens (0:
+    all); scale: head_dim ** -0.5 by default.  See nvfp4_paged_attention in
+    include/nvfp4.h."""
+    import torch
+    if q.dtype != torch.bfloat16 or not q.is_cuda or q.dim() != 3 or q.shape[2] != cache.head_dim or \
+            q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != cache.head_dim):
+        raise ValueError("q must be a bf16 CUDA tensor [sequences, q_heads, head_dim] with contiguous sequences")
+    n, heads, dim = q.shape
+    tp, sequences, pages, stride = _table_of(table)
+    if sequences != n:
+        raise ValueError("table must have one row per sequence")
+    lp = _ints(lengths, (n,), "lengths")
+    made = lse = None
+    if out is None:
+        out = made = torch.empty((n, heads, dim), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or not out.is_cuda or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 CUDA tensor shaped like q")
+    if return_lse:
+        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    if workspace is not None and (not workspace.is_cuda or
+                                  workspace.nbytes < nvfp4_paged_attention_workspace_bytes(cache.desc, heads)):
+        raise ValueError("workspace too small: make it with attention_workspace(cache, q_heads)")
+    _check(nvfp4_paged_attention(cache.desc, q.data_ptr(), q.stride(0) if n > 1 else heads * dim, n, heads, lp, tp,
+                                 pages, stride, dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                 None if lse is None else lse.data_ptr(),
+                                 None if workspace is None else workspace.data_ptr(), _on(stream, made, lse)),
+           "nvfp4_paged_attention")
+    return (out, lse) if return_lse else out
 
 
 def swizzle_scales(scales, rows: int, cols: int, stream=None):

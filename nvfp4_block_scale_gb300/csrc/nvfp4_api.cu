@@ -182,19 +182,64 @@ int grid_for(const DevInfo &d, int kern, int64_t work_items) {
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
+// The checks that a cache's description and its page table get, and their
+// translation for the kernels.
+int kv_args(const nvfp4_kv_cache *c, KvArgs *a) {
+  if (!c) return NVFP4_ERR_INVALID_ARG;
+  const bool e4m3 = c->dtype == NVFP4_DTYPE_E4M3;
+  if (!e4m3 && (c->dtype != NVFP4_DTYPE_BF16 || c->k_scale || c->v_scale)) return NVFP4_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NVFP4_ERR_INVALID_ARG;
+  if (c->page_size < 8 || c->page_size > 65536 || (c->page_size & (c->page_size - 1))) return NVFP4_ERR_INVALID_ARG;
+  if (c->kv_heads < 1 || int64_t(c->kv_heads) * c->page_size > INT32_MAX) return NVFP4_ERR_INVALID_ARG;
+  if (c->pages < 0 || c->pages > INT32_MAX || (c->pages > 0 && (!c->k || !c->v))) return NVFP4_ERR_INVALID_ARG;
+  const int64_t page = int64_t(c->kv_heads) * c->page_size * c->head_dim, unit = e4m3 ? 16 : 8;
+  for (const int64_t stride : {c->k_page_stride, c->v_page_stride}) {
+    // the last page's last byte stays inside the 64-bit byte range
+    if (stride < page || stride > INT64_MAX / 4 / std::max<int64_t>(1, c->pages)) return NVFP4_ERR_INVALID_ARG;
+    if (stride % unit) return NVFP4_ERR_MISALIGNED;
+  }
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return NVFP4_ERR_MISALIGNED;
+  *a = KvArgs{c->k, c->v, c->k_page_stride, c->v_page_stride, c->pages, 0, c->kv_heads, c->head_dim, e4m3,
+              c->k_scale, c->v_scale, nullptr, 0, 0};
+  while ((1 << a->page_shift) < c->page_size) ++a->page_shift;
+  return NVFP4_OK;
+}
+
+int kv_table(KvArgs *a, const int32_t *table, int64_t sequences, int64_t width, int64_t stride) {
+  if (sequences < 0 || sequences > INT32_MAX || width < 0 || width > INT32_MAX || stride < width ||
+      stride > INT64_MAX / 4 / std::max<int64_t>(1, sequences) || (sequences > 0 && width > 0 && !table))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(table, 4)) return NVFP4_ERR_MISALIGNED;
+  a->table = table;
+  a->table_width = width;
+  a->table_stride = stride;
+  return NVFP4_OK;
+}
+
+// A product's or an attention's workspace begins with counters that every
+// call finds and leaves zero; a workspace from the pool gets them cleared.
+cudaError_t take_workspace(void **ws, size_t bytes, const DevInfo &d, cudaStream_t stream) {
+  if (bytes == 0) return cudaSuccess;
+  cudaError_t e = pool_alloc(ws, bytes, d.pool, stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(*ws, 0, std::min<size_t>(bytes, kCounterBytes), stream);
+  return e;
+}
+
 // ---------------------------------------------------------------------------
 // Kernel tracing: CUDA events around each launch while enabled.
 // ---------------------------------------------------------------------------
 
 enum { kTrAmax = 0, kTrQuantMax, kTrQuantFos, kTrCjsoInit, kTrCjsoIter, kTrDecoupled, kTrDequant, kTrEncode,
        kTrGroupAmax, kTrGroupQuantMax, kTrGroupQuantFos, kTrGemv, kTrSwizzle, kTrAmaxLdg, kTrGemmTc,
-       kTrGemmTcReduce, kTrKinds };
+       kTrGemmTcReduce, kTrLinear, kTrKvAppend, kTrAttend, kTrKinds };
 const char *const kTraceNames[kTrKinds] = {"k_amax_bulk",        "k_quant_max_fos<max>", "k_quant_max_fos<fos>",
                                            "k_cjso_sweep<init>",  "k_cjso_sweep<iter>",   "k_decoupled",
                                            "k_dequant",           "k_encode",             "k_group_amax",
                                            "k_group_quant<max>",  "k_group_quant<fos>",   "k_gemv",
                                            "k_swizzle_scales",   "k_amax_partials",      "k_gemm_tc",
-                                           "k_gemm_tc_reduce"};
+                                           "k_gemm_tc_reduce",   "k_linear",             "k_kv_append",
+                                           "k_attend"};
 
 struct TraceRec {
   int kind;
@@ -517,6 +562,152 @@ int nvfp4_gemm(const uint8_t *codes, const uint8_t *scales, const float *alpha, 
     e = launch_gemm_tc_reduce(part, rows, cols, batch, d->sms, y, grid_for(*d, kKernDequant, ny), stream);
   }
   cudaError_t ef = cudaFreeAsync(ws, stream);
+  return map_cuda(e != cudaSuccess ? e : ef);
+}
+
+int64_t nvfp4_linear_workspace_bytes(int64_t rows, int64_t cols, int64_t batch) {
+  if (check_shape(rows, cols) != NVFP4_OK || batch < 0) return -1;
+  DevInfo *d = nullptr;
+  if (device_info(&d) != NVFP4_OK) return -1;
+  if (rows == 0 || cols == 0 || batch == 0) return 0;
+  // the largest slice and the last one
+  size_t need = linear_workspace_bytes(rows, cols, (int)std::min<int64_t>(batch, kLinearSlice), d->sms);
+  if (batch > kLinearSlice && batch % kLinearSlice)
+    need = std::max(need, linear_workspace_bytes(rows, cols, (int)(batch % kLinearSlice), d->sms));
+  return (int64_t)need;
+}
+
+int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows, int64_t cols,
+                 const void *x, int64_t x_stride, int64_t batch, const nvfp4_epilogue *epilogue, void *y,
+                 int64_t y_stride, void *workspace, cudaStream_t stream) {
+  int st = check_shape(rows, cols);
+  if (st != NVFP4_OK) return st;
+  const nvfp4_epilogue none = {};
+  const nvfp4_epilogue &ep = epilogue ? *epilogue : none;
+  if (batch < 0 || ep.activation < NVFP4_ACT_NONE || ep.activation > NVFP4_ACT_SILU) return NVFP4_ERR_INVALID_ARG;
+  auto bad_stride = [&](int64_t s, int64_t width) {
+    return s < width || s >= kMaxElems || (batch > 0 && s > INT64_MAX / 4 / batch);
+  };
+  if (bad_stride(x_stride, cols) || bad_stride(y_stride, rows) || (ep.gate && bad_stride(ep.gate_stride, rows)) ||
+      (ep.residual && bad_stride(ep.residual_stride, rows)))
+    return NVFP4_ERR_INVALID_ARG;
+  const bool work = rows > 0 && batch > 0, sum = work && cols > 0;
+  if (!alpha || (work && !y) || (sum && (!codes || !scales || !x))) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(alpha, 4) || !aligned(y, 2) || !aligned(ep.bias, 2) || !aligned(ep.gate, 2) ||
+      !aligned(ep.residual, 2) || !aligned(workspace, 256) || x_stride % 8 != 0 ||
+      (sum && (!aligned(codes, 8) || !aligned(x, 16))))
+    return NVFP4_ERR_MISALIGNED;
+  DevInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != NVFP4_OK) return st;
+  if (!work) return NVFP4_OK;
+  const size_t bytes = cols == 0 ? 0 : (size_t)nvfp4_linear_workspace_bytes(rows, cols, batch);
+  void *own = nullptr;
+  cudaError_t e = workspace ? cudaSuccess : take_workspace(&own, bytes, *d, stream);
+  for (int64_t b = 0; b < batch && e == cudaSuccess; b += kLinearSlice) {
+    auto at = [&](const void *p, int64_t stride) {
+      return p ? static_cast<const char *>(p) + 2 * b * stride : nullptr;
+    };
+    const LinearArgs a = {codes, scales, alpha, rows, cols, at(x, x_stride), x_stride,
+                          (int)std::min<int64_t>(batch - b, kLinearSlice), ep.bias, at(ep.gate, ep.gate_stride),
+                          ep.gate_stride, at(ep.residual, ep.residual_stride), ep.residual_stride, ep.activation,
+                          const_cast<char *>(at(y, y_stride)), y_stride};
+    TraceScope tr(kTrLinear, stream);
+    e = launch_linear(a, d->sms, workspace ? workspace : own, stream);
+  }
+  const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
+  return map_cuda(e != cudaSuccess ? e : ef);
+}
+
+int nvfp4_kv_append(const nvfp4_kv_cache *cache, const void *qkv, int qkv_dtype, int64_t qkv_stride, int64_t tokens,
+                    int q_heads, const int32_t *seq, const int32_t *pos, const int32_t *table, int64_t sequences,
+                    int64_t table_width, int64_t table_stride, const float *cos_sin, int64_t positions,
+                    int rotary_dim, int interleaved, void *q_out, cudaStream_t stream) {
+  AppendArgs a = {};
+  int st = kv_args(cache, &a.kv);
+  if (st == NVFP4_OK) st = kv_table(&a.kv, table, sequences, table_width, table_stride);
+  if (st != NVFP4_OK) return st;
+  if (qkv_dtype != NVFP4_DTYPE_BF16 && qkv_dtype != NVFP4_DTYPE_FP32) return NVFP4_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > INT32_MAX || q_heads < 0 || q_heads > (1 << 16) || cache->kv_heads > (1 << 16))
+    return NVFP4_ERR_INVALID_ARG;
+  const int64_t width = (int64_t(q_heads) + 2 * int64_t(cache->kv_heads)) * cache->head_dim;
+  const bool fp32 = qkv_dtype == NVFP4_DTYPE_FP32;
+  if (qkv_stride < width || qkv_stride >= kMaxElems) return NVFP4_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > cache->head_dim || rotary_dim % 16 != 0 || (interleaved != 0 && interleaved != 1))
+    return NVFP4_ERR_INVALID_ARG;
+  if (positions < 0 || (tokens > 0 && (!qkv || !seq || !pos || (q_heads > 0 && !q_out) ||
+                                       (rotary_dim > 0 && positions > 0 && !cos_sin))))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(cos_sin, 16) || !aligned(seq, 4) || !aligned(pos, 4) ||
+      qkv_stride % (fp32 ? 4 : 8) != 0)
+    return NVFP4_ERR_MISALIGNED;
+  DevInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != NVFP4_OK) return st;
+  if (tokens == 0) return NVFP4_OK;
+  a.qkv = qkv;
+  a.fp32 = fp32;
+  a.qkv_stride = qkv_stride;
+  a.tokens = tokens;
+  a.q_heads = q_heads;
+  a.seq = seq;
+  a.pos = pos;
+  a.sequences = sequences;
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.rotary = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.q_out = q_out;
+  TraceScope tr(kTrKvAppend, stream);
+  return map_cuda(launch_kv_append(a, d->sms, stream));
+}
+
+int64_t nvfp4_paged_attention_workspace_bytes(const nvfp4_kv_cache *cache, int q_heads) {
+  KvArgs kv = {};
+  if (kv_args(cache, &kv) != NVFP4_OK || q_heads < kv.kv_heads || q_heads > kMaxQHeads || q_heads % kv.kv_heads)
+    return -1;
+  DevInfo *d = nullptr;
+  if (device_info(&d) != NVFP4_OK) return -1;
+  return (int64_t)attend_workspace_bytes(kv, q_heads, d->sms);
+}
+
+int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_stride, int64_t sequences, int q_heads,
+                          const int32_t *lengths, const int32_t *table, int64_t table_width, int64_t table_stride,
+                          float scale, int64_t window, void *out, float *lse, void *workspace, cudaStream_t stream) {
+  AttendArgs a = {};
+  int st = kv_args(cache, &a.kv);
+  if (st == NVFP4_OK) st = kv_table(&a.kv, table, sequences, table_width, table_stride);
+  if (st != NVFP4_OK) return st;
+  if (sequences > 65535 || q_heads < cache->kv_heads || q_heads > kMaxQHeads || q_heads % cache->kv_heads)
+    return NVFP4_ERR_INVALID_ARG;
+  if (q_stride < int64_t(q_heads) * cache->head_dim || q_stride >= kMaxElems || window < 0 || !(scale - scale == 0.0f))
+    return NVFP4_ERR_INVALID_ARG;
+  if (table_width * cache->page_size > INT32_MAX) return NVFP4_ERR_INVALID_ARG;
+  if (sequences > 0 && (!q || !lengths || !out)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(lse, 4) || !aligned(workspace, 256) ||
+      q_stride % 8 != 0)
+    return NVFP4_ERR_MISALIGNED;
+  DevInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != NVFP4_OK) return st;
+  if (sequences == 0) return NVFP4_OK;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.sequences = (int)sequences;
+  a.q_heads = q_heads;
+  a.lengths = lengths;
+  a.scale = scale;
+  a.window = window;
+  a.out = out;
+  a.lse = lse;
+  void *own = nullptr;
+  cudaError_t e = workspace ? cudaSuccess
+                            : take_workspace(&own, attend_workspace_bytes(a.kv, q_heads, d->sms), *d, stream);
+  if (e == cudaSuccess) {
+    TraceScope tr(kTrAttend, stream);
+    e = launch_attend(a, d->sms, workspace ? workspace : own, stream);
+  }
+  const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);
 }
 

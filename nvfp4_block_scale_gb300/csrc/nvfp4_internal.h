@@ -75,6 +75,66 @@ int max_active_ctas(int which);
 cudaError_t check_take_kernels(uint32_t *site);
 cudaError_t check_take_decoupled(uint32_t *site);
 cudaError_t launch_check_selftest(int64_t i, int64_t n, cudaStream_t st);
+constexpr int kLinearSlice = 256;        // vectors of one product launch at most
+constexpr int kMaxQHeads = 1024;
+constexpr size_t kCounterBytes = 8192;   // zeroed head of a product's or an attention's workspace
+// Launch arguments of the decode-step operators (checked by the C ABI).
+struct LinearArgs {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  const float *alpha;
+  int64_t rows, cols;
+  const void *x;  // bf16
+  int64_t x_stride;
+  int batch;  // 1..256
+  const void *bias;
+  const void *gate;
+  int64_t gate_stride;
+  const void *residual;
+  int64_t residual_stride;
+  int act;
+  void *y;
+  int64_t y_stride;
+};
+struct KvArgs {  // the cache and its page table
+  void *k, *v;
+  int64_t k_page_stride, v_page_stride, pages;
+  int page_shift, kv_heads, head_dim;
+  bool e4m3;
+  const float *k_scale, *v_scale;
+  const int32_t *table;
+  int64_t table_width, table_stride;
+};
+struct AppendArgs {
+  KvArgs kv;
+  const void *qkv;
+  bool fp32;
+  int64_t qkv_stride, tokens;
+  int q_heads;
+  const int32_t *seq, *pos;
+  int64_t sequences;
+  const float *cos_sin;
+  int64_t positions;
+  int rotary;
+  bool interleaved;
+  void *q_out;
+};
+struct AttendArgs {
+  KvArgs kv;
+  const void *q;
+  int64_t q_stride;
+  int sequences, q_heads;
+  const int32_t *lengths;
+  float scale;
+  int64_t window;
+  void *out;
+  float *lse;
+};
+size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
+cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, cudaStream_t st);
+cudaError_t launch_kv_append(const AppendArgs &a, int sms, cudaStream_t st);
+size_t attend_workspace_bytes(const KvArgs &kv, int q_heads, int sms);
+cudaError_t launch_attend(const AttendArgs &a, int sms, void *ws, cudaStream_t st);
 int64_t ffma_probe_fmas_per_thread(int packed, int64_t rounds);
 cudaError_t launch_ffma_probe(int packed, int64_t rounds, int grid, float *sink, cudaStream_t st);
 int ffma_probe_threads();
