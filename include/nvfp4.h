@@ -263,8 +263,8 @@ int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha
  *   k, v        device, 16-byte aligned.  dtype NVFP4_DTYPE_BF16 or
  *               NVFP4_DTYPE_E4M3.
  *   *_page_stride  elements between pages, >= kv_heads * page_size * head_dim,
- *               a multiple of 16 bytes (keys and values may share one
- *               allocation).
+ *               below 2^39, a multiple of 16 bytes (keys and values may share
+ *               one allocation).
  *   page_size   a power of two, 8 .. 65536.  head_dim 64, 128 or 256.
  *               pages and kv_heads * page_size below 2^31.
  *   k_scale, v_scale  E4M3 only: device, [kv_heads] fp32 > 0, the value of one
@@ -341,6 +341,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const void *qkv, int qkv_dtype,
  *   q       device, bf16, 16-byte aligned, [sequences][q_heads][head_dim],
  *           sequences q_stride elements apart (a multiple of 8).
  *   sequences 0 .. 65535.  q_heads a multiple of kv_heads, at most 1024.
+ *           The cache has at least one page and table_width * page_size is at
+ *           most 2^30.
  *   lengths device, [sequences] int32: tokens in the cache, the new one
  *           included; clipped to [0, table_width * page_size].
  *   table   as for nvfp4_kv_append.  Entries behind a sequence's last page are

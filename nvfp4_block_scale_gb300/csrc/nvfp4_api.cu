@@ -109,6 +109,7 @@ int device_info(DevInfo **out) {
       for (int k = 0; k < kKernCount; ++k) d.occ[k] = max_active_ctas(k);
       e = prepare_gemv_kernels();
       if (e == cudaSuccess) e = prepare_gemm_tc_kernels();
+      if (e == cudaSuccess) e = prepare_attention_kernels();
       if (e != cudaSuccess) return map_cuda(e);
       cudaMemPoolProps props = {};
       props.allocType = cudaMemAllocationTypePinned;
@@ -194,8 +195,7 @@ int kv_args(const nvfp4_kv_cache *c, KvArgs *a) {
   if (c->pages < 0 || c->pages > INT32_MAX || (c->pages > 0 && (!c->k || !c->v))) return NVFP4_ERR_INVALID_ARG;
   const int64_t page = int64_t(c->kv_heads) * c->page_size * c->head_dim, unit = e4m3 ? 16 : 8;
   for (const int64_t stride : {c->k_page_stride, c->v_page_stride}) {
-    // the last page's last byte stays inside the 64-bit byte range
-    if (stride < page || stride > INT64_MAX / 4 / std::max<int64_t>(1, c->pages)) return NVFP4_ERR_INVALID_ARG;
+    if (stride < page || stride >= kMaxElems / 2) return NVFP4_ERR_INVALID_ARG;
     if (stride % unit) return NVFP4_ERR_MISALIGNED;
   }
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
@@ -682,8 +682,8 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
     return NVFP4_ERR_INVALID_ARG;
   if (q_stride < int64_t(q_heads) * cache->head_dim || q_stride >= kMaxElems || window < 0 || !(scale - scale == 0.0f))
     return NVFP4_ERR_INVALID_ARG;
-  if (table_width * cache->page_size > INT32_MAX) return NVFP4_ERR_INVALID_ARG;
-  if (sequences > 0 && (!q || !lengths || !out)) return NVFP4_ERR_INVALID_ARG;
+  if (table_width > (int64_t(1) << 30) / cache->page_size) return NVFP4_ERR_INVALID_ARG;
+  if (sequences > 0 && (!q || !lengths || !out || a.kv.pages < 1)) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(lse, 4) || !aligned(workspace, 256) ||
       q_stride % 8 != 0)
     return NVFP4_ERR_MISALIGNED;

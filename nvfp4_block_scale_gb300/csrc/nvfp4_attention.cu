@@ -1,10 +1,45 @@
 // nvfp4_attention.cu -- attention of one new token per sequence over a paged
 // key-value cache.
 //
-// One CTA per query head and sequence; each warp takes every fourth token, a
-// lane head_dim / 32 dimensions, with a running maximum and sum; the warps'
-// parts meet in shared memory.
+//   s_t = scale ks (q . k_t), m = max s_t, l = sum exp(s_t - m),
+//   out = vs / l sum exp(s_t - m) v_t, lse = m + ln l, over the visible tokens.
+//
+// Bound: HBM.  Every visible key and value is read once; the products are
+// 4 flop per element and query head of the group, far below the tensor cores'
+// rate, so the work is to keep enough copies in flight.
+//
+// Work split: an item is one sequence and one block of up to 8 NT query heads
+// that share a cache head.  Its visible tokens are cut into tiles of KT, and the
+// tiles of all items form one sequence; CTA c takes the contiguous range
+// [c T / G, (c + 1) T / G) of it, so ragged lengths balance without the host
+// knowing them.  The part of an item inside a CTA's range is a segment.  Warp w
+// takes every fourth tile of a segment and keeps a running maximum, sum and
+// output of its own (no barrier inside a segment); the four meet in shared
+// memory at the segment's end.  An item inside one CTA is finished there; the
+// parts of a longer one go to the workspace and the CTA that writes the last
+// part (a counter per item) adds them in CTA order, so that results do not
+// depend on timing.  Nothing waits for another CTA.
+//
+// Loads: each warp owns a ring of S tiles that it fills by TMA S tiles ahead,
+// across segments too (keys and values of a page as boxes of 128-byte rows,
+// 128-byte swizzle; pages outside the cache read as zeros).
+//
+// Products: mma.sync with the tokens as the M side, S^T = K Q^T and
+// O^T = V^T P^T: 16 tokens x 8 heads fill an m16n8 tile, so a group of 8 heads
+// wastes nothing, and S^T and O^T keep a head in the same lanes, so the running
+// maximum never moves between lanes.  (tcgen05 would want 64 or 128 rows of
+// tokens per instruction and the softmax through tensor memory; at 4 flop per
+// byte per head the legacy path is not the limit.)  bf16 keys and values enter
+// as they are, with P rounded to bf16.  E4M3 ones are converted exactly to
+// f16; q is scaled by a power of two per head to fit f16 (its entries keep
+// their 8 bits down to 2^-27 of the head's largest), and P, scaled by 2^14,
+// keeps 11 bits.
+#include <algorithm>
+#include <cstring>
+
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "nvfp4_device.cuh"
@@ -13,71 +48,726 @@
 namespace nvfp4 {
 
 constexpr int kAttWarps = 4;
+constexpr int kAttThreads = kAttWarps * 32;
+constexpr int kAttMinTiles = 8;      // tiles per CTA below which fewer CTAs take part
+constexpr int kAttMaxCtas = 1024;    // counters in the workspace's zeroed head
+constexpr int kAttTries = 2000;      // x 1 ms: bound of a wait for a copy
+static_assert(kAttMaxCtas * 4 <= (int)kCounterBytes, "counters");
 
-__device__ __forceinline__ float kv_value(const void *p, int64_t i, bool e4m3) {
-  if (e4m3) return e4m3_value(static_cast<const uint8_t *>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+template <int D, bool E4M3, int NT>
+struct AttCfg {
+  static constexpr int kElem = E4M3 ? 1 : 2;
+  static constexpr int kRow = D * kElem;                       // bytes of a token's key
+  static constexpr int kBoxRow = kRow < 128 ? kRow : 128;      // bytes of a box's row = swizzle span
+  static constexpr int kBoxes = kRow / kBoxRow;
+  static constexpr int KT = kRow <= 128 ? 32 : 16;             // tokens per tile
+  static constexpr int kHalf = KT * kRow;                      // bytes of a tile's keys
+  static constexpr int kTile = 2 * kHalf;
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kRedStride = D + 4;                     // floats; keeps the lanes of a store in distinct banks
+  static constexpr int kRed = kAttWarps * kHeads * kRedStride * 4;
+  static constexpr int kBudget = 113 * 1024 - 2048;            // dynamic shared memory of one of two CTAs per SM
+  static constexpr int S0 = (kBudget - 1024 - kRed) / (kAttWarps * kTile);
+  static constexpr int S = S0 >= 4 ? 4 : S0 >= 2 ? S0 : 2;
+  static constexpr int kRing = kAttWarps * S * kTile;
+  static constexpr size_t kSmem = 1024 + kRing + kRed;
+  static_assert(kSmem <= 225 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t att_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ float att_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAttWarps * 32) k_attend(const __grid_constant__ AttendArgs a) {
-  constexpr int N = D / 32;
-  __shared__ float sm[kAttWarps], sl[kAttWarps], so[kAttWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x, s = blockIdx.y, kh = h / (a.q_heads / a.kv.kv_heads);
-  const int64_t cap = a.kv.table_width << a.kv.page_shift;
-  const int64_t n = max((int64_t)0, min((int64_t)a.lengths[s], cap));
-  const int64_t lo = a.window > 0 && n > a.window ? n - a.window : 0;
-  const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + s * a.q_stride + (int64_t)h * D;
-  float qv[N], o[N], m = -INFINITY, l = 0.0f;
-  const float sc = a.scale * (a.kv.k_scale ? a.kv.k_scale[kh] : 1.0f);
-  for (int i = 0; i < N; ++i) {
-    qv[i] = __bfloat162float(q[lane + 32 * i]);
-    o[i] = 0.0f;
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+// c += a b, 16 x 8 x 16, fp32 accumulators; f16 or bf16 operands.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 bytes -> two f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}" : "=r"(r) : "r"(b));
+  return r;
+}
+
+// {lo, hi} fp32 -> packed 16-bit pair.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+__device__ __forceinline__ bool att_wait(uint32_t mb, uint32_t parity, int tries) {
+  for (int i = 0; i < tries; ++i) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(mb), "r"(parity), "r"(1000000u) : "memory");
+    if (done) return true;
   }
-  for (int64_t t = lo + warp; t < n; t += kAttWarps) {
-    const int64_t page = a.kv.table[s * a.kv.table_stride + (t >> a.kv.page_shift)];
-    const bool in = page >= 0 && page < a.kv.pages;
-    const int64_t row = (((int64_t)kh << a.kv.page_shift) + (t & ((1 << a.kv.page_shift) - 1))) * D + lane;
-    float dot = 0.0f;
-    for (int i = 0; i < N; ++i)
-      dot = fmaf(qv[i], in ? kv_value(a.kv.k, page * a.kv.k_page_stride + row + 32 * i, a.kv.e4m3) : 0.0f, dot);
-    for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
-    dot *= sc;
-    const float m1 = fmaxf(m, dot), base = m1 == -INFINITY ? 0.0f : m1;
-    const float f = expf(m - base), p = expf(dot - base);
-    l = l * f + p;
-    for (int i = 0; i < N; ++i)
-      o[i] = o[i] * f + p * (in ? kv_value(a.kv.v, page * a.kv.v_page_stride + row + 32 * i, a.kv.e4m3) : 0.0f);
-    m = m1;
+  return false;
+}
+
+// What the kernel needs beside the caller's arguments.
+struct AttLaunch {
+  AttendArgs a;
+  uint32_t *count;   // [kAttMaxCtas], zero between calls
+  float *part;       // [2 G][heads][D] sums, then [2 G][heads][2] maxima and sums
+  int blocks;        // head blocks per cache head
+  int piece_shift;   // log2 of the rows of a box: min(page, KT)
+};
+
+// A position in a CTA's range: a segment (tiles [first, first + count) of
+// sequence b, head block hg) and the tiles left behind it.
+struct AttSeg {
+  int b, hg;
+  int first, count;  // tiles, numbered from token 0
+  int off, total;    // the segment's place among the item's tiles, and their number
+  int64_t left;      // tiles of the range behind this segment
+  int n, lo;         // visible tokens [lo, n)
+};
+
+template <int KT>
+__device__ __forceinline__ void att_visible(const AttendArgs &a, int b, int &n, int &lo) {
+  const int64_t cap = a.kv.table_width << a.kv.page_shift;  // at most 2^30
+  n = (int)max((int64_t)0, min((int64_t)__ldg(a.lengths + b), cap));
+  lo = a.window > 0 && n > a.window ? n - (int)a.window : 0;
+}
+template <int KT>
+__device__ __forceinline__ int att_tiles(int n, int lo) { return n > 0 ? (n - 1) / KT - lo / KT + 1 : 0; }
+
+// The segment at tile `off` of item (b, hg), at most `left` tiles long.
+template <int KT>
+__device__ __forceinline__ void att_segment(const AttendArgs &a, AttSeg &s, int off, int64_t left) {
+  att_visible<KT>(a, s.b, s.n, s.lo);
+  s.total = att_tiles<KT>(s.n, s.lo);
+  s.off = off;
+  s.first = s.lo / KT + off;
+  s.count = (int)min((int64_t)(s.total - off), left);
+  s.left = left - s.count;
+}
+// Moves to the next segment; s.left > 0.
+template <int KT>
+__device__ __forceinline__ void att_next(const AttendArgs &a, AttSeg &s, int groups) {
+  if (++s.hg == groups) {
+    s.hg = 0;
+    int n, lo;
+    do {  // (a later sequence holds the tiles that are left)
+      ++s.b;
+      att_visible<KT>(a, s.b, n, lo);
+    } while (n == 0);
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  for (int i = 0; i < N; ++i) so[warp][lane + 32 * i] = o[i];
+  att_segment<KT>(a, s, 0, s.left);
+}
+
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ CUtensorMap kmap,
+                                                        const __grid_constant__ CUtensorMap vmap,
+                                                        const __grid_constant__ AttLaunch p) {
+  using C = AttCfg<D, E4M3, NT>;
+  constexpr int KT = C::KT, S = C::S, SUB = KT / 16, KS = D / 16;
+  extern __shared__ uint8_t dsm[];
+  __shared__ __align__(8) uint64_t full[kAttWarps][S];
+  __shared__ int64_t s_sum[kAttWarps];
+  __shared__ int s_start[3];
+  __shared__ float s_ml[kAttWarps][C::kHeads][2];
+  __shared__ int s_last;
+  const AttendArgs &a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.q_heads / a.kv.kv_heads, groups = a.kv.kv_heads * p.blocks;
+  const uint32_t raw = att_smem(dsm), base = (raw + 1023u) & ~1023u;
+  float *red = reinterpret_cast<float *>(dsm + (base - raw) + C::kRing);  // [warps][heads][kRedStride]
+  const uint32_t ring = base + warp * S * C::kTile;
+  const uint32_t bars = att_smem(&full[warp][0]);
+
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * s) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+
+  // ---- the tiles before each sequence; this CTA's range
+  const int per = (a.sequences + kAttThreads - 1) / kAttThreads;
+  const int sb0 = min(tid * per, a.sequences), sb1 = min(sb0 + per, a.sequences);
+  int64_t mine = 0;
+  for (int b = sb0; b < sb1; ++b) {
+    int n, lo;
+    att_visible<KT>(a, b, n, lo);
+    mine += att_tiles<KT>(n, lo);
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, sm[w]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  for (int w = 0; w < kAttWarps; ++w) sum += sl[w] * expf(sm[w] - base);
-  const int64_t at = (int64_t)s * a.q_heads + h;
-  for (int d = threadIdx.x; d < D; d += kAttWarps * 32) {
-    float v = 0.0f;
-    for (int w = 0; w < kAttWarps; ++w) v += so[w][d] * expf(sm[w] - base);
-    v = sum == 0.0f ? 0.0f : v * (a.kv.v_scale ? a.kv.v_scale[kh] : 1.0f) / sum;
-    static_cast<__nv_bfloat16 *>(a.out)[at * D + d] = __float2bfloat16(v);
+  int64_t T = 0;
+#pragma unroll
+  for (int w = 0; w < kAttWarps; ++w) {
+    if (w < warp) incl += s_sum[w];
+    T += s_sum[w];
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[at] = base + logf(sum);
+  T *= groups;
+  const int64_t G = min((int64_t)gridDim.x, max((int64_t)1, (T + kAttMinTiles - 1) / kAttMinTiles));
+  const int64_t c = blockIdx.x;
+  const int64_t g0 = c < G ? c * T / G : T, g1 = c < G ? (c + 1) * T / G : T;
+  if (g0 < g1 && (incl - mine) * groups <= g0 && g0 < incl * groups) {  // one thread
+    int64_t rem = g0 - (incl - mine) * groups;
+    int b = sb0;
+    for (;; ++b) {
+      int n, lo;
+      att_visible<KT>(a, b, n, lo);
+      const int64_t nt = att_tiles<KT>(n, lo), all = nt * groups;
+      if (rem < all) {
+        s_start[0] = b;
+        s_start[1] = (int)(rem / nt);
+        s_start[2] = (int)(rem % nt);
+        break;
+      }
+      rem -= all;
+    }
+  }
+  // rows of empty sequences
+  for (int b = blockIdx.x; b < a.sequences; b += gridDim.x) {
+    int n, lo;
+    att_visible<KT>(a, b, n, lo);
+    if (n > 0) continue;
+    uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (int64_t)b * a.q_heads * D);
+    for (int i = tid; i < a.q_heads * D / 8; i += kAttThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse)
+      for (int i = tid; i < a.q_heads; i += kAttThreads) a.lse[(int64_t)b * a.q_heads + i] = -INFINITY;
+  }
+  __syncthreads();
+  if (g0 >= g1) return;
+
+  AttSeg seg;
+  seg.b = s_start[0];
+  seg.hg = s_start[1];
+  att_segment<KT>(a, seg, s_start[2], g1 - g0);
+
+  // ---- the ring: `ahead` is the segment of the next tile to request, `at` that tile
+  const int piece = 1 << p.piece_shift, pp = KT >> p.piece_shift;  // pieces (pages) per tile: 1, 2 or 4
+  const int page_mask = (1 << a.kv.page_shift) - 1;
+  AttSeg ahead = seg;
+  int at = ahead.first + warp, ids_base = 0, ids = -1;  // this lane's page number, for tiles from ids_base on
+  bool more = true, fresh = true;
+  int issued = 0;
+  auto request = [&]() {  // the warp's next tile into stage issued % S
+    while (at >= ahead.first + ahead.count) {
+      if (ahead.left == 0) {
+        more = false;
+        return;
+      }
+      att_next<KT>(a, ahead, groups);
+      at = ahead.first + warp;
+      fresh = true;
+    }
+    if (fresh || at >= ids_base + kAttWarps * (32 / pp)) {  // page numbers of the next 32 / pp tiles, a lane each
+      ids_base = at;
+      const int tok = (at + kAttWarps * (lane / pp)) * KT + (lane % pp) * piece;
+      ids = tok < ahead.n ? __ldg(a.kv.table + ahead.b * a.kv.table_stride + (tok >> a.kv.page_shift)) : -1;
+      fresh = false;
+    }
+    const int t0 = at * KT, slot = (at - ids_base) / kAttWarps * pp;
+    const int pieces = min(pp, (ahead.n - t0 + piece - 1) >> p.piece_shift);
+    const uint32_t mb = bars + 8 * (issued % S), dst = ring + (issued % S) * C::kTile;
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                   ::"r"(mb), "r"(2 * pieces * piece * C::kRow) : "memory");
+    // lane: piece, then box, then keys or values
+    const int my_piece = lane % pp, my_box = lane / pp % C::kBoxes, kind = lane / pp / C::kBoxes;
+    const int page = __shfl_sync(0xFFFFFFFFu, ids, slot + my_piece);
+    if (kind < 2 && my_piece < pieces) {
+      const int kh = ahead.hg / p.blocks;
+      const int y = (kh << a.kv.page_shift) + ((t0 + my_piece * piece) & page_mask);
+      const uint32_t to = dst + kind * C::kHalf + my_box * (KT * C::kBoxRow) + my_piece * piece * C::kBoxRow;
+      asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                   " [%0], [%1, {%2, %3, %4}], [%5];"
+                   ::"r"(to), "l"(kind ? &vmap : &kmap), "r"(my_box * (C::kBoxRow / C::kElem)), "r"(y), "r"(page), "r"(mb)
+                   : "memory");
+    }
+    ++issued;
+    at += kAttWarps;
+  };
+  for (int s = 0; s < S && more; ++s) request();
+
+  int done = 0;      // tiles consumed
+  bool bad = false;  // a copy did not arrive
+  // ldmatrix rows and chunks of this lane
+  const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchk = lane >> 4;
+  const int vrow = E4M3 ? krow : (lane & 7) + ((lane >> 4) & 1) * 8, vchk = E4M3 ? kchk : (lane >> 3) & 1;
+  auto chunk_at = [&](int row, int ch) {  // byte offset of 16-byte chunk ch of a row of a tile's half
+    constexpr int kPer = C::kBoxRow / 16;
+    const int sw = C::kBoxRow == 128 ? row & 7 : (row >> 1) & 3;
+    return (uint32_t)((ch / kPer) * (KT * C::kBoxRow) + row * C::kBoxRow + (((ch % kPer) ^ sw) << 4));
+  };
+
+  for (;;) {
+    const int kh = seg.hg / p.blocks, h0 = kh * group + (seg.hg % p.blocks) * C::kHeads;
+    const int heads = min(C::kHeads, (kh + 1) * group - h0);
+    const float sc = a.scale * (E4M3 && a.kv.k_scale ? __ldg(a.kv.k_scale + kh) : 1.0f) * 1.4426950408889634f;
+
+    // ---- q as the B side: this lane's head is 8 nt + lane / 4
+    uint32_t qf[NT][KS][2];
+    float qs[NT][2];  // factor of the scores of heads 8 nt + 2 (lane % 4) + j
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = 8 * nt + (lane >> 2);
+      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + seg.b * a.q_stride + (int64_t)(h0 + h) * D;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (E4M3) {  // dimensions 4c .. 4c + 3 of the step: the order in which ldmatrix hands out bytes
+          const uint2 v = h < heads ? __ldg(reinterpret_cast<const uint2 *>(q + 16 * ks) + (lane & 3)) : make_uint2(0u, 0u);
+          qf[nt][ks][0] = v.x;
+          qf[nt][ks][1] = v.y;
+        } else {
+          qf[nt][ks][0] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks) + (lane & 3)) : 0u;
+          qf[nt][ks][1] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks + 8) + (lane & 3)) : 0u;
+        }
+      }
+      qs[nt][0] = qs[nt][1] = sc;
+      if (E4M3) {
+        uint32_t top = 0u;  // bf16 bits of the head's largest |q|
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w = qf[nt][ks][j] & 0x7FFF7FFFu;
+            top = max(top, max(w & 0xFFFFu, w >> 16));
+          }
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // 2^-up takes the largest into [2^13, 2^14); zero, inf and NaN heads stay as they are
+        const int e = (int)(top >> 7), up = e == 0 || e == 255 ? 0 : e - 127 - 13;
+        const float f1 = __uint_as_float((uint32_t)(127 - up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 - (up - up / 2)) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w = qf[nt][ks][j];
+            qf[nt][ks][j] = pack16<true>(__uint_as_float(w << 16) * f1 * f2, __uint_as_float(w & 0xFFFF0000u) * f1 * f2);
+          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int u = __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * (lane & 3) + j));
+          qs[nt][j] = sc * __uint_as_float((uint32_t)(127 + u / 2) << 23) * __uint_as_float((uint32_t)(127 + u - u / 2) << 23);
+        }
+      }
+    }
+
+    float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < KS; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][d][j] = 0.0f;
+    }
+
+    for (int t = seg.first + warp; t < seg.first + seg.count; t += kAttWarps) {
+      const int st = done % S;
+      if (!bad) bad = !__all_sync(0xFFFFFFFFu, att_wait(bars + 8 * st, (uint32_t)(done / S) & 1u, kAttTries));
+      const uint32_t kb = ring + st * C::kTile, vb = kb + C::kHalf;
+      const int t0 = t * KT;
+      const bool edge = t0 < seg.lo || t0 + KT > seg.n;
+      if (edge) {
+        // values outside [lo, n) become zeros: their weights are zero, but what is stored there need not be finite
+        for (int i = lane; i < KT * (C::kRow / 16); i += 32) {
+          const int row = i / (C::kRow / 16);
+          if (t0 + row < seg.lo || t0 + row >= seg.n)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + chunk_at(row, i % (C::kRow / 16))), "r"(0)
+                         : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy into this stage
+        __syncwarp();
+      }
+
+      // ---- S^T: 16 SUB tokens x 8 NT heads
+      float s[SUB][NT][4];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[u][nt][j] = 0.0f;
+      if (E4M3) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2)
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            uint32_t r[4];
+            ldsm4<false>(kb + chunk_at(16 * u + krow, ks + kchk), r);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t f[4] = {e4m3x2_f16x2(r[2 * x]), e4m3x2_f16x2(r[2 * x + 1]), e4m3x2_f16x2_hi(r[2 * x]),
+                                     e4m3x2_f16x2_hi(r[2 * x + 1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[u][nt], f, qf[nt][ks + x][0], qf[nt][ks + x][1]);
+            }
+          }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            uint32_t r[4];
+            ldsm4<false>(kb + chunk_at(16 * u + krow, 2 * ks + kchk), r);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[u][nt], r, qf[nt][ks][0], qf[nt][ks][1]);
+          }
+      }
+
+      // ---- running maximum and sum: this lane's tokens lane / 4 (+ 8), heads 2 (lane % 4) + {0, 1}
+      bool grew = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float &v = s[u][nt][2 * r + j];
+              v *= qs[nt][j];
+              if (edge) {
+                const int tok = t0 + 16 * u + 8 * r + (lane >> 2);
+                if (tok < seg.lo || tok >= seg.n) v = -INFINITY;
+              }
+              x = fmaxf(x, v);
+            }
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
+          top[nt][j] = fmaxf(m[nt][j], x);
+          grew |= top[nt][j] > m[nt][j];
+        }
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float f = top[nt][j] == m[nt][j] ? 1.0f : att_exp2(m[nt][j] - top[nt][j]);
+            m[nt][j] = top[nt][j];
+            l[nt][j] *= f;
+#pragma unroll
+            for (int d = 0; d < KS; ++d) {
+              o[nt][d][j] *= f;
+              o[nt][d][2 + j] *= f;
+            }
+          }
+      }
+      uint32_t pf[SUB][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float ref[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ref[j] = m[nt][j] == -INFINITY ? 0.0f : E4M3 ? m[nt][j] - 14.0f : m[nt][j];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float x = att_exp2(s[u][nt][2 * r] - ref[0]), y = att_exp2(s[u][nt][2 * r + 1] - ref[1]);
+            l[nt][0] += x;
+            l[nt][1] += y;
+            pf[u][nt][r] = transpose8x8(pack16<E4M3>(x, y));
+          }
+      }
+
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        if (E4M3) {
+#pragma unroll
+          for (int d = 0; d < KS; d += 2) {
+            uint32_t r[4];
+            ldsm4<true>(vb + chunk_at(16 * u + vrow, d + vchk), r);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t w0 = __byte_perm(r[2 * x], 0u, 0x3120), w1 = __byte_perm(r[2 * x + 1], 0u, 0x3120);
+              const uint32_t f[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2_hi(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2_hi(w1)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[nt][d + x], f, pf[u][nt][0], pf[u][nt][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < KS; ++d) {
+            uint32_t r[4];
+            ldsm4<true>(vb + chunk_at(16 * u + vrow, 2 * d + vchk), r);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][d], r, pf[u][nt][0], pf[u][nt][1]);
+          }
+        }
+      }
+      ++done;
+      __syncwarp();  // every lane has read the stage
+      if (more && !bad) request();
+    }
+
+    // ---- the four warps' parts meet
+    const int parts = min(kAttWarps, seg.count);
+    if (warp < parts) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = l[nt][j];
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, w);
+          const int h = 8 * nt + 2 * (lane & 3) + j;
+          if (lane < 4) {
+            s_ml[warp][h][0] = m[nt][j];
+            s_ml[warp][h][1] = bad ? __int_as_float(0x7FC00000) : x;
+          }
+          float *to = red + (warp * C::kHeads + h) * C::kRedStride;
+#pragma unroll
+          for (int d = 0; d < KS; ++d) {
+            // rows g and g + 8 of a 16-row tile: dimensions g, g + 8, or 2 g, 2 g + 1 (E4M3)
+            const int d0 = 16 * d + (E4M3 ? 2 : 1) * (lane >> 2);
+            to[d0] = o[nt][d][j];
+            to[d0 + (E4M3 ? 1 : 8)] = o[nt][d][2 + j];
+          }
+        }
+    }
+    __syncthreads();
+    const bool whole = seg.count == seg.total;
+    const int64_t item0 = g1 - seg.left - seg.count - seg.off;  // the item's first tile
+    // parts of an item: the first in its CTA's slot 2c + 1, the others in their CTAs' slots 2c
+    const int64_t slot = 2 * c + (seg.off == 0 ? 1 : 0);
+    const float vs = E4M3 && a.kv.v_scale ? __ldg(a.kv.v_scale + kh) : 1.0f;
+    float *ml_all = p.part + (int64_t)2 * gridDim.x * C::kHeads * D;
+    for (int i = tid; i < heads * (D / 8); i += kAttThreads) {
+      const int h = i / (D / 8), d = i % (D / 8) * 8;
+      float mx = s_ml[0][h][0], sum = 0.0f, v[8] = {};
+      for (int w = 1; w < parts; ++w) mx = fmaxf(mx, s_ml[w][h][0]);
+      const float ref = mx == -INFINITY ? 0.0f : mx;
+      for (int w = 0; w < parts; ++w) {
+        const float f = att_exp2(s_ml[w][h][0] - ref);
+        sum += s_ml[w][h][1] * f;
+        const float4 *x = reinterpret_cast<const float4 *>(red + (w * C::kHeads + h) * C::kRedStride + d);
+        const float4 x0 = x[0], x1 = x[1];
+        v[0] = fmaf(x0.x, f, v[0]), v[1] = fmaf(x0.y, f, v[1]), v[2] = fmaf(x0.z, f, v[2]), v[3] = fmaf(x0.w, f, v[3]);
+        v[4] = fmaf(x1.x, f, v[4]), v[5] = fmaf(x1.y, f, v[5]), v[6] = fmaf(x1.z, f, v[6]), v[7] = fmaf(x1.w, f, v[7]);
+      }
+      if (whole) {
+        const float r = sum == 0.0f ? 0.0f : vs / sum;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack16<false>(v[2 * j] * r, v[2 * j + 1] * r);
+        const int64_t row = (int64_t)seg.b * a.q_heads + h0 + h;
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (d == 0 && a.lse) a.lse[row] = (ref - (E4M3 ? 14.0f : 0.0f) + log2f(sum)) * 0.69314718055994531f;
+      } else {
+        float4 *to = reinterpret_cast<float4 *>(p.part + (slot * C::kHeads + h) * D + d);
+        __stcg(to, make_float4(v[0], v[1], v[2], v[3]));
+        __stcg(to + 1, make_float4(v[4], v[5], v[6], v[7]));
+        if (d == 0) __stcg(reinterpret_cast<float2 *>(ml_all) + slot * C::kHeads + h, make_float2(mx, sum));
+      }
+    }
+    if (!whole) {
+      // ---- the parts of an item that several CTAs share
+      const int64_t c0 = ((item0 + 1) * G - 1) / T, c1 = ((item0 + seg.total) * G - 1) / T;
+      const int n = (int)(c1 - c0) + 1;
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        const uint32_t before = atomicAdd(p.count + c0, 1u);
+        s_last = before == (uint32_t)(n - 1);
+        if (s_last) p.count[c0] = 0u;  // as the next call wants it
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        const float2 *ml = reinterpret_cast<const float2 *>(ml_all);
+        auto slot_of = [&](int j) { return 2 * (c0 + j) + (j == 0 ? 1 : 0); };
+        for (int i = tid; i < heads * (D / 4); i += kAttThreads) {
+          const int h = i / (D / 4), d = i % (D / 4) * 4;
+          float mx = -INFINITY, sum = 0.0f;
+          for (int j = 0; j < n; ++j) mx = fmaxf(mx, __ldcg(&ml[slot_of(j) * C::kHeads + h]).x);
+          const float ref = mx == -INFINITY ? 0.0f : mx;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+          for (int j = 0; j < n; ++j) {
+            const float2 e = __ldcg(&ml[slot_of(j) * C::kHeads + h]);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(j) * C::kHeads + h) * D + d));
+            const float f = att_exp2(e.x - ref);
+            sum = fmaf(e.y, f, sum);
+            v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
+          }
+          const float r = sum == 0.0f ? 0.0f : vs / sum;
+          const int64_t row = (int64_t)seg.b * a.q_heads + h0 + h;
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) =
+              make_uint2(pack16<false>(v.x * r, v.y * r), pack16<false>(v.z * r, v.w * r));
+          if (d == 0 && a.lse) a.lse[row] = (ref - (E4M3 ? 14.0f : 0.0f) + log2f(sum)) * 0.69314718055994531f;
+        }
+      }
+    }
+    if (seg.left == 0) break;
+    att_next<KT>(a, seg, groups);
+    __syncthreads();  // red and s_ml are free again
+  }
+  // copies requested but not waited for (after a failure only): let them land
+  if (bad)
+    for (int i = done; i < issued; ++i) att_wait(bars + 8 * (i % S), (uint32_t)(i / S) & 1u, kAttTries);
 }
 
-size_t attend_workspace_bytes(const KvArgs &, int, int) { return kCounterBytes; }
+namespace {
 
-cudaError_t launch_attend(const AttendArgs &a, int, void *, cudaStream_t st) {
-  const dim3 grid((unsigned)a.q_heads, (unsigned)a.sequences);
-  switch (a.kv.head_dim) {
-    case 64: k_attend<64><<<grid, kAttWarps * 32, 0, st>>>(a); break;
-    case 128: k_attend<128><<<grid, kAttWarps * 32, 0, st>>>(a); break;
-    default: k_attend<256><<<grid, kAttWarps * 32, 0, st>>>(a); break;
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn g_att_encode = nullptr;
+
+// NT of a launch: the smallest block of 8 NT heads that holds the group; larger
+// groups take the largest block that the registers hold and read the cache
+// once per block.
+int att_nt(int head_dim, int group) {
+  const int most = head_dim == 256 ? 2 : 4;
+  return group <= 8 ? 1 : group <= 16 || most == 2 ? 2 : 4;
+}
+
+template <int D, bool E4M3, int NT>
+int att_ctas_per_sm() {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_attend<D, E4M3, NT>, kAttThreads,
+                                                    AttCfg<D, E4M3, NT>::kSmem) != cudaSuccess || n < 1)
+    n = 1;
+  return n;
+}
+
+// Calls f<D, E4M3, NT>() for the runtime values.
+template <typename F>
+auto att_dispatch(int head_dim, bool e4m3, int nt, F &&f) {
+#define NVFP4_ATT(D, N) (e4m3 ? f.template operator()<D, true, N>() : f.template operator()<D, false, N>())
+  if (head_dim == 64) return nt == 1 ? NVFP4_ATT(64, 1) : nt == 2 ? NVFP4_ATT(64, 2) : NVFP4_ATT(64, 4);
+  if (head_dim == 128) return nt == 1 ? NVFP4_ATT(128, 1) : nt == 2 ? NVFP4_ATT(128, 2) : NVFP4_ATT(128, 4);
+  return nt == 1 ? NVFP4_ATT(256, 1) : NVFP4_ATT(256, 2);
+#undef NVFP4_ATT
+}
+
+struct AttGrid {
+  int sms;
+  template <int D, bool E4M3, int NT>
+  int operator()() const {
+    static const int per_sm = att_ctas_per_sm<D, E4M3, NT>();
+    return std::min(kAttMaxCtas, sms * per_sm);
   }
-  return cudaGetLastError();
+};
+
+struct AttPrepare {
+  template <int D, bool E4M3, int NT>
+  cudaError_t operator()() const {
+    return cudaFuncSetAttribute(k_attend<D, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)AttCfg<D, E4M3, NT>::kSmem);
+  }
+};
+
+struct AttRun {
+  const AttendArgs &a;
+  int grid_max, nt;
+  void *ws;
+  cudaStream_t st;
+  template <int D, bool E4M3, int NT>
+  cudaError_t operator()() const {
+    using C = AttCfg<D, E4M3, NT>;
+    AttLaunch p;
+    p.a = a;
+    const int group = a.q_heads / a.kv.kv_heads, page = 1 << a.kv.page_shift, piece = std::min(page, C::KT);
+    p.blocks = (group + C::kHeads - 1) / C::kHeads;
+    p.piece_shift = 0;
+    while ((1 << p.piece_shift) < piece) ++p.piece_shift;
+    // the tiles that the longest possible lengths have bound the grid
+    const int64_t cap = a.kv.table_width << a.kv.page_shift;
+    const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, a.window + C::KT) : cap;
+    const int64_t tiles = (seen / C::KT + 1) * a.sequences * a.kv.kv_heads * p.blocks;
+    const int grid = (int)std::min<int64_t>(grid_max, (tiles + kAttMinTiles - 1) / kAttMinTiles);
+    p.count = static_cast<uint32_t *>(ws);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
+    CUtensorMap m[2];
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.kv.kv_heads << a.kv.page_shift, (cuuint64_t)a.kv.pages};
+    const cuuint32_t box[3] = {(cuuint32_t)(C::kBoxRow / C::kElem), (cuuint32_t)piece, 1u}, es[3] = {1u, 1u, 1u};
+    for (int i = 0; i < 2; ++i) {
+      const cuuint64_t strides[2] = {(cuuint64_t)C::kRow,
+                                     (cuuint64_t)(i ? a.kv.v_page_stride : a.kv.k_page_stride) * C::kElem};
+      if (g_att_encode(&m[i], E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                       i ? a.kv.v : a.kv.k, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       C::kBoxRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    }
+    k_attend<D, E4M3, NT><<<grid, kAttThreads, C::kSmem, st>>>(m[0], m[1], p);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+
+size_t attend_workspace_bytes(const KvArgs &kv, int q_heads, int sms) {
+  const int nt = att_nt(kv.head_dim, q_heads / kv.kv_heads);
+  const size_t grid = (size_t)att_dispatch(kv.head_dim, kv.e4m3, nt, AttGrid{sms});
+  return kCounterBytes + 2 * grid * 8 * nt * (kv.head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_attend(const AttendArgs &a, int sms, void *ws, cudaStream_t st) {
+  if (!g_att_encode) return cudaErrorInitializationError;
+  const int nt = att_nt(a.kv.head_dim, a.q_heads / a.kv.kv_heads);
+  const int grid = att_dispatch(a.kv.head_dim, a.kv.e4m3, nt, AttGrid{sms});
+  return att_dispatch(a.kv.head_dim, a.kv.e4m3, nt, AttRun{a, grid, nt, ws, st});
+}
+
+cudaError_t prepare_attention_kernels() {
+  void *fn = nullptr;
+  cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess) return e;
+  if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorSymbolNotFound;
+  g_att_encode = reinterpret_cast<EncodeTiledFn>(fn);
+  for (const int dim : {64, 128, 256})
+    for (const bool e4m3 : {false, true})
+      for (const int nt : {1, 2, 4})
+        if (e == cudaSuccess && !(dim == 256 && nt == 4)) e = att_dispatch(dim, e4m3, nt, AttPrepare{});
+  return e;
 }
 
 }  // namespace nvfp4

@@ -134,6 +134,7 @@ size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
 cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, cudaStream_t st);
 cudaError_t launch_kv_append(const AppendArgs &a, int sms, cudaStream_t st);
 size_t attend_workspace_bytes(const KvArgs &kv, int q_heads, int sms);
+cudaError_t prepare_attention_kernels();
 cudaError_t launch_attend(const AttendArgs &a, int sms, void *ws, cudaStream_t st);
 int64_t ffma_probe_fmas_per_thread(int packed, int64_t rounds);
 cudaError_t launch_ffma_probe(int packed, int64_t rounds, int grid, float *sink, cudaStream_t st);
