@@ -554,7 +554,7 @@ int nvfp4_gemm(const uint8_t *codes, const uint8_t *scales, const float *alpha, 
   {
     TraceScope tr(kTrGemmTc, stream);
     const long fw = g_first_wait.load();
-    e = launch_gemm_tc(codes, scales, alpha, rows, cols, x, batch, d->sms, part, y,
+    e = launch_gemm_tc(codes, scales, alpha, rows, cols, x, cols, batch, d->sms, part,
                        fw < 0 ? -1 : (int)std::min<long>(fw, INT32_MAX), stream);
   }
   if (e == cudaSuccess) {

@@ -44,6 +44,7 @@
 #include <cuda_runtime.h>
 
 #include "nvfp4_device.cuh"
+#include "nvfp4_epilogue.cuh"
 #include "nvfp4_internal.h"
 
 namespace nvfp4 {
@@ -194,7 +195,7 @@ __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 struct TcArgs {
   const uint8_t *codes;
   const uint8_t *scales;
-  const float *alpha;
+  const float *alpha;  // or nullptr: weights without it
   int64_t rows, cols;
   int batch;
   int64_t K;      // steps per tile
@@ -233,7 +234,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_gemm_tc(const __grid_constant
   const int nseg = (int)((g1 - 1) / a.K - t_first + 1);
   volatile int *vfail = &fail;
 
-  if (tid < 256) s_tab[tid] = __fmul_rn(*a.alpha, e4m3_value(tid));
+  // weights as nvfp4_dequantize writes them, or (no alpha) the exact q * Delta of nvfp4_linear
+  if (tid < 256) s_tab[tid] = a.alpha ? __fmul_rn(*a.alpha, e4m3_value(tid)) : e4m3_value(tid);
   if (tid == 0) fail = 0;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&tmem_slot)),
@@ -586,6 +588,30 @@ __global__ void __launch_bounds__(256) k_gemm_tc_reduce(const float *__restrict_
   }
 }
 
+// nvfp4_linear's reduction: the same sums, each finished by the epilogue.
+__global__ void __launch_bounds__(256) k_linear_reduce(const float *__restrict__ ws, const __grid_constant__ LinearArgs a,
+                                                       int64_t K, int64_t T, int64_t G, int maxc) {
+  const int64_t tiles = (a.rows + kTcM - 1) / kTcM;
+  const int64_t n = (int64_t)a.batch * tiles * (kTcM / 4);  // groups of 4 rows
+  const int64_t s4 = (int64_t)a.batch * kTcM / 4;
+  const float alpha = *a.alpha;
+  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n; g += (int64_t)gridDim.x * 256) {
+    const int64_t rg = g % (tiles * (kTcM / 4)), b = g / (tiles * (kTcM / 4));
+    const int64_t t = rg / (kTcM / 4), r0 = t * kTcM + (rg % (kTcM / 4)) * 4;
+    if (r0 >= a.rows) continue;
+    const int cnt = (int)(tc_cta_of((t + 1) * K - 1, T, G) - tc_cta_of(t * K, T, G)) + 1;
+    const float4 *p = reinterpret_cast<const float4 *>(ws + ((t * maxc) * a.batch + b) * kTcM + (r0 - t * kTcM));
+    float4 acc = p[0];
+#pragma unroll 4
+    for (int j = 1; j < cnt; ++j) {
+      const float4 v = p[j * s4];
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    const float w[4] = {acc.x, acc.y, acc.z, acc.w};
+    for (int u = 0; u < 4 && r0 + u < a.rows; ++u) finish(a, alpha, (int)b, r0 + u, w[u]);
+  }
+}
+
 namespace {
 
 // cuTensorMapEncodeTiled, reached through the runtime's driver entry point
@@ -641,8 +667,8 @@ size_t gemm_tc_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms) {
 }
 
 cudaError_t launch_gemm_tc(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows,
-                           int64_t cols, const void *x, int batch, int sms, float *ws, float *y, int first_tries,
-                           cudaStream_t st) {
+                           int64_t cols, const void *x, int64_t x_stride, int batch, int sms, float *ws,
+                           int first_tries, cudaStream_t st) {
   if (!g_encode) return cudaErrorInitializationError;
   const TcPlan p = tc_plan(rows, cols, sms);
   const int n = gemm_tc_tile_n(batch);
@@ -650,7 +676,7 @@ cudaError_t launch_gemm_tc(const uint8_t *codes, const uint8_t *scales, const fl
   // and columns past the end read as zeros), 128-byte swizzle
   CUtensorMap m;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)batch};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint64_t strides[1] = {(cuuint64_t)x_stride * 2};
   const cuuint32_t box[2] = {64u, (cuuint32_t)n};
   const cuuint32_t es[2] = {1u, 1u};
   if (g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(x), dims, strides, box, es,
@@ -683,6 +709,13 @@ cudaError_t launch_gemm_tc_reduce(const float *ws, int64_t rows, int64_t cols, i
                                   int grid, cudaStream_t st) {
   const TcPlan p = tc_plan(rows, cols, sms);
   k_gemm_tc_reduce<<<grid, 256, 0, st>>>(ws, rows, batch, p.K, p.T, p.G, p.maxc, y);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_reduce(const float *ws, const LinearArgs &a, int sms, cudaStream_t st) {
+  const TcPlan p = tc_plan(a.rows, a.cols, sms);
+  const int64_t n = (int64_t)a.batch * p.tiles * (kTcM / 4);
+  k_linear_reduce<<<(int)std::min<int64_t>((n + 255) / 256, 8 * sms), 256, 0, st>>>(ws, a, p.K, p.T, p.G, p.maxc);
   return cudaGetLastError();
 }
 

@@ -48,9 +48,17 @@ __global__ void __launch_bounds__(kLinWarps * 32) k_linear(const __grid_constant
   }
 }
 
-size_t linear_workspace_bytes(int64_t, int64_t, int, int) { return 0; }
+size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms) {
+  return kCounterBytes + (batch > 16 ? gemm_tc_workspace_bytes(rows, cols, batch, sms) : 0);
+}
 
-cudaError_t launch_linear(const LinearArgs &a, int, void *, cudaStream_t st) {
+cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, cudaStream_t st) {
+  if (a.cols > 0 && a.batch > 16) {
+    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
+    const cudaError_t e = launch_gemm_tc(a.codes, a.scales, nullptr, a.rows, a.cols, a.x, a.x_stride, a.batch, sms, part,
+                                         -1, st);
+    return e != cudaSuccess ? e : launch_linear_reduce(part, a, sms, st);
+  }
   const int64_t gx = (a.rows + kLinWarps - 1) / kLinWarps;
   if (gx > INT32_MAX) return cudaErrorInvalidValue;
   k_linear<<<dim3((unsigned)gx, (unsigned)((a.batch + kLinVecs - 1) / kLinVecs)), kLinWarps * 32, 0, st>>>(a);
