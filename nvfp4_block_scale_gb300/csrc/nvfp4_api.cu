@@ -77,6 +77,12 @@ cudaError_t pool_alloc(void **p, size_t bytes, cudaMemPool_t pool, cudaStream_t 
   return cudaMallocFromPoolAsync(p, bytes, pool, stream);
 }
 
+// The hook's limit as the tensor-core kernels take it.
+int first_tries() {
+  const long fw = g_first_wait.load();
+  return fw < 0 ? -1 : (int)std::min<long>(fw, INT32_MAX);
+}
+
 int map_cuda(cudaError_t e) {
   if (e == cudaSuccess) return NVFP4_OK;
   if (e == cudaErrorMemoryAllocation) return NVFP4_ERR_OUT_OF_MEMORY;
@@ -109,6 +115,8 @@ int device_info(DevInfo **out) {
       for (int k = 0; k < kKernCount; ++k) d.occ[k] = max_active_ctas(k);
       e = prepare_gemv_kernels();
       if (e == cudaSuccess) e = prepare_gemm_tc_kernels();
+      if (e == cudaSuccess) e = prepare_linear_kernels();
+      if (e == cudaSuccess) e = prepare_linear_tc_kernels();
       if (e == cudaSuccess) e = prepare_attention_kernels();
       if (e != cudaSuccess) return map_cuda(e);
       cudaMemPoolProps props = {};
@@ -554,7 +562,7 @@ int nvfp4_gemm(const uint8_t *codes, const uint8_t *scales, const float *alpha, 
   {
     TraceScope tr(kTrGemmTc, stream);
     const long fw = g_first_wait.load();
-    e = launch_gemm_tc(codes, scales, alpha, rows, cols, x, cols, batch, d->sms, part,
+    e = launch_gemm_tc(codes, scales, alpha, rows, cols, x, batch, d->sms, part, y,
                        fw < 0 ? -1 : (int)std::min<long>(fw, INT32_MAX), stream);
   }
   if (e == cudaSuccess) {
@@ -613,7 +621,7 @@ int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha
                           ep.gate_stride, at(ep.residual, ep.residual_stride), ep.residual_stride, ep.activation,
                           const_cast<char *>(at(y, y_stride)), y_stride};
     TraceScope tr(kTrLinear, stream);
-    e = launch_linear(a, d->sms, workspace ? workspace : own, stream);
+    e = launch_linear(a, d->sms, workspace ? workspace : own, first_tries(), stream);
   }
   const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);

@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
           }
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        // 2^-up takes the largest into [2^13, 2^14); zero, inf and NaN heads stay as they are
-        const int e = (int)(top >> 7), up = e == 0 || e == 255 ? 0 : e - 127 - 13;
+        // 2^-up takes the largest into [2^13, 2^14); inf and NaN heads stay as they are
+        const int e = (int)(top >> 7), up = e == 255 ? 0 : max(e, 1) - 127 - 13;
         const float f1 = __uint_as_float((uint32_t)(127 - up / 2) << 23), f2 = __uint_as_float((uint32_t)(127 - (up - up / 2)) << 23);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)

@@ -44,8 +44,8 @@
 #include <cuda_runtime.h>
 
 #include "nvfp4_device.cuh"
-#include "nvfp4_epilogue.cuh"
 #include "nvfp4_internal.h"
+#include "nvfp4_tc.cuh"
 
 namespace nvfp4 {
 
@@ -61,12 +61,6 @@ constexpr int kTcThreads = 768;
 // per-thread layout [512 threads][16 code bytes] + [256][4 scale bytes]
 constexpr uint32_t kTcSlot = 10240;
 constexpr int kTcDynBudget = 227 * 1024 - 2048;  // dynamic shared memory (static arrays take the rest)
-// A wait suspends the thread (no spinning) for up to kTcSuspendNs per try,
-// and gives up after kTcTries tries (about 2 s): far beyond any legitimate
-// wait, which lasts a few microseconds.
-constexpr uint32_t kTcSuspendNs = 1000000u;
-constexpr int kTcTries = 2000;
-
 // S stages, each a dequantized A tile (32 KiB) and the matching N x 128 tile
 // of X (N x 256 bytes), then D ring slots of codes (10 KiB each), within
 // 227 KiB.  A stage is freed by the completion of its MMAs.
@@ -87,25 +81,6 @@ struct TcCfg {
   static_assert(kSmem <= (size_t)kTcDynBudget, "shared memory");
 };
 
-__device__ __forceinline__ uint32_t tc_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-// Byte offset of 16-byte chunk `c` (0..7) of row `r` in a K-major tile with
-// the 128-byte swizzle: rows of 128 bytes, chunk index XOR (row mod 8).
-__device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
-
-// Shared-memory matrix descriptor of a K-major, 128-byte-swizzled operand:
-// start address >> 4 (bits 0-13), leading byte offset 16 (unused by this
-// layout), stride byte offset 1024 (8 rows of 128 bytes, bits 32-45),
-// descriptor version 1 (bits 46-47), swizzle mode 128 bytes (bits 61-63).
-__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
 // Instruction descriptor of kind::f16: fp32 accumulator (bits 4-5 = 1), A and
 // B bf16 (bits 7-9 = 1, bits 10-12 = 1), both K-major, N >> 3 at bits 17-22,
 // M >> 4 at bits 24-28.
@@ -113,89 +88,11 @@ __device__ __forceinline__ uint32_t tc_idesc(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTcM >> 4) << 24);
 }
 
-__device__ __forceinline__ void mbar_init(uint32_t mb, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mb), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t mb) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mb) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t mb, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mb), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t mb, uint32_t parity) {
-  uint32_t done;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(mb), "r"(parity), "n"(kTcSuspendNs) : "memory");
-  return done != 0;
-}
-
-__device__ __forceinline__ bool mbar_test(uint32_t mb, uint32_t parity) {
-  uint32_t done;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(mb), "r"(parity) : "memory");
-  return done != 0;
-}
-
-// Bounded wait for the phase of `parity`; gives up early once another role of
-// the CTA has raised `fail`, and raises it itself when the limit (about 2 s)
-// runs out.  SLEEP_NS = 0: suspending tries, for the waits on the critical
-// path; otherwise the warp sleeps that long between tests, which keeps
-// waiting warps that are off the critical path from taking issue slots from
-// the dequantizing ones.
-template <int SLEEP_NS = 0>
-__device__ __forceinline__ bool tc_wait(uint32_t mb, uint32_t parity, volatile int *fail) {
-  if (mbar_test(mb, parity)) return true;
-  constexpr int kTries = SLEEP_NS ? 2000000000 / SLEEP_NS : kTcTries;
-  for (int it = 0; it < kTries; ++it) {
-    if (SLEEP_NS) {
-      __nanosleep(SLEEP_NS);
-      if (mbar_test(mb, parity)) return true;
-    } else if (mbar_try(mb, parity)) {
-      return true;
-    }
-    if (*fail) return false;
-  }
-  *fail = 1;
-  return false;
-}
-
-// The first wait of a CTA's MMA thread under the test hook: gives up after
-// `tries` tries (0: at once) and raises `fail`.
-__device__ __forceinline__ bool tc_wait_tries(uint32_t mb, uint32_t parity, volatile int *fail, int tries) {
-  for (int it = 0; it < tries; ++it)
-    if (mbar_try(mb, parity)) return true;
-  *fail = 1;
-  return false;
-}
-
-// The same wait without the early exit: used after a failure to let this
-// CTA's own copies and MMAs in flight finish before it leaves.
-__device__ __forceinline__ void tc_drain(uint32_t mb, uint32_t parity) {
-  for (int it = 0; it < kTcTries && !mbar_try(mb, parity); ++it) {
-  }
-}
-
-// Tiles of the work sequence: CTA c covers steps [c T / G, (c+1) T / G); the
-// CTA holding step g is floor(((g+1) G - 1) / T).
-__host__ __device__ __forceinline__ int64_t tc_first_step(int64_t c, int64_t T, int64_t G) { return c * T / G; }
-__host__ __device__ __forceinline__ int64_t tc_cta_of(int64_t g, int64_t T, int64_t G) { return ((g + 1) * G - 1) / T; }
-
-// 16 consecutive fp32 columns of tensor memory, one lane per thread (the
-// warp's 32 lanes); the caller waits with tcgen05.wait::ld.
-__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-               "%12, %13, %14, %15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                 "=r"(r[15])
-               : "r"(taddr));
-}
-
 // Kernel arguments beside the tensor map.
 struct TcArgs {
   const uint8_t *codes;
   const uint8_t *scales;
-  const float *alpha;  // or nullptr: weights without it
+  const float *alpha;
   int64_t rows, cols;
   int batch;
   int64_t K;      // steps per tile
@@ -234,8 +131,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_gemm_tc(const __grid_constant
   const int nseg = (int)((g1 - 1) / a.K - t_first + 1);
   volatile int *vfail = &fail;
 
-  // weights as nvfp4_dequantize writes them, or (no alpha) the exact q * Delta of nvfp4_linear
-  if (tid < 256) s_tab[tid] = a.alpha ? __fmul_rn(*a.alpha, e4m3_value(tid)) : e4m3_value(tid);
+  if (tid < 256) s_tab[tid] = __fmul_rn(*a.alpha, e4m3_value(tid));
   if (tid == 0) fail = 0;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_smem(&tmem_slot)),
@@ -588,30 +484,6 @@ __global__ void __launch_bounds__(256) k_gemm_tc_reduce(const float *__restrict_
   }
 }
 
-// nvfp4_linear's reduction: the same sums, each finished by the epilogue.
-__global__ void __launch_bounds__(256) k_linear_reduce(const float *__restrict__ ws, const __grid_constant__ LinearArgs a,
-                                                       int64_t K, int64_t T, int64_t G, int maxc) {
-  const int64_t tiles = (a.rows + kTcM - 1) / kTcM;
-  const int64_t n = (int64_t)a.batch * tiles * (kTcM / 4);  // groups of 4 rows
-  const int64_t s4 = (int64_t)a.batch * kTcM / 4;
-  const float alpha = *a.alpha;
-  for (int64_t g = (int64_t)blockIdx.x * 256 + threadIdx.x; g < n; g += (int64_t)gridDim.x * 256) {
-    const int64_t rg = g % (tiles * (kTcM / 4)), b = g / (tiles * (kTcM / 4));
-    const int64_t t = rg / (kTcM / 4), r0 = t * kTcM + (rg % (kTcM / 4)) * 4;
-    if (r0 >= a.rows) continue;
-    const int cnt = (int)(tc_cta_of((t + 1) * K - 1, T, G) - tc_cta_of(t * K, T, G)) + 1;
-    const float4 *p = reinterpret_cast<const float4 *>(ws + ((t * maxc) * a.batch + b) * kTcM + (r0 - t * kTcM));
-    float4 acc = p[0];
-#pragma unroll 4
-    for (int j = 1; j < cnt; ++j) {
-      const float4 v = p[j * s4];
-      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-    }
-    const float w[4] = {acc.x, acc.y, acc.z, acc.w};
-    for (int u = 0; u < 4 && r0 + u < a.rows; ++u) finish(a, alpha, (int)b, r0 + u, w[u]);
-  }
-}
-
 namespace {
 
 // cuTensorMapEncodeTiled, reached through the runtime's driver entry point
@@ -667,8 +539,8 @@ size_t gemm_tc_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms) {
 }
 
 cudaError_t launch_gemm_tc(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows,
-                           int64_t cols, const void *x, int64_t x_stride, int batch, int sms, float *ws,
-                           int first_tries, cudaStream_t st) {
+                           int64_t cols, const void *x, int batch, int sms, float *ws, float *y, int first_tries,
+                           cudaStream_t st) {
   if (!g_encode) return cudaErrorInitializationError;
   const TcPlan p = tc_plan(rows, cols, sms);
   const int n = gemm_tc_tile_n(batch);
@@ -676,7 +548,7 @@ cudaError_t launch_gemm_tc(const uint8_t *codes, const uint8_t *scales, const fl
   // and columns past the end read as zeros), 128-byte swizzle
   CUtensorMap m;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)batch};
-  const cuuint64_t strides[1] = {(cuuint64_t)x_stride * 2};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
   const cuuint32_t box[2] = {64u, (cuuint32_t)n};
   const cuuint32_t es[2] = {1u, 1u};
   if (g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(x), dims, strides, box, es,
@@ -709,13 +581,6 @@ cudaError_t launch_gemm_tc_reduce(const float *ws, int64_t rows, int64_t cols, i
                                   int grid, cudaStream_t st) {
   const TcPlan p = tc_plan(rows, cols, sms);
   k_gemm_tc_reduce<<<grid, 256, 0, st>>>(ws, rows, batch, p.K, p.T, p.G, p.maxc, y);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_linear_reduce(const float *ws, const LinearArgs &a, int sms, cudaStream_t st) {
-  const TcPlan p = tc_plan(a.rows, a.cols, sms);
-  const int64_t n = (int64_t)a.batch * p.tiles * (kTcM / 4);
-  k_linear_reduce<<<(int)std::min<int64_t>((n + 255) / 256, 8 * sms), 256, 0, st>>>(ws, a, p.K, p.T, p.G, p.maxc);
   return cudaGetLastError();
 }
 

@@ -62,8 +62,8 @@ cudaError_t launch_swizzle_scales(const uint8_t *scales, int64_t rows, int64_t k
 int gemm_tc_tile_n(int batch);
 size_t gemm_tc_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
 cudaError_t launch_gemm_tc(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows,
-                           int64_t cols, const void *x, int64_t x_stride, int batch, int sms, float *ws,
-                           int first_tries, cudaStream_t st);
+                           int64_t cols, const void *x, int batch, int sms, float *ws, float *y, int first_tries,
+                           cudaStream_t st);
 cudaError_t launch_gemm_tc_reduce(const float *ws, int64_t rows, int64_t cols, int batch, int sms, float *y,
                                   int grid, cudaStream_t st);
 cudaError_t prepare_gemm_tc_kernels();
@@ -130,9 +130,12 @@ struct AttendArgs {
   void *out;
   float *lse;
 };
-cudaError_t launch_linear_reduce(const float *ws, const LinearArgs &a, int sms, cudaStream_t st);
 size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
-cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, cudaStream_t st);
+cudaError_t prepare_linear_kernels();
+cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st);
+size_t linear_tc_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
+cudaError_t launch_linear_tc(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st);
+cudaError_t prepare_linear_tc_kernels();
 cudaError_t launch_kv_append(const AppendArgs &a, int sms, cudaStream_t st);
 size_t attend_workspace_bytes(const KvArgs &kv, int q_heads, int sms);
 cudaError_t prepare_attention_kernels();

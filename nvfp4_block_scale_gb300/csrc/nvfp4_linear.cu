@@ -1,8 +1,32 @@
 // nvfp4_linear.cu -- the W4A16 product with its epilogue:
 //   y[b][r] = bf16( residual + gate * act( alpha * sum_c q Delta x[b][c] + bias ) ).
 //
-// One warp per row and group of kLinVecs vectors, a lane every 32nd block of
-// 16 columns, fp32 sums joined by a butterfly.
+// More than kLinMmaVecs vectors go to the tcgen05 product (nvfp4_gemm_tc.cu)
+// with unrounded weights.  Fewer are bound by reading the weights once
+// (0.5625 B each) and run here, in one launch:
+//
+// Products: mma.sync m16n8k16 (f16 x f16 -> fp32), 16 rows of W by 8 vectors.
+// q * Delta is formed in registers in f16, two instructions per pair, exactly:
+// six significant bits between 2^-10 and 2688.  x is held in f16 too, each
+// vector scaled by a power of two so that its largest entry in the CTA's
+// columns lies in [2^13, 2^14): its 8 bits stay exact down to 2^-27 of that
+// entry, and an entry below is off by at most 2^-39 of it.
+//
+// Work split: a CTA owns a rectangle of W, `tiles` row tiles of 16 by `steps`
+// column steps of 128, and keeps x for its columns in shared memory in the
+// order in which the MMAs read it.  The rectangle's (tile, step) units, tile
+// by tile, are cut into eight contiguous runs of equal length, one per warp,
+// so no warp waits for another until the end.  A warp's sums of a tile go to
+// shared memory: to the tile's place if the warp took the tile's first step,
+// else (its run began inside the tile) to a place of the warp's own; after one
+// barrier they are added in warp order.  Rectangles that share rows meet in
+// the workspace, where the CTA that comes last (a counter per group of rows)
+// adds them in column order.
+//
+// Loads: a lane takes 16 consecutive code bytes (32 columns) of two rows per
+// step, kLinDepth steps ahead, straight into registers.  The order of the
+// columns inside a step is permuted alike on both sides, so that those bytes
+// feed the MMAs without a shuffle.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -14,55 +38,356 @@
 
 namespace nvfp4 {
 
+constexpr int kLinMmaVecs = 8;     // vectors up to which this kernel runs
 constexpr int kLinWarps = 8;
-constexpr int kLinVecs = 4;
+constexpr int kLinThreads = kLinWarps * 32;
+constexpr int kLinDepth = 4;       // steps in flight per warp
+constexpr int kLinMaxGroups = (int)(kCounterBytes / 4);
+constexpr int kLinSmem = 88 * 1024;  // dynamic shared memory of one of two CTAs per SM
 
-__device__ __forceinline__ float e2m1_value(uint32_t n) {
-  const float m = (n & 6u) ? (float)(2u + (n & 1u)) * 0.5f * (float)(1u << ((n & 7u) >> 1)) * 0.5f : 0.5f * (float)(n & 1u);
-  return n & 8u ? -m : m;
+// Shared memory of a rectangle: x, the tiles' sums, the warps' own.
+__host__ __device__ constexpr int64_t lin_smem(int nt, int64_t steps, int64_t tiles) {
+  return steps * nt * 2048 + (tiles + kLinWarps) * nt * 512;
 }
 
-__global__ void __launch_bounds__(kLinWarps * 32) k_linear(const __grid_constant__ LinearArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kLinWarps + (threadIdx.x >> 5);
-  const int b0 = blockIdx.y * kLinVecs;
-  if (row >= a.rows) return;
+struct LinPlan {
+  int steps, tiles;         // of W
+  int ranges, groups;       // column ranges, row groups
+  int max_steps, max_tiles; // of a rectangle
+};
+
+struct LinLaunch {
+  LinearArgs a;
+  LinPlan p;
+  uint32_t *count;  // [groups], zero between calls
+  float4 *part;     // [ranges][tiles][NT][32]: sums in the MMA's lane order
+};
+
+// One step of a lane: 32 columns (two blocks) of rows g and g + 8.
+struct LinLoad {
+  uint4 c[2];
+  uint32_t s[2];
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The finished sums of one lane's fragment: rows g, g + 8 of a tile, vectors 8 nt + 2 cq + {0, 1}.
+__device__ __forceinline__ void finish4(const LinearArgs &a, float alpha, int64_t tile, int nt, int lane, const float4 &v) {
+  const float w[4] = {v.x, v.y, v.z, v.w};
+  auto b = [&](int j) { return (int64_t)(8 * nt + 2 * (lane & 3) + (j & 1)); };
+  auto r = [&](int j) { return tile * 16 + 8 * (j >> 1) + (lane >> 2); };
+  finish<4>(a, alpha, w, [&](int j) { return b(j) < a.batch && r(j) < a.rows; }, b, r);
+}
+
+// WIDE: rows of codes are whole multiples of 16 bytes and of scales of 2, and
+// so aligned; otherwise a block at a time.
+template <int NT, bool WIDE>
+__global__ void __launch_bounds__(kLinThreads, 2) k_linear(const __grid_constant__ LinLaunch p) {
+  constexpr int N = 8 * NT;
+  extern __shared__ uint4 dsm[];
+  __shared__ uint32_t s_top[N];  // bf16 bits of each vector's largest |x| in the CTA's columns
+  __shared__ int s_last;
+  const LinearArgs &a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
+  const int range = blockIdx.x % p.p.ranges, group = blockIdx.x / p.p.ranges;
+  const int k0 = (int)((int64_t)range * p.p.steps / p.p.ranges), k1 = (int)((int64_t)(range + 1) * p.p.steps / p.p.ranges);
+  const int t0 = (int)((int64_t)group * p.p.tiles / p.p.groups), t1 = (int)((int64_t)(group + 1) * p.p.tiles / p.p.groups);
+  const int nk = k1 - k0, ntile = t1 - t0;
+  uint4 *xs = dsm;                                                              // [nk][4][N][4] 16-byte units
+  float4 *sums = reinterpret_cast<float4 *>(dsm + (size_t)p.p.max_steps * NT * 128);  // [tiles][NT][32], then [warps][NT][32]
+  float4 *own = sums + p.p.max_tiles * NT * 32;
+
+  // ---- this warp's run of units and its first loads.  Rows and columns past
+  // the end read the last ones: those rows are not written, and x is zero there.
+  const int units = ntile * nk;  // (a CTA's rectangle fits its shared memory: far below 2^31)
+  const int u0 = (int)((int64_t)warp * units / kLinWarps), u1 = (int)((int64_t)(warp + 1) * units / kLinWarps);
   const int64_t nblk = a.cols / 16;
-  float acc[kLinVecs] = {};
-  for (int64_t j = lane; j < nblk; j += 32) {
-    const uint2 c = reinterpret_cast<const uint2 *>(a.codes)[row * nblk + j];
-    const float s = e4m3_value(a.scales[row * nblk + j]);
-    for (int i = 0; i < 16; ++i) {
-      const float w = e2m1_value(((i < 8 ? c.x : c.y) >> (4 * (i & 7))) & 15u) * s;
+  int ft = u0 / nk, fk = u0 - ft * nk;  // next unit to load
+  const uint8_t *fc[2], *fs[2];         // its rows' codes and scales, from the lane's first column
+  const int last = (int)min(nblk - 1, (int64_t)INT32_MAX);
+  auto rows_of = [&](int t) {
 #pragma unroll
-      for (int v = 0; v < kLinVecs; ++v)
-        if (b0 + v < a.batch)
-          acc[v] = fmaf(w, __bfloat162float(static_cast<const __nv_bfloat16 *>(a.x)[(b0 + v) * a.x_stride + 16 * j + i]),
-                        acc[v]);
+    for (int h = 0; h < 2; ++h) {
+      const int64_t row = min((int64_t)(t0 + t) * 16 + 8 * h + g, a.rows - 1);
+      fc[h] = a.codes + row * nblk * 8;
+      fs[h] = a.scales + row * nblk;
+    }
+  };
+  rows_of(ft);
+  auto fetch = [&](LinLoad &d) {
+    const int blk = (k0 + fk) * 8 + 2 * cq;
+    if (WIDE) {
+      const int64_t at = min(blk, last - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        d.c[h] = __ldcs(reinterpret_cast<const uint4 *>(fc[h] + 8 * at));
+        d.s[h] = __ldg(reinterpret_cast<const uint16_t *>(fs[h] + at));
+      }
+    } else {
+      const int64_t at = min(blk, last), at1 = min(blk + 1, last);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint2 lo = __ldcs(reinterpret_cast<const uint2 *>(fc[h]) + at), hi = __ldcs(reinterpret_cast<const uint2 *>(fc[h]) + at1);
+        d.c[h] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        d.s[h] = (uint32_t)__ldg(fs[h] + at) | (uint32_t)__ldg(fs[h] + at1) << 8;
+      }
+    }
+    if (++fk == nk) {
+      fk = 0;
+      rows_of(++ft);
+    }
+  };
+  LinLoad buf[kLinDepth];
+  int ahead = u0;  // units loaded
+#pragma unroll
+  for (int i = 0; i < kLinDepth; ++i)
+    if (ahead < u1) {
+      fetch(buf[i]);
+      ++ahead;
+    }
+
+  // ---- x into shared memory: the largest entry of each vector, then the scaled f16 values
+  if (tid < N) s_top[tid] = 0u;
+  __syncthreads();
+  const int xu = nk * 16, chunks = (xu + 31) / 32;  // 8-column units of a vector; a warp takes 32 at a time
+  const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
+  auto load_x = [&](int n, int u) {
+    const int64_t col = (int64_t)k0 * 128 + 8 * u;
+    return n < a.batch && u < xu && col < a.cols ? __ldg(reinterpret_cast<const uint4 *>(x + n * a.x_stride + col))
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+  };
+#pragma unroll 4
+  for (int t = warp; t < a.batch * chunks; t += kLinWarps) {
+    const int n = t / chunks;
+    const uint4 v = load_x(n, (t - n * chunks) * 32 + lane);
+    uint32_t m;
+    asm("{\n\t.reg .b32 t;\n\tmax.xorsign.abs.bf16x2 %0, %1, %2;\n\tmax.xorsign.abs.bf16x2 t, %3, %4;\n\t"
+        "max.xorsign.abs.bf16x2 %0, %0, t;\n\t}" : "=r"(m) : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+    m &= 0x7FFF7FFFu;
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+    if (lane == 0) atomicMax(&s_top[n], m);
+  }
+  __syncthreads();
+  auto up_of = [&](int n) {  // 2^-up takes the vector's largest entry into [2^13, 2^14)
+    const int e = (int)(s_top[n] >> 7);
+    return e == 255 ? 0 : max(e, 1) - 127 - 13;
+  };
+#pragma unroll 2
+  for (int t = warp; t < N * chunks; t += kLinWarps) {
+    const int n = t / chunks, u = (t - n * chunks) * 32 + lane, up = up_of(n);
+    const float f1 = pow2(-up / 2), f2 = pow2(-up - (-up / 2));  // (2^-up alone may be out of range)
+    const uint4 v = load_x(n, u);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+          : "=r"(o[i]) : "f"(__uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2), "f"(__uint_as_float(w[i] << 16) * f1 * f2));
+    // unit u of the range: step u / 16, lane quarter (u / 4) % 4, pair of k-steps u % 4
+    if (u < xu) xs[(((u >> 4) * 4 + (u & 3)) * N + n) * 4 + ((u >> 2) & 3)] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  __syncthreads();
+
+  // ---- the run
+  {
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[nt][j] = 0.0f;
+    int ct = u0 / nk, ck = u0 - ct * nk;
+    bool mine = ck == 0;  // this warp takes the current tile's first step
+    const uint4 *xl = xs + g * 4 + cq;
+    auto unit = [&](LinLoad &d) {
+      uint32_t sc[2][2];  // rows g, g + 8: f16 pairs {Delta, Delta} of the lane's two blocks
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t f;
+        asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(f) : "r"(d.s[h]));
+        sc[h][0] = __byte_perm(f, 0u, 0x1010);
+        sc[h][1] = __byte_perm(f, 0u, 0x3232);
+      }
+      const uint32_t cw[2][4] = {{d.c[0].x, d.c[0].y, d.c[0].z, d.c[0].w}, {d.c[1].x, d.c[1].y, d.c[1].z, d.c[1].w}};
+      const uint4 *xk = xl + ck * (16 * N);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {  // a word of codes: 8 columns, two k-steps
+        uint4 xb[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) xb[nt] = xk[jj * (4 * N) + nt * 32];
+        uint32_t w[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          e2m1x8_f16(cw[h][jj], w[h]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) w[h][b] = mul_f16x2(w[h][b], sc[h][jj >> 1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(acc[nt], w[0][0], w[1][0], w[0][1], w[1][1], xb[nt].x, xb[nt].y);
+          mma_f16(acc[nt], w[0][2], w[1][2], w[0][3], w[1][3], xb[nt].z, xb[nt].w);
+        }
+      }
+      if (ahead < u1) {
+        fetch(d);
+        ++ahead;
+      }
+      if (++ck == nk) {  // the tile's last step
+        float4 *to = mine ? sums + ct * NT * 32 : own + warp * NT * 32;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          to[nt * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+          acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+        }
+        ck = 0;
+        ++ct;
+        mine = true;
+      }
+    };
+    int left = u1 - u0;
+    while (left > 0) {
+#pragma unroll
+      for (int i = 0; i < kLinDepth; ++i)
+        if (left > 0) {
+          unit(buf[i]);
+          --left;
+        }
+    }
+    if (ck > 0 && u1 > u0) {  // the run ends inside a tile
+      float4 *to = mine ? sums + ct * NT * 32 : own + warp * NT * 32;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) to[nt * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
     }
   }
-#pragma unroll
-  for (int v = 0; v < kLinVecs; ++v) {
-    for (int o = 16; o > 0; o >>= 1) acc[v] += __shfl_xor_sync(0xFFFFFFFFu, acc[v], o);
-    if (lane == 0 && b0 + v < a.batch) finish(a, *a.alpha, b0 + v, row, acc[v]);
+  __syncthreads();
+
+  // ---- each tile's sum, and its way out
+  const float alpha = *a.alpha;
+  for (int i = tid; i < ntile * NT * 32; i += kLinThreads) {
+    const int t = i / (NT * 32), f = i - t * (NT * 32), nt = f >> 5, l = f & 31;
+    float4 v = sums[i];
+    // warps whose run began inside the tile: those holding its units after the first
+    const int wa = (int)(((int64_t)(t * nk + 1) * kLinWarps - 1) / units), wb = (int)(((int64_t)(t + 1) * nk * kLinWarps - 1) / units);
+    for (int w = wa + 1; w <= wb; ++w) {
+      if ((int)((int64_t)w * units / kLinWarps) == (int)((int64_t)(w + 1) * units / kLinWarps)) continue;  // an empty run
+      const float4 o = own[w * NT * 32 + f];
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    const int up0 = up_of(8 * nt + 2 * (l & 3)), up1 = up_of(8 * nt + 2 * (l & 3) + 1);
+    const float a0 = pow2(up0 / 2), a1 = pow2(up0 - up0 / 2), b0 = pow2(up1 / 2), b1 = pow2(up1 - up1 / 2);
+    v = make_float4(v.x * a0 * a1, v.y * b0 * b1, v.z * a0 * a1, v.w * b0 * b1);
+    if (p.p.ranges == 1) finish4(a, alpha, t0 + t, nt, l, v);
+    else __stcg(p.part + ((int64_t)range * p.p.tiles + t0) * NT * 32 + i, v);
+  }
+  if (p.p.ranges == 1) return;
+
+  // ---- the ranges of this group of rows
+  __syncthreads();
+  if (tid == 0) {
+    s_last = arrive_count(p.count + group) == (uint32_t)(p.p.ranges - 1);
+    if (s_last) p.count[group] = 0u;  // as the next call wants it
+  }
+  __syncthreads();
+  if (!s_last) return;
+  for (int i = tid; i < ntile * NT * 32; i += kLinThreads) {
+    const float4 *from = p.part + (int64_t)t0 * NT * 32 + i;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int k = 0; k < p.p.ranges; ++k) {
+      const float4 o = __ldcg(from + (int64_t)k * p.p.tiles * NT * 32);
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    finish4(a, alpha, t0 + i / (NT * 32), i % (NT * 32) >> 5, i & 31, v);
   }
 }
+
+// cols == 0: the epilogue of a zero sum.
+__global__ void __launch_bounds__(256) k_linear_empty(const __grid_constant__ LinearArgs a) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.rows * a.batch; i += (int64_t)gridDim.x * 256) {
+    const float zero[1] = {0.0f};
+    finish<1>(a, *a.alpha, zero, [](int) { return true; }, [&](int) { return i / a.rows; }, [&](int) { return i % a.rows; });
+  }
+}
+
+namespace {
+
+int lin_nt(int batch) { return batch <= 8 ? 1 : batch <= 16 ? 2 : 4; }
+
+// The cut into rectangles with the least estimated time per wave of 2 CTAs per
+// SM, in bytes of weights that a CTA reads meanwhile: the rectangle itself, x
+// (converted by every CTA), and, with several ranges, their sums' way through
+// L2.  false: none fits (then the tcgen05 product runs).
+bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {
+  const int nt = lin_nt(batch), ctas = 2 * sms;
+  const int64_t steps = (cols + 127) / 128, tiles = (rows + 15) / 16;
+  if (steps > (1 << 24) || tiles > (1 << 27)) return false;
+  int64_t least = -1;
+  for (int64_t ranges = 1; ranges <= std::min<int64_t>(steps, 96); ++ranges) {
+    const int64_t ms = (steps + ranges - 1) / ranges;
+    const int64_t most = (kLinSmem - lin_smem(nt, ms, 0)) / (nt * 512);  // tiles that fit
+    if (most < 1) continue;
+    int64_t groups = std::min<int64_t>(tiles, std::max<int64_t>(1, ctas / ranges));
+    if ((tiles + groups - 1) / groups > most) groups = (tiles + most - 1) / most;
+    if (ranges > 1 && groups > kLinMaxGroups) continue;
+    const int64_t mt = (tiles + groups - 1) / groups, waves = (groups * ranges + ctas - 1) / ctas;
+    const int64_t cost = waves * (mt * ms * 1152 + ms * batch * 100 + (ranges > 1 ? 24000 + mt * nt * 512 * (2 + ranges / 4) : 0));
+    if (least < 0 || cost < least) {
+      least = cost;
+      *best = LinPlan{(int)steps, (int)tiles, (int)ranges, (int)groups, (int)ms, (int)mt};
+    }
+  }
+  return least >= 0;
+}
+
+template <int NT>
+cudaError_t lin_launch(const LinLaunch &p, bool wide, cudaStream_t st) {
+  const size_t smem = (size_t)lin_smem(NT, p.p.max_steps, p.p.max_tiles);
+  const int grid = p.p.ranges * p.p.groups;
+  if (wide) k_linear<NT, true><<<grid, kLinThreads, smem, st>>>(p);
+  else k_linear<NT, false><<<grid, kLinThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
 
 size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms) {
-  return kCounterBytes + (batch > 16 ? gemm_tc_workspace_bytes(rows, cols, batch, sms) : 0);
+  LinPlan p;
+  if (batch > kLinMmaVecs || !lin_plan(rows, cols, batch, sms, &p))
+    return linear_tc_workspace_bytes(rows, cols, batch, sms);
+  return p.ranges == 1 ? 0 : kCounterBytes + (size_t)p.ranges * p.tiles * lin_nt(batch) * 512;
 }
 
-cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, cudaStream_t st) {
-  if (a.cols > 0 && a.batch > 16) {
-    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
-    const cudaError_t e = launch_gemm_tc(a.codes, a.scales, nullptr, a.rows, a.cols, a.x, a.x_stride, a.batch, sms, part,
-                                         -1, st);
-    return e != cudaSuccess ? e : launch_linear_reduce(part, a, sms, st);
+cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st) {
+  if (a.cols == 0) {
+    k_linear_empty<<<(int)std::min<int64_t>((a.rows * a.batch + 255) / 256, 8 * sms), 256, 0, st>>>(a);
+    return cudaGetLastError();
   }
-  const int64_t gx = (a.rows + kLinWarps - 1) / kLinWarps;
-  if (gx > INT32_MAX) return cudaErrorInvalidValue;
-  k_linear<<<dim3((unsigned)gx, (unsigned)((a.batch + kLinVecs - 1) / kLinVecs)), kLinWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  void *part = static_cast<char *>(ws) + kCounterBytes;
+  LinPlan plan;
+  if (a.batch > kLinMmaVecs || !lin_plan(a.rows, a.cols, a.batch, sms, &plan))
+    return launch_linear_tc(a, sms, ws, first_tries, st);
+  const LinLaunch p = {a, plan, static_cast<uint32_t *>(ws), static_cast<float4 *>(part)};
+  const bool wide = a.cols % 32 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.scales) % 2 == 0;
+  switch (lin_nt(a.batch)) {
+    case 1: return lin_launch<1>(p, wide, st);
+    case 2: return lin_launch<2>(p, wide, st);
+    default: return lin_launch<4>(p, wide, st);
+  }
+}
+
+cudaError_t prepare_linear_kernels() {
+  auto set = [](auto *k) { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmem); };
+  cudaError_t e = cudaSuccess;
+  for (auto *k : {k_linear<1, true>, k_linear<1, false>, k_linear<2, true>, k_linear<2, false>, k_linear<4, true>,
+                  k_linear<4, false>})
+    if (e == cudaSuccess) e = set(k);
+  return e;
 }
 
 }  // namespace nvfp4
