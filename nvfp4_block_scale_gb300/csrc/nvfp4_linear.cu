@@ -1,16 +1,15 @@
 // nvfp4_linear.cu -- the W4A16 product with its epilogue:
 //   y[b][r] = bf16( residual + gate * act( alpha * sum_c q Delta x[b][c] + bias ) ).
 //
-// More than kLinMmaVecs vectors go to the tcgen05 product (nvfp4_gemm_tc.cu)
-// with unrounded weights.  Fewer are bound by reading the weights once
-// (0.5625 B each) and run here, in one launch:
+// Many vectors and large tensors go to the tcgen05 product
+// (nvfp4_linear_tc.cu).  The others are bound by latency, then by reading the
+// weights once (0.5625 B each), and run here, in one launch without tensor
+// memory:
 //
-// Products: mma.sync m16n8k16 (f16 x f16 -> fp32), 16 rows of W by 8 vectors.
-// q * Delta is formed in registers in f16, two instructions per pair, exactly:
-// six significant bits between 2^-10 and 2688.  x is held in f16 too, each
-// vector scaled by a power of two so that its largest entry in the CTA's
-// columns lies in [2^13, 2^14): its 8 bits stay exact down to 2^-27 of that
-// entry, and an entry below is off by at most 2^-39 of it.
+// Products: mma.sync m16n8k16 (bf16 x bf16 -> fp32), 16 rows of W by 8 vectors.
+// q * Delta is formed in registers, exactly: six significant bits between
+// 2^-10 and 2688, in f16 first (two instructions per pair), then bf16 (three
+// more), so that x is used as it is.
 //
 // Work split: a CTA owns a rectangle of W, `tiles` row tiles of 16 by `steps`
 // column steps of 128, and keeps x for its columns in shared memory in the
@@ -38,7 +37,12 @@
 
 namespace nvfp4 {
 
-constexpr int kLinMmaVecs = 8;     // vectors up to which this kernel runs
+// This kernel takes up to 16 vectors, and W up to so many blocks of 16 x 128
+// per CTA of a full wave.  Measured against the tcgen05 product (us): 1 vector
+// 4096 x 4096 (27 blocks) 10.2 against 12.1, 14336 x 4096 (94) 17.5 against
+// 17.9; 8 vectors 24 against 17.9 there; 16 vectors 1024 x 4096 (7) 9.2 against
+// 9.4, 4096 x 4096 14.5 against 12.4.
+constexpr int kLinVecs = 16, kLinBlocks8 = 32, kLinBlocks16 = 8;
 constexpr int kLinWarps = 8;
 constexpr int kLinThreads = kLinWarps * 32;
 constexpr int kLinDepth = 4;       // steps in flight per warp
@@ -61,6 +65,7 @@ struct LinLaunch {
   LinPlan p;
   uint32_t *count;  // [groups], zero between calls
   float4 *part;     // [ranges][tiles][NT][32]: sums in the MMA's lane order
+  int min_steps, long_ranges, min_tiles, long_groups;  // steps = min_steps * ranges + long_ranges, tiles likewise
 };
 
 // One step of a lane: 32 columns (two blocks) of rows g and g + 8.
@@ -69,9 +74,16 @@ struct LinLoad {
   uint32_t s[2];
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+// f16 pair -> bf16 pair (exact for six significant bits).
+__device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t v) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+  return r;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -91,22 +103,21 @@ template <int NT, bool WIDE>
 __global__ void __launch_bounds__(kLinThreads, 2) k_linear(const __grid_constant__ LinLaunch p) {
   constexpr int N = 8 * NT;
   extern __shared__ uint4 dsm[];
-  __shared__ uint32_t s_top[N];  // bf16 bits of each vector's largest |x| in the CTA's columns
   __shared__ int s_last;
   const LinearArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
-  const int range = blockIdx.x % p.p.ranges, group = blockIdx.x / p.p.ranges;
-  const int k0 = (int)((int64_t)range * p.p.steps / p.p.ranges), k1 = (int)((int64_t)(range + 1) * p.p.steps / p.p.ranges);
-  const int t0 = (int)((int64_t)group * p.p.tiles / p.p.groups), t1 = (int)((int64_t)(group + 1) * p.p.tiles / p.p.groups);
-  const int nk = k1 - k0, ntile = t1 - t0;
+  // the first (steps mod ranges) ranges and (tiles mod groups) groups are one longer
+  const int group = blockIdx.x / (uint32_t)p.p.ranges, range = blockIdx.x - group * p.p.ranges;
+  const int nk = p.min_steps + (range < p.long_ranges), k0 = range * p.min_steps + min(range, p.long_ranges);
+  const int ntile = p.min_tiles + (group < p.long_groups), t0 = group * p.min_tiles + min(group, p.long_groups);
   uint4 *xs = dsm;                                                              // [nk][4][N][4] 16-byte units
   float4 *sums = reinterpret_cast<float4 *>(dsm + (size_t)p.p.max_steps * NT * 128);  // [tiles][NT][32], then [warps][NT][32]
   float4 *own = sums + p.p.max_tiles * NT * 32;
 
   // ---- this warp's run of units and its first loads.  Rows and columns past
   // the end read the last ones: those rows are not written, and x is zero there.
-  const int units = ntile * nk;  // (a CTA's rectangle fits its shared memory: far below 2^31)
-  const int u0 = (int)((int64_t)warp * units / kLinWarps), u1 = (int)((int64_t)(warp + 1) * units / kLinWarps);
+  const int units = ntile * nk;  // (a CTA's rectangle fits its shared memory: 8 units is far below 2^31)
+  const int u0 = warp * units / kLinWarps, u1 = (warp + 1) * units / kLinWarps;
   const int64_t nblk = a.cols / 16;
   int ft = u0 / nk, fk = u0 - ft * nk;  // next unit to load
   const uint8_t *fc[2], *fs[2];         // its rows' codes and scales, from the lane's first column
@@ -152,46 +163,19 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear(const __grid_constant
       ++ahead;
     }
 
-  // ---- x into shared memory: the largest entry of each vector, then the scaled f16 values
-  if (tid < N) s_top[tid] = 0u;
-  __syncthreads();
-  const int xu = nk * 16, chunks = (xu + 31) / 32;  // 8-column units of a vector; a warp takes 32 at a time
-  const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
-  auto load_x = [&](int n, int u) {
+  // ---- x into shared memory, 16 bytes (8 columns) at a time; zeros past the
+  // last vector and column
+  const int xu = nk * 16;  // 8-column units of a vector
+  for (int i = tid; i < N * xu; i += kLinThreads) {
+    const int n = i / xu, u = i - n * xu;
     const int64_t col = (int64_t)k0 * 128 + 8 * u;
-    return n < a.batch && u < xu && col < a.cols ? __ldg(reinterpret_cast<const uint4 *>(x + n * a.x_stride + col))
-                                                 : make_uint4(0u, 0u, 0u, 0u);
-  };
-#pragma unroll 4
-  for (int t = warp; t < a.batch * chunks; t += kLinWarps) {
-    const int n = t / chunks;
-    const uint4 v = load_x(n, (t - n * chunks) * 32 + lane);
-    uint32_t m;
-    asm("{\n\t.reg .b32 t;\n\tmax.xorsign.abs.bf16x2 %0, %1, %2;\n\tmax.xorsign.abs.bf16x2 t, %3, %4;\n\t"
-        "max.xorsign.abs.bf16x2 %0, %0, t;\n\t}" : "=r"(m) : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
-    m &= 0x7FFF7FFFu;
-    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-    if (lane == 0) atomicMax(&s_top[n], m);
-  }
-  __syncthreads();
-  auto up_of = [&](int n) {  // 2^-up takes the vector's largest entry into [2^13, 2^14)
-    const int e = (int)(s_top[n] >> 7);
-    return e == 255 ? 0 : max(e, 1) - 127 - 13;
-  };
-#pragma unroll 2
-  for (int t = warp; t < N * chunks; t += kLinWarps) {
-    const int n = t / chunks, u = (t - n * chunks) * 32 + lane, up = up_of(n);
-    const float f1 = pow2(-up / 2), f2 = pow2(-up - (-up / 2));  // (2^-up alone may be out of range)
-    const uint4 v = load_x(n, u);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-          : "=r"(o[i]) : "f"(__uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2), "f"(__uint_as_float(w[i] << 16) * f1 * f2));
+    const bool in = n < a.batch && col < a.cols;
     // unit u of the range: step u / 16, lane quarter (u / 4) % 4, pair of k-steps u % 4
-    if (u < xu) xs[(((u >> 4) * 4 + (u & 3)) * N + n) * 4 + ((u >> 2) & 3)] = make_uint4(o[0], o[1], o[2], o[3]);
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(xs + (((u >> 4) * 4 + (u & 3)) * N + n) * 4 + ((u >> 2) & 3)));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(to), "l"(static_cast<const __nv_bfloat16 *>(a.x) + (in ? n * a.x_stride + col : 0)), "r"(in ? 16 : 0) : "memory");
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 
   // ---- the run
@@ -225,12 +209,12 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear(const __grid_constant
         for (int h = 0; h < 2; ++h) {
           e2m1x8_f16(cw[h][jj], w[h]);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) w[h][b] = mul_f16x2(w[h][b], sc[h][jj >> 1]);
+          for (int b = 0; b < 4; ++b) w[h][b] = f16x2_bf16x2(mul_f16x2(w[h][b], sc[h][jj >> 1]));
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(acc[nt], w[0][0], w[1][0], w[0][1], w[1][1], xb[nt].x, xb[nt].y);
-          mma_f16(acc[nt], w[0][2], w[1][2], w[0][3], w[1][3], xb[nt].z, xb[nt].w);
+          mma_bf16(acc[nt], w[0][0], w[1][0], w[0][1], w[1][1], xb[nt].x, xb[nt].y);
+          mma_bf16(acc[nt], w[0][2], w[1][2], w[0][3], w[1][3], xb[nt].z, xb[nt].w);
         }
       }
       if (ahead < u1) {
@@ -272,15 +256,12 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear(const __grid_constant
     const int t = i / (NT * 32), f = i - t * (NT * 32), nt = f >> 5, l = f & 31;
     float4 v = sums[i];
     // warps whose run began inside the tile: those holding its units after the first
-    const int wa = (int)(((int64_t)(t * nk + 1) * kLinWarps - 1) / units), wb = (int)(((int64_t)(t + 1) * nk * kLinWarps - 1) / units);
+    const int wa = ((t * nk + 1) * kLinWarps - 1) / units, wb = ((t + 1) * nk * kLinWarps - 1) / units;
     for (int w = wa + 1; w <= wb; ++w) {
-      if ((int)((int64_t)w * units / kLinWarps) == (int)((int64_t)(w + 1) * units / kLinWarps)) continue;  // an empty run
+      if (w * units / kLinWarps == (w + 1) * units / kLinWarps) continue;  // an empty run
       const float4 o = own[w * NT * 32 + f];
       v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
     }
-    const int up0 = up_of(8 * nt + 2 * (l & 3)), up1 = up_of(8 * nt + 2 * (l & 3) + 1);
-    const float a0 = pow2(up0 / 2), a1 = pow2(up0 - up0 / 2), b0 = pow2(up1 / 2), b1 = pow2(up1 - up1 / 2);
-    v = make_float4(v.x * a0 * a1, v.y * b0 * b1, v.z * a0 * a1, v.w * b0 * b1);
     if (p.p.ranges == 1) finish4(a, alpha, t0 + t, nt, l, v);
     else __stcg(p.part + ((int64_t)range * p.p.tiles + t0) * NT * 32 + i, v);
   }
@@ -316,16 +297,18 @@ __global__ void __launch_bounds__(256) k_linear_empty(const __grid_constant__ Li
 
 namespace {
 
-int lin_nt(int batch) { return batch <= 8 ? 1 : batch <= 16 ? 2 : 4; }
+int lin_nt(int batch) { return batch <= 8 ? 1 : 2; }
 
 // The cut into rectangles with the least estimated time per wave of 2 CTAs per
 // SM, in bytes of weights that a CTA reads meanwhile: the rectangle itself, x
-// (converted by every CTA), and, with several ranges, their sums' way through
-// L2.  false: none fits (then the tcgen05 product runs).
+// (read by every CTA), and, with several ranges, their sums' way through
+// L2.  false: the tcgen05 product runs.
 bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {
   const int nt = lin_nt(batch), ctas = 2 * sms;
   const int64_t steps = (cols + 127) / 128, tiles = (rows + 15) / 16;
-  if (steps > (1 << 24) || tiles > (1 << 27)) return false;
+  if (batch > kLinVecs || tiles > (int64_t)ctas * kLinBlocks8 ||
+      steps * tiles > (int64_t)ctas * (batch <= 8 ? kLinBlocks8 : kLinBlocks16))
+    return false;
   int64_t least = -1;
   for (int64_t ranges = 1; ranges <= std::min<int64_t>(steps, 96); ++ranges) {
     const int64_t ms = (steps + ranges - 1) / ranges;
@@ -335,7 +318,7 @@ bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {
     if ((tiles + groups - 1) / groups > most) groups = (tiles + most - 1) / most;
     if (ranges > 1 && groups > kLinMaxGroups) continue;
     const int64_t mt = (tiles + groups - 1) / groups, waves = (groups * ranges + ctas - 1) / ctas;
-    const int64_t cost = waves * (mt * ms * 1152 + ms * batch * 100 + (ranges > 1 ? 24000 + mt * nt * 512 * (2 + ranges / 4) : 0));
+    const int64_t cost = waves * (mt * ms * 1152 + ms * batch * 500 + (ranges > 1 ? 44000 + mt * nt * 512 * (2 + ranges / 4) : 0));
     if (least < 0 || cost < least) {
       least = cost;
       *best = LinPlan{(int)steps, (int)tiles, (int)ranges, (int)groups, (int)ms, (int)mt};
@@ -357,7 +340,7 @@ cudaError_t lin_launch(const LinLaunch &p, bool wide, cudaStream_t st) {
 
 size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms) {
   LinPlan p;
-  if (batch > kLinMmaVecs || !lin_plan(rows, cols, batch, sms, &p))
+  if (!lin_plan(rows, cols, batch, sms, &p))
     return linear_tc_workspace_bytes(rows, cols, batch, sms);
   return p.ranges == 1 ? 0 : kCounterBytes + (size_t)p.ranges * p.tiles * lin_nt(batch) * 512;
 }
@@ -369,23 +352,19 @@ cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_trie
   }
   void *part = static_cast<char *>(ws) + kCounterBytes;
   LinPlan plan;
-  if (a.batch > kLinMmaVecs || !lin_plan(a.rows, a.cols, a.batch, sms, &plan))
+  if (!lin_plan(a.rows, a.cols, a.batch, sms, &plan))
     return launch_linear_tc(a, sms, ws, first_tries, st);
-  const LinLaunch p = {a, plan, static_cast<uint32_t *>(ws), static_cast<float4 *>(part)};
+  const LinLaunch p = {a, plan, static_cast<uint32_t *>(ws), static_cast<float4 *>(part), plan.steps / plan.ranges,
+                       plan.steps % plan.ranges, plan.tiles / plan.groups, plan.tiles % plan.groups};
   const bool wide = a.cols % 32 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(a.scales) % 2 == 0;
-  switch (lin_nt(a.batch)) {
-    case 1: return lin_launch<1>(p, wide, st);
-    case 2: return lin_launch<2>(p, wide, st);
-    default: return lin_launch<4>(p, wide, st);
-  }
+  return a.batch <= 8 ? lin_launch<1>(p, wide, st) : lin_launch<2>(p, wide, st);
 }
 
 cudaError_t prepare_linear_kernels() {
   auto set = [](auto *k) { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmem); };
   cudaError_t e = cudaSuccess;
-  for (auto *k : {k_linear<1, true>, k_linear<1, false>, k_linear<2, true>, k_linear<2, false>, k_linear<4, true>,
-                  k_linear<4, false>})
+  for (auto *k : {k_linear<1, true>, k_linear<1, false>, k_linear<2, true>, k_linear<2, false>})
     if (e == cudaSuccess) e = set(k);
   return e;
 }
