@@ -708,6 +708,7 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
   a.window = window;
   a.out = out;
   a.lse = lse;
+  a.first_tries = first_tries();
   void *own = nullptr;
   cudaError_t e = workspace ? cudaSuccess
                             : take_workspace(&own, attend_workspace_bytes(a.kv, q_heads, d->sms), *d, stream);

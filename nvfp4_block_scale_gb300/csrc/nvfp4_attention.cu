@@ -12,17 +12,21 @@
 // that share a cache head.  Its visible tokens are cut into tiles of KT, and the
 // tiles of all items form one sequence; CTA c takes the contiguous range
 // [c T / G, (c + 1) T / G) of it, so ragged lengths balance without the host
-// knowing them.  The part of an item inside a CTA's range is a segment.  Warp w
-// takes every fourth tile of a segment and keeps a running maximum, sum and
-// output of its own (no barrier inside a segment); the four meet in shared
-// memory at the segment's end.  An item inside one CTA is finished there; the
-// parts of a longer one go to the workspace and the CTA that writes the last
-// part (a counter per item) adds them in CTA order, so that results do not
-// depend on timing.  Nothing waits for another CTA.
+// knowing them.  The part of an item inside a CTA's range is a segment.  The
+// four consuming warps take the CTA's tiles in turn, each with a running
+// maximum, sum and output of its own (no barrier inside a segment), and meet in
+// shared memory at the segment's end.  An item inside one CTA is finished
+// there; the parts of a longer one go to the workspace, where a second launch
+// (k_attend_join) adds them in CTA order, so that results do not depend on
+// timing.  (When the CTA that came last added them, behind a fence and a
+// counter, it cost up to 14 us under load: 61 ragged sequences of up to 2048
+// tokens took 62 us.)
 //
-// Loads: each warp owns a ring of S tiles that it fills by TMA S tiles ahead,
-// across segments too (keys and values of a page as boxes of 128-byte rows,
-// 128-byte swizzle; pages outside the cache read as zeros).
+// Loads: a fifth warp fills a ring of S tiles per consuming warp by TMA, across
+// segments (keys and values of a page as boxes of 128-byte rows, 128-byte
+// swizzle; pages outside the cache read as zeros), and the queries of each
+// segment.  When the consumers asked for their own tiles, that took 700 clocks
+// of each tile's 1700.
 //
 // Products: mma.sync with the tokens as the M side, S^T = K Q^T and
 // O^T = V^T P^T: 16 tokens x 8 heads fill an m16n8 tile, so a group of 8 heads
@@ -48,11 +52,11 @@
 namespace nvfp4 {
 
 constexpr int kAttWarps = 4;
-constexpr int kAttThreads = kAttWarps * 32;
-constexpr int kAttMinTiles = 8;      // tiles per CTA below which fewer CTAs take part
-constexpr int kAttMaxCtas = 1024;    // counters in the workspace's zeroed head
+constexpr int kAttConsumers = kAttWarps * 32;
+constexpr int kAttThreads = kAttConsumers + 32;
+constexpr int kAttMinTiles = 4;      // tiles per CTA below which fewer CTAs take part
+constexpr int kAttMaxCtas = 1024;
 constexpr int kAttTries = 2000;      // x 1 ms: bound of a wait for a copy
-static_assert(kAttMaxCtas * 4 <= (int)kCounterBytes, "counters");
 
 template <int D, bool E4M3, int NT>
 struct AttCfg {
@@ -66,12 +70,14 @@ struct AttCfg {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRedStride = D + 4;                     // floats; keeps the lanes of a store in distinct banks
   static constexpr int kRed = kAttWarps * kHeads * kRedStride * 4;
+  static constexpr int kQRow = D * 2 + 16;                     // bytes of a staged query head (ldmatrix without conflicts)
+  static constexpr int kQ = kHeads * kQRow;                    // one of two buffers
   static constexpr int kBudget = 113 * 1024 - 2048;            // dynamic shared memory of one of two CTAs per SM
-  static constexpr int S0 = (kBudget - 1024 - kRed) / (kAttWarps * kTile);
+  static constexpr int S0 = (kBudget - 1024 - kRed - 2 * kQ) / (kAttWarps * kTile);
   static constexpr int S = S0 >= 4 ? 4 : S0 >= 2 ? S0 : 2;
   static constexpr int kRing = kAttWarps * S * kTile;
-  static constexpr size_t kSmem = 1024 + kRing + kRed;
-  static_assert(kSmem <= 225 * 1024, "shared memory");
+  static constexpr size_t kSmem = 1024 + kRing + kRed + 2 * kQ;
+  static_assert(kSmem <= 226 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t att_smem(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -134,6 +140,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return r;
 }
 
+// One thread of a converged warp, known as such to the compiler.
+__device__ __forceinline__ bool att_elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ bool att_wait(uint32_t mb, uint32_t parity, int tries) {
   for (int i = 0; i < tries; ++i) {
     uint32_t done;
@@ -144,13 +157,36 @@ __device__ __forceinline__ bool att_wait(uint32_t mb, uint32_t parity, int tries
   return false;
 }
 
+// An item that several CTAs share, from CTA c on: what k_attend_join needs.
+struct AttShared {
+  int64_t row;       // sequence * q_heads + first head
+  int heads, parts;  // parts 0: no such item begins in this CTA
+};
+
 // What the kernel needs beside the caller's arguments.
 struct AttLaunch {
   AttendArgs a;
-  uint32_t *count;   // [kAttMaxCtas], zero between calls
-  float *part;       // [2 G][heads][D] sums, then [2 G][heads][2] maxima and sums
-  int blocks;        // head blocks per cache head
-  int piece_shift;   // log2 of the rows of a box: min(page, KT)
+  AttShared *shared;  // [G]
+  float *part;        // [2 G][heads][D] sums, then [2 G][heads][2] maxima and sums
+  int blocks;         // head blocks per cache head
+  int piece_shift;    // log2 of the rows of a box: min(page, KT)
+};
+
+// Quotient of non-negative integers; the 64-bit one only where it is needed.
+__device__ __forceinline__ int64_t att_div(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The even split of T tiles over G CTAs: c T / G.
+struct AttSplit {
+  int64_t q, T;  // T / G
+  int r, G;      // T mod G
+  __device__ __forceinline__ AttSplit(int64_t T_, int G_) : T(T_), G(G_) {
+    q = att_div(T, G);
+    r = (int)(T - q * G);
+  }
+  __device__ __forceinline__ int64_t first(int c) const { return c * q + c * r / G; }
+  __device__ __forceinline__ int cta_of(int64_t g) const { return (int)att_div((g + 1) * G - 1, T); }
 };
 
 // A position in a CTA's range: a segment (tiles [first, first + count) of
@@ -163,7 +199,6 @@ struct AttSeg {
   int n, lo;         // visible tokens [lo, n)
 };
 
-template <int KT>
 __device__ __forceinline__ void att_visible(const AttendArgs &a, int b, int &n, int &lo) {
   const int64_t cap = a.kv.table_width << a.kv.page_shift;  // at most 2^30
   n = (int)max((int64_t)0, min((int64_t)__ldg(a.lengths + b), cap));
@@ -174,9 +209,7 @@ __device__ __forceinline__ int att_tiles(int n, int lo) { return n > 0 ? (n - 1)
 
 // The segment at tile `off` of item (b, hg), at most `left` tiles long.
 template <int KT>
-__device__ __forceinline__ void att_segment(const AttendArgs &a, AttSeg &s, int off, int64_t left) {
-  att_visible<KT>(a, s.b, s.n, s.lo);
-  s.total = att_tiles<KT>(s.n, s.lo);
+__device__ __forceinline__ void att_segment(AttSeg &s, int off, int64_t left) {
   s.off = off;
   s.first = s.lo / KT + off;
   s.count = (int)min((int64_t)(s.total - off), left);
@@ -187,13 +220,18 @@ template <int KT>
 __device__ __forceinline__ void att_next(const AttendArgs &a, AttSeg &s, int groups) {
   if (++s.hg == groups) {
     s.hg = 0;
-    int n, lo;
     do {  // (a later sequence holds the tiles that are left)
-      ++s.b;
-      att_visible<KT>(a, s.b, n, lo);
-    } while (n == 0);
+      att_visible(a, ++s.b, s.n, s.lo);
+    } while (s.n == 0);
+    s.total = att_tiles<KT>(s.n, s.lo);
   }
-  att_segment<KT>(a, s, 0, s.left);
+  att_segment<KT>(s, 0, s.left);
+}
+
+// 14: the scale 2^14 of E4M3's weights, which the sums have too.
+template <bool E4M3>
+__device__ __forceinline__ float att_lse(float ref, float sum) {
+  return (ref - (E4M3 ? 14.0f : 0.0f) + log2f(sum)) * 0.69314718055994531f;
 }
 
 template <int D, bool E4M3, int NT>
@@ -203,23 +241,30 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   using C = AttCfg<D, E4M3, NT>;
   constexpr int KT = C::KT, S = C::S, SUB = KT / 16, KS = D / 16;
   extern __shared__ uint8_t dsm[];
-  __shared__ __align__(8) uint64_t full[kAttWarps][S];
-  __shared__ int64_t s_sum[kAttWarps];
-  __shared__ int s_start[3];
+  // full: a tile has landed; empty: it has been read; q_*: the queries of a segment
+  __shared__ __align__(8) uint64_t full[kAttWarps * S], empty[kAttWarps * S], q_full[2], q_empty[2];
+  __shared__ int64_t s_sum[kAttWarps + 1];
+  __shared__ int s_start[3], s_fail;
   __shared__ float s_ml[kAttWarps][C::kHeads][2];
-  __shared__ int s_last;
   const AttendArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.q_heads / a.kv.kv_heads, groups = a.kv.kv_heads * p.blocks;
   const uint32_t raw = att_smem(dsm), base = (raw + 1023u) & ~1023u;
   float *red = reinterpret_cast<float *>(dsm + (base - raw) + C::kRing);  // [warps][heads][kRedStride]
-  const uint32_t ring = base + warp * S * C::kTile;
-  const uint32_t bars = att_smem(&full[warp][0]);
+  const uint32_t qs_smem = base + C::kRing + C::kRed;
+  pdl_launch_dependents();  // k_attend_join waits for the whole grid all the same
 
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s)
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + 8 * s) : "memory");
+  if (tid == 0) {
+    for (int i = 0; i < kAttWarps * S; ++i) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&full[i])) : "memory");
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&empty[i])) : "memory");
+    }
+    for (int i = 0; i < 2; ++i) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&q_full[i])) : "memory");
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(att_smem(&q_empty[i])), "r"(kAttWarps) : "memory");
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_fail = 0;
   }
 
   // ---- the tiles before each sequence; this CTA's range
@@ -228,7 +273,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   int64_t mine = 0;
   for (int b = sb0; b < sb1; ++b) {
     int n, lo;
-    att_visible<KT>(a, b, n, lo);
+    att_visible(a, b, n, lo);
     mine += att_tiles<KT>(n, lo);
   }
   int64_t incl = mine;
@@ -241,96 +286,146 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   __syncthreads();
   int64_t T = 0;
 #pragma unroll
-  for (int w = 0; w < kAttWarps; ++w) {
+  for (int w = 0; w <= kAttWarps; ++w) {
     if (w < warp) incl += s_sum[w];
     T += s_sum[w];
   }
   T *= groups;
-  const int64_t G = min((int64_t)gridDim.x, max((int64_t)1, (T + kAttMinTiles - 1) / kAttMinTiles));
-  const int64_t c = blockIdx.x;
-  const int64_t g0 = c < G ? c * T / G : T, g1 = c < G ? (c + 1) * T / G : T;
+  const int G = (int)min((int64_t)gridDim.x, max((int64_t)1, (T + kAttMinTiles - 1) / kAttMinTiles));
+  const int c = blockIdx.x;
+  const AttSplit split(T, G);
+  const int64_t g0 = c < G ? split.first(c) : T, g1 = c < G ? split.first(c + 1) : T;
   if (g0 < g1 && (incl - mine) * groups <= g0 && g0 < incl * groups) {  // one thread
     int64_t rem = g0 - (incl - mine) * groups;
-    int b = sb0;
-    for (;; ++b) {
+    for (int b = sb0;; ++b) {
       int n, lo;
-      att_visible<KT>(a, b, n, lo);
+      att_visible(a, b, n, lo);
       const int64_t nt = att_tiles<KT>(n, lo), all = nt * groups;
       if (rem < all) {
         s_start[0] = b;
-        s_start[1] = (int)(rem / nt);
-        s_start[2] = (int)(rem % nt);
+        s_start[1] = (int)att_div(rem, nt);
+        s_start[2] = (int)(rem - s_start[1] * nt);
         break;
       }
       rem -= all;
     }
   }
-  // rows of empty sequences
-  for (int b = blockIdx.x; b < a.sequences; b += gridDim.x) {
-    int n, lo;
-    att_visible<KT>(a, b, n, lo);
-    if (n > 0) continue;
-    uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (int64_t)b * a.q_heads * D);
-    for (int i = tid; i < a.q_heads * D / 8; i += kAttThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (a.lse)
-      for (int i = tid; i < a.q_heads; i += kAttThreads) a.lse[(int64_t)b * a.q_heads + i] = -INFINITY;
-  }
   __syncthreads();
-  if (g0 >= g1) return;
 
   AttSeg seg;
-  seg.b = s_start[0];
-  seg.hg = s_start[1];
-  att_segment<KT>(a, seg, s_start[2], g1 - g0);
+  if (g0 < g1) {
+    seg.b = s_start[0];
+    seg.hg = s_start[1];
+    att_visible(a, seg.b, seg.n, seg.lo);
+    seg.total = att_tiles<KT>(seg.n, seg.lo);
+    att_segment<KT>(seg, s_start[2], g1 - g0);
+  }
 
-  // ---- the ring: `ahead` is the segment of the next tile to request, `at` that tile
-  const int piece = 1 << p.piece_shift, pp = KT >> p.piece_shift;  // pieces (pages) per tile: 1, 2 or 4
-  const int page_mask = (1 << a.kv.page_shift) - 1;
-  AttSeg ahead = seg;
-  int at = ahead.first + warp, ids_base = 0, ids = -1;  // this lane's page number, for tiles from ids_base on
-  bool more = true, fresh = true;
-  int issued = 0;
-  auto request = [&]() {  // the warp's next tile into stage issued % S
-    while (at >= ahead.first + ahead.count) {
-      if (ahead.left == 0) {
-        more = false;
-        return;
+  if (warp == kAttWarps) {
+    // ---- loads: tile i of the CTA goes to consumer i % 4, stage (i / 4) % S
+    int issued = 0;  // tiles
+    if (g0 < g1) {
+      const int piece = 1 << p.piece_shift, pp = KT >> p.piece_shift;  // pieces (pages) per tile: 1, 2 or 4
+      const int page_mask = (1 << a.kv.page_shift) - 1;
+      int ids_b = -1, ids_base = 0, ids = -1;  // this lane's page number, for tiles of ids_b from ids_base on
+      int stage = 0, slot = 0;                 // of the next tile: round of the rings, ring
+      uint32_t empty_ph = 1u, q_ph = 1u;       // parities to wait for (an untouched stage is empty)
+      bool ok = true;
+      for (int k = 0; ok; ++k) {  // segments
+        const int kh = seg.hg / p.blocks, h0 = kh * group + (seg.hg % p.blocks) * C::kHeads;
+        const int heads = min(C::kHeads, (kh + 1) * group - h0);
+        if (!att_wait(att_smem(&q_empty[k & 1]), q_ph, kAttTries)) break;
+        if (k & 1) q_ph ^= 1u;
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + seg.b * a.q_stride + (int64_t)h0 * D;
+        const uint32_t q_bar = att_smem(&q_full[k & 1]);
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(q_bar), "r"(heads * D * 2) : "memory");
+        __syncwarp();
+        if (lane < heads)
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                       ::"r"(qs_smem + (k & 1) * C::kQ + lane * C::kQRow), "l"(q + (int64_t)lane * D), "r"(D * 2), "r"(q_bar)
+                       : "memory");
+        for (int t = seg.first; t < seg.first + seg.count; ++t) {
+          if (ids_b != seg.b || t < ids_base || t >= ids_base + 32 / pp) {  // page numbers of 32 / pp tiles, a lane each
+            ids_b = seg.b;
+            ids_base = t;
+            const int tok = (t + lane / pp) * KT + (lane % pp) * piece;
+            ids = tok < seg.n ? __ldg(a.kv.table + seg.b * a.kv.table_stride + (tok >> a.kv.page_shift)) : -1;
+          }
+          const int t0 = t * KT, pieces = min(pp, (seg.n - t0 + piece - 1) >> p.piece_shift);
+          int page[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) page[j] = __shfl_sync(0xFFFFFFFFu, ids, ((t - ids_base) * pp + j) & 31);
+          const int at = slot * S + stage;
+          if (!att_wait(att_smem(&empty[at]), empty_ph, kAttTries)) {
+            ok = false;
+            break;
+          }
+          if (att_elect()) {
+            const uint32_t mb = att_smem(&full[at]), dst = base + at * C::kTile;
+            const int y = (kh << a.kv.page_shift) + (t0 & page_mask);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                         ::"r"(mb), "r"(2 * pieces * piece * C::kRow) : "memory");
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < pieces) {
+                // (pieces of a tile are whole pages, except where a page holds the whole tile)
+                const int yj = pp == 1 ? y : kh << a.kv.page_shift;
+#pragma unroll
+                for (int x = 0; x < 2 * C::kBoxes; ++x) {
+                  const int kind = x / C::kBoxes, box = x % C::kBoxes;
+                  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                               " [%0], [%1, {%2, %3, %4}], [%5];"
+                               ::"r"(dst + kind * C::kHalf + box * (KT * C::kBoxRow) + j * piece * C::kBoxRow),
+                                 "l"(kind ? &vmap : &kmap), "r"(box * (C::kBoxRow / C::kElem)), "r"(yj), "r"(page[j]), "r"(mb)
+                               : "memory");
+                }
+              }
+          }
+          __syncwarp();
+          ++issued;
+          if (++slot == kAttWarps) {
+            slot = 0;
+            if (++stage == S) {
+              stage = 0;
+              empty_ph ^= 1u;
+            }
+          }
+        }
+        if (seg.left == 0) break;
+        att_next<KT>(a, seg, groups);
       }
-      att_next<KT>(a, ahead, groups);
-      at = ahead.first + warp;
-      fresh = true;
     }
-    if (fresh || at >= ids_base + kAttWarps * (32 / pp)) {  // page numbers of the next 32 / pp tiles, a lane each
-      ids_base = at;
-      const int tok = (at + kAttWarps * (lane / pp)) * KT + (lane % pp) * piece;
-      ids = tok < ahead.n ? __ldg(a.kv.table + ahead.b * a.kv.table_stride + (tok >> a.kv.page_shift)) : -1;
-      fresh = false;
-    }
-    const int t0 = at * KT, slot = (at - ids_base) / kAttWarps * pp;
-    const int pieces = min(pp, (ahead.n - t0 + piece - 1) >> p.piece_shift);
-    const uint32_t mb = bars + 8 * (issued % S), dst = ring + (issued % S) * C::kTile;
-    if (lane == 0)
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                   ::"r"(mb), "r"(2 * pieces * piece * C::kRow) : "memory");
-    // lane: piece, then box, then keys or values
-    const int my_piece = lane % pp, my_box = lane / pp % C::kBoxes, kind = lane / pp / C::kBoxes;
-    const int page = __shfl_sync(0xFFFFFFFFu, ids, slot + my_piece);
-    if (kind < 2 && my_piece < pieces) {
-      const int kh = ahead.hg / p.blocks;
-      const int y = (kh << a.kv.page_shift) + ((t0 + my_piece * piece) & page_mask);
-      const uint32_t to = dst + kind * C::kHalf + my_box * (KT * C::kBoxRow) + my_piece * piece * C::kBoxRow;
-      asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                   " [%0], [%1, {%2, %3, %4}], [%5];"
-                   ::"r"(to), "l"(kind ? &vmap : &kmap), "r"(my_box * (C::kBoxRow / C::kElem)), "r"(y), "r"(page), "r"(mb)
-                   : "memory");
-    }
-    ++issued;
-    at += kAttWarps;
-  };
-  for (int s = 0; s < S && more; ++s) request();
+    __syncthreads();  // the consumers are done
+    if (s_fail)       // copies that nothing waited for: let them land
+      for (int i = max(0, issued - kAttWarps * S); i < issued; ++i)
+        att_wait(att_smem(&full[i % kAttWarps * S + i / kAttWarps % S]), (uint32_t)(i / kAttWarps / S) & 1u, kAttTries);
+    return;
+  }
 
-  int done = 0;      // tiles consumed
-  bool bad = false;  // a copy did not arrive
+  // ---- rows of empty sequences
+  for (int b = blockIdx.x; b < a.sequences; b += gridDim.x) {
+    int n, lo;
+    att_visible(a, b, n, lo);
+    if (n > 0) continue;
+    uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (int64_t)b * a.q_heads * D);
+    for (int i = tid; i < a.q_heads * D / 8; i += kAttConsumers) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse)
+      for (int i = tid; i < a.q_heads; i += kAttConsumers) a.lse[(int64_t)b * a.q_heads + i] = -INFINITY;
+  }
+  AttShared shared = {0, 0, 0};
+  if (g0 >= g1) {
+    if (tid == 0) p.shared[c] = shared;
+    __syncthreads();
+    return;
+  }
+
+  int i0 = 0;               // the segment's first tile among the CTA's
+  int stage = 0;            // of this warp's next tile
+  uint32_t full_ph = 0u;
+  bool bad = false;         // a copy did not arrive in time: this warp's sums become NaN
+  bool dead = false;        // nor later: nothing is waited for or handed back any more
+  int tries = p.a.first_tries >= 0 && warp == 0 ? p.a.first_tries : kAttTries;
   // ldmatrix rows and chunks of this lane
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchk = lane >> 4;
   const int vrow = E4M3 ? krow : (lane & 7) + ((lane >> 4) & 1) * 8, vchk = E4M3 ? kchk : (lane >> 3) & 1;
@@ -340,27 +435,31 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
     return (uint32_t)((ch / kPer) * (KT * C::kBoxRow) + row * C::kBoxRow + (((ch % kPer) ^ sw) << 4));
   };
 
-  for (;;) {
+  for (int k = 0;; ++k) {
     const int kh = seg.hg / p.blocks, h0 = kh * group + (seg.hg % p.blocks) * C::kHeads;
     const int heads = min(C::kHeads, (kh + 1) * group - h0);
     const float sc = a.scale * (E4M3 && a.kv.k_scale ? __ldg(a.kv.k_scale + kh) : 1.0f) * 1.4426950408889634f;
 
     // ---- q as the B side: this lane's head is 8 nt + lane / 4
+    if (!dead && !__all_sync(0xFFFFFFFFu, att_wait(att_smem(&q_full[k & 1]), (uint32_t)(k >> 1) & 1u, kAttTries)))
+      bad = dead = true;
     uint32_t qf[NT][KS][2];
     float qs[NT][2];  // factor of the scores of heads 8 nt + 2 (lane % 4) + j
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int h = 8 * nt + (lane >> 2);
-      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + seg.b * a.q_stride + (int64_t)(h0 + h) * D;
+      // (rows past the last head hold anything: their columns of S^T and O^T are not used)
+      const uint32_t qrow = qs_smem + (k & 1) * C::kQ + (8 * nt + (lane & 7)) * C::kQRow;
+      if (E4M3) {  // dimensions 4c .. 4c + 3 of the step: the order in which ldmatrix hands out bytes
+        const uint32_t at = qs_smem + (k & 1) * C::kQ + (8 * nt + (lane >> 2)) * C::kQRow + 8 * (lane & 3);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (E4M3) {  // dimensions 4c .. 4c + 3 of the step: the order in which ldmatrix hands out bytes
-          const uint2 v = h < heads ? __ldg(reinterpret_cast<const uint2 *>(q + 16 * ks) + (lane & 3)) : make_uint2(0u, 0u);
-          qf[nt][ks][0] = v.x;
-          qf[nt][ks][1] = v.y;
-        } else {
-          qf[nt][ks][0] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks) + (lane & 3)) : 0u;
-          qf[nt][ks][1] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks + 8) + (lane & 3)) : 0u;
+        for (int ks = 0; ks < KS; ++ks)
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(qf[nt][ks][0]), "=r"(qf[nt][ks][1]) : "r"(at + 32 * ks));
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+          uint32_t r[4];
+          ldsm4<false>(qrow + 32 * ks + 16 * (lane >> 3), r);
+          qf[nt][ks][0] = r[0], qf[nt][ks][1] = r[1], qf[nt][ks + 1][0] = r[2], qf[nt][ks + 1][1] = r[3];
         }
       }
       qs[nt][0] = qs[nt][1] = sc;
@@ -393,6 +492,10 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
       }
     }
 
+    __syncwarp();
+    if (lane == 0 && !dead)
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&q_empty[k & 1])) : "memory");
+
     float o[NT][KS][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -404,10 +507,14 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
         for (int j = 0; j < 4; ++j) o[nt][d][j] = 0.0f;
     }
 
-    for (int t = seg.first + warp; t < seg.first + seg.count; t += kAttWarps) {
-      const int st = done % S;
-      if (!bad) bad = !__all_sync(0xFFFFFFFFu, att_wait(bars + 8 * st, (uint32_t)(done / S) & 1u, kAttTries));
-      const uint32_t kb = ring + st * C::kTile, vb = kb + C::kHalf;
+    for (int t = seg.first + ((warp - i0) & (kAttWarps - 1)); t < seg.first + seg.count; t += kAttWarps) {
+      const int at = warp * S + stage;
+      if (!dead && !__all_sync(0xFFFFFFFFu, att_wait(att_smem(&full[at]), full_ph, tries))) {
+        bad = true;  // (a stage goes back only once its copy has landed)
+        dead = !__all_sync(0xFFFFFFFFu, att_wait(att_smem(&full[at]), full_ph, kAttTries));
+      }
+      tries = kAttTries;
+      const uint32_t kb = base + at * C::kTile, vb = kb + C::kHalf;
       const int t0 = t * KT;
       const bool edge = t0 < seg.lo || t0 + KT > seg.n;
       if (edge) {
@@ -540,14 +647,18 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
           }
         }
       }
-      ++done;
       __syncwarp();  // every lane has read the stage
-      if (more && !bad) request();
+      if (lane == 0 && !dead)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&empty[at])) : "memory");
+      if (++stage == S) {
+        stage = 0;
+        full_ph ^= 1u;
+      }
     }
 
-    // ---- the four warps' parts meet
+    // ---- the warps' parts meet: those of the segment's first tiles
     const int parts = min(kAttWarps, seg.count);
-    if (warp < parts) {
+    if (((warp - i0) & (kAttWarps - 1)) < parts) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -570,19 +681,20 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
           }
         }
     }
-    __syncthreads();
+    if (dead) s_fail = 1;
+    asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");
     const bool whole = seg.count == seg.total;
-    const int64_t item0 = g1 - seg.left - seg.count - seg.off;  // the item's first tile
     // parts of an item: the first in its CTA's slot 2c + 1, the others in their CTAs' slots 2c
     const int64_t slot = 2 * c + (seg.off == 0 ? 1 : 0);
     const float vs = E4M3 && a.kv.v_scale ? __ldg(a.kv.v_scale + kh) : 1.0f;
-    float *ml_all = p.part + (int64_t)2 * gridDim.x * C::kHeads * D;
-    for (int i = tid; i < heads * (D / 8); i += kAttThreads) {
+    float2 *ml_all = reinterpret_cast<float2 *>(p.part + (int64_t)2 * gridDim.x * C::kHeads * D);
+    for (int i = tid; i < heads * (D / 8); i += kAttConsumers) {
       const int h = i / (D / 8), d = i % (D / 8) * 8;
-      float mx = s_ml[0][h][0], sum = 0.0f, v[8] = {};
-      for (int w = 1; w < parts; ++w) mx = fmaxf(mx, s_ml[w][h][0]);
+      float mx = -INFINITY, sum = 0.0f, v[8] = {};
+      for (int j = 0; j < parts; ++j) mx = fmaxf(mx, s_ml[(i0 + j) & (kAttWarps - 1)][h][0]);
       const float ref = mx == -INFINITY ? 0.0f : mx;
-      for (int w = 0; w < parts; ++w) {
+      for (int j = 0; j < parts; ++j) {
+        const int w = (i0 + j) & (kAttWarps - 1);
         const float f = att_exp2(s_ml[w][h][0] - ref);
         sum += s_ml[w][h][1] * f;
         const float4 *x = reinterpret_cast<const float4 *>(red + (w * C::kHeads + h) * C::kRedStride + d);
@@ -597,59 +709,78 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
         for (int j = 0; j < 4; ++j) w[j] = pack16<false>(v[2 * j] * r, v[2 * j + 1] * r);
         const int64_t row = (int64_t)seg.b * a.q_heads + h0 + h;
         *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (d == 0 && a.lse) a.lse[row] = (ref - (E4M3 ? 14.0f : 0.0f) + log2f(sum)) * 0.69314718055994531f;
+        if (d == 0 && a.lse) a.lse[row] = att_lse<E4M3>(ref, sum);
       } else {
         float4 *to = reinterpret_cast<float4 *>(p.part + (slot * C::kHeads + h) * D + d);
-        __stcg(to, make_float4(v[0], v[1], v[2], v[3]));
-        __stcg(to + 1, make_float4(v[4], v[5], v[6], v[7]));
-        if (d == 0) __stcg(reinterpret_cast<float2 *>(ml_all) + slot * C::kHeads + h, make_float2(mx, sum));
+        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (d == 0) ml_all[slot * C::kHeads + h] = make_float2(mx, sum);
       }
     }
-    if (!whole) {
-      // ---- the parts of an item that several CTAs share
-      const int64_t c0 = ((item0 + 1) * G - 1) / T, c1 = ((item0 + seg.total) * G - 1) / T;
-      const int n = (int)(c1 - c0) + 1;
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        const uint32_t before = atomicAdd(p.count + c0, 1u);
-        s_last = before == (uint32_t)(n - 1);
-        if (s_last) p.count[c0] = 0u;  // as the next call wants it
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_last) {
-        const float2 *ml = reinterpret_cast<const float2 *>(ml_all);
-        auto slot_of = [&](int j) { return 2 * (c0 + j) + (j == 0 ? 1 : 0); };
-        for (int i = tid; i < heads * (D / 4); i += kAttThreads) {
-          const int h = i / (D / 4), d = i % (D / 4) * 4;
-          float mx = -INFINITY, sum = 0.0f;
-          for (int j = 0; j < n; ++j) mx = fmaxf(mx, __ldcg(&ml[slot_of(j) * C::kHeads + h]).x);
-          const float ref = mx == -INFINITY ? 0.0f : mx;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (int j = 0; j < n; ++j) {
-            const float2 e = __ldcg(&ml[slot_of(j) * C::kHeads + h]);
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(j) * C::kHeads + h) * D + d));
-            const float f = att_exp2(e.x - ref);
-            sum = fmaf(e.y, f, sum);
-            v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
-          }
-          const float r = sum == 0.0f ? 0.0f : vs / sum;
-          const int64_t row = (int64_t)seg.b * a.q_heads + h0 + h;
-          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) =
-              make_uint2(pack16<false>(v.x * r, v.y * r), pack16<false>(v.z * r, v.w * r));
-          if (d == 0 && a.lse) a.lse[row] = (ref - (E4M3 ? 14.0f : 0.0f) + log2f(sum)) * 0.69314718055994531f;
-        }
-      }
+    if (!whole && seg.off == 0) {  // this CTA holds the item's first part: the range's last segment
+      shared.row = (int64_t)seg.b * a.q_heads + h0;
+      shared.heads = heads;
+      shared.parts = split.cta_of(g1 - seg.count + seg.total - 1) - c + 1;
     }
     if (seg.left == 0) break;
+    i0 += seg.count;
     att_next<KT>(a, seg, groups);
-    __syncthreads();  // red and s_ml are free again
+    asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");  // red and s_ml are free again
   }
-  // copies requested but not waited for (after a failure only): let them land
-  if (bad)
-    for (int i = done; i < issued; ++i) att_wait(bars + 8 * (i % S), (uint32_t)(i / S) & 1u, kAttTries);
+  if (tid == 0) p.shared[c] = shared;
+  __syncthreads();
+}
+
+// Adds the parts of the items that several CTAs share, in CTA order; block c
+// has the one that begins in CTA c, if any.
+constexpr int kAttJoinThreads = 256;
+template <bool E4M3>
+__global__ void __launch_bounds__(kAttJoinThreads) k_attend_join(const __grid_constant__ AttLaunch p, int D, int heads, int grid) {
+  pdl_wait();
+  const int c = blockIdx.x;
+  const AttShared it = p.shared[c];
+  if (it.parts == 0) return;
+  const AttendArgs &a = p.a;
+  const float2 *ml = reinterpret_cast<const float2 *>(p.part + (int64_t)2 * grid * heads * D);
+  auto slot_of = [&](int j) { return (int64_t)(2 * (c + j) + (j == 0 ? 1 : 0)); };
+  const int kh = (int)(it.row % a.q_heads) / (a.q_heads / a.kv.kv_heads);
+  const float vs = E4M3 && a.kv.v_scale ? __ldg(a.kv.v_scale + kh) : 1.0f;
+  for (int i = threadIdx.x; i < it.heads * (D / 4); i += kAttJoinThreads) {
+    const int h = i / (D / 4), d = i % (D / 4) * 4;
+    // one pass with a running maximum, eight parts in flight
+    float mx = -INFINITY, sum = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j0 = 0; j0 < it.parts; j0 += 8) {
+      float2 e[8];
+      float4 x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = j0 + j < it.parts;
+        const int64_t s = slot_of(in ? j0 + j : 0) * heads + h;
+        e[j] = in ? ml[s] : make_float2(-INFINITY, 0.0f);
+        x[j] = *reinterpret_cast<const float4 *>(p.part + s * D + d);
+      }
+      float top = mx;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, e[j].x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float f0 = att_exp2(mx - ref);
+      sum *= f0, v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < it.parts) {
+          const float f = att_exp2(e[j].x - ref);
+          sum = fmaf(e[j].y, f, sum);
+          v.x = fmaf(x[j].x, f, v.x), v.y = fmaf(x[j].y, f, v.y), v.z = fmaf(x[j].z, f, v.z), v.w = fmaf(x[j].w, f, v.w);
+        }
+      mx = top;
+    }
+    const float ref = mx == -INFINITY ? 0.0f : mx, r = sum == 0.0f ? 0.0f : vs / sum;
+    const int64_t row = it.row + h;
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) =
+        make_uint2(pack16<false>(v.x * r, v.y * r), pack16<false>(v.z * r, v.w * r));
+    if (d == 0 && a.lse) a.lse[row] = att_lse<E4M3>(ref, sum);
+  }
 }
 
 namespace {
@@ -722,8 +853,8 @@ struct AttRun {
     const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, a.window + C::KT) : cap;
     const int64_t tiles = (seen / C::KT + 1) * a.sequences * a.kv.kv_heads * p.blocks;
     const int grid = (int)std::min<int64_t>(grid_max, (tiles + kAttMinTiles - 1) / kAttMinTiles);
-    p.count = static_cast<uint32_t *>(ws);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
+    p.shared = static_cast<AttShared *>(ws);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + kAttMaxCtas * sizeof(AttShared));
     CUtensorMap m[2];
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.kv.kv_heads << a.kv.page_shift, (cuuint64_t)a.kv.pages};
     const cuuint32_t box[3] = {(cuuint32_t)(C::kBoxRow / C::kElem), (cuuint32_t)piece, 1u}, es[3] = {1u, 1u, 1u};
@@ -737,7 +868,19 @@ struct AttRun {
         return cudaErrorInvalidValue;
     }
     k_attend<D, E4M3, NT><<<grid, kAttThreads, C::kSmem, st>>>(m[0], m[1], p);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    // the parts of split items; one CTA, or a CTA for every item's tiles, splits none
+    if (e != cudaSuccess || grid == 1) return e;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kAttJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attend_join<E4M3>, p, D, C::kHeads, grid);
   }
 };
 
@@ -746,7 +889,7 @@ struct AttRun {
 size_t attend_workspace_bytes(const KvArgs &kv, int q_heads, int sms) {
   const int nt = att_nt(kv.head_dim, q_heads / kv.kv_heads);
   const size_t grid = (size_t)att_dispatch(kv.head_dim, kv.e4m3, nt, AttGrid{sms});
-  return kCounterBytes + 2 * grid * 8 * nt * (kv.head_dim + 2) * sizeof(float);
+  return kAttMaxCtas * sizeof(AttShared) + 2 * grid * 8 * nt * (kv.head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_attend(const AttendArgs &a, int sms, void *ws, cudaStream_t st) {

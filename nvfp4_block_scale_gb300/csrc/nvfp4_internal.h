@@ -129,6 +129,7 @@ struct AttendArgs {
   int64_t window;
   void *out;
   float *lse;
+  int first_tries;  // < 0: normal (test hook)
 };
 size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
 cudaError_t prepare_linear_kernels();
