@@ -223,12 +223,11 @@ int nvfp4_gemm(const uint8_t *codes, const uint8_t *scales, const float *alpha, 
  *   y      device, bf16, 2-byte aligned, [batch, rows] with rows y_stride
  *          elements apart (>= rows).  y may be the residual or the gate
  *          itself (same address and stride).
- *   workspace  device, 256-byte aligned, nvfp4_linear_workspace_bytes(rows,
- *          cols, batch) bytes, or NULL: then the library's pool provides it.
- *          A caller's workspace must be all zero before its first use; each
- *          call leaves it ready for the next one of any shape that it is
- *          large enough for.  Calls that may overlap on the GPU need
- *          workspaces of their own.
+ *   workspace  device, 256-byte aligned, of workspace_bytes >=
+ *          nvfp4_linear_workspace_bytes(rows, cols, batch) bytes, or NULL:
+ *          then the library's pool provides it.  A caller's workspace needs no
+ *          preparation and holds nothing from one call to the next; calls that
+ *          may overlap on the GPU need workspaces of their own.
  *   stream cudaStream_t.
  * Returns an nvfp4_status.  nvfp4_linear_workspace_bytes returns -1 for an
  * invalid shape or without a supported device.
@@ -252,7 +251,7 @@ int64_t nvfp4_linear_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
 int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows,
                  int64_t cols, const void *x, int64_t x_stride, int64_t batch,
                  const nvfp4_epilogue *epilogue, void *y, int64_t y_stride, void *workspace,
-                 cudaStream_t stream);
+                 int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * A paged key-value cache: `pages` pages of page_size tokens; page p holds
@@ -352,8 +351,9 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const void *qkv, int qkv_dtype,
  *           (written).
  *   lse     device, fp32, 4-byte aligned, [sequences][q_heads] (written), or
  *           NULL.
- *   workspace  as for nvfp4_linear, nvfp4_paged_attention_workspace_bytes(
- *           cache, q_heads) bytes whatever the sequences and lengths; or NULL.
+ *   workspace, workspace_bytes  as for nvfp4_linear,
+ *           nvfp4_paged_attention_workspace_bytes(cache, q_heads) bytes
+ *           whatever the sequences and lengths; or NULL.
  * Returns an nvfp4_status.  Stored keys and values behind a sequence's length
  * may hold anything.  Every wait inside the kernel is bounded: should a copy
  * never complete, the affected outputs are NaN.
@@ -363,7 +363,7 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
                           int64_t sequences, int q_heads, const int32_t *lengths,
                           const int32_t *table, int64_t table_width, int64_t table_stride,
                           float scale, int64_t window, void *out, float *lse, void *workspace,
-                          cudaStream_t stream);
+                          int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * nvfp4_swizzle_scales -- the E4M3 block scales of a quantized [rows, cols]

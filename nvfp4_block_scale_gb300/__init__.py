@@ -29,6 +29,7 @@ ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_G
 DTYPE_BF16, DTYPE_FP32, DTYPE_E4M3 = 0, 1, 2
 
 _lib = None
+_raw_stream = None
 
 
 class nvfp4_epilogue(ctypes.Structure):
@@ -59,7 +60,7 @@ class Nvfp4Error(RuntimeError):
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Loads the CUDA library (building it first if it is absent or stale)."""
-    global _lib
+    global _lib, _raw_stream
     if _lib is not None:
         return _lib
     if path is None:
@@ -84,7 +85,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_gemm.restype = ci
     L.nvfp4_linear_workspace_bytes.argtypes = [i64, i64, i64]
     L.nvfp4_linear_workspace_bytes.restype = i64
-    L.nvfp4_linear.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, ctypes.POINTER(nvfp4_epilogue), vp, i64, vp, vp]
+    L.nvfp4_linear.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, ctypes.POINTER(nvfp4_epilogue), vp, i64, vp, i64, vp]
     L.nvfp4_linear.restype = ci
     L.nvfp4_kv_append.argtypes = [ctypes.POINTER(nvfp4_kv_cache), vp, ci, i64, i64, ci, vp, vp, vp, i64, i64, i64,
                                   vp, i64, ci, ci, vp, vp]
@@ -92,7 +93,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_paged_attention_workspace_bytes.argtypes = [ctypes.POINTER(nvfp4_kv_cache), ci]
     L.nvfp4_paged_attention_workspace_bytes.restype = i64
     L.nvfp4_paged_attention.argtypes = [ctypes.POINTER(nvfp4_kv_cache), vp, i64, i64, ci, vp, vp, i64, i64,
-                                        ctypes.c_float, i64, vp, vp, vp, vp]
+                                        ctypes.c_float, i64, vp, vp, vp, i64, vp]
     L.nvfp4_paged_attention.restype = ci
     L.nvfp4_swizzled_scales_bytes.argtypes = [i64, i64]
     L.nvfp4_swizzled_scales_bytes.restype = i64
@@ -123,6 +124,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_check_selftest.restype = ci
     L.nvfp4_status_string.argtypes = [ci]
     L.nvfp4_status_string.restype = ctypes.c_char_p
+    _raw_stream = _current_raw()
     _lib = L
     return L
 
@@ -171,10 +173,10 @@ def nvfp4_linear_workspace_bytes(rows, cols, batch) -> int:
 
 
 def nvfp4_linear(codes, scales, alpha, rows, cols, x, x_stride, batch, epilogue, y, y_stride, workspace,
-                 stream) -> int:
+                 workspace_bytes, stream) -> int:
     """`epilogue`: an nvfp4_epilogue (passed by reference) or None."""
     return load().nvfp4_linear(codes, scales, alpha, rows, cols, x, x_stride, batch, epilogue, y, y_stride,
-                               workspace, stream)
+                               workspace, workspace_bytes, stream)
 
 
 def nvfp4_kv_append(cache, qkv, qkv_dtype, qkv_stride, tokens, q_heads, seq, pos, table, sequences, table_width,
@@ -190,9 +192,9 @@ def nvfp4_paged_attention_workspace_bytes(cache, q_heads) -> int:
 
 
 def nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table, table_width, table_stride, scale,
-                          window, out, lse, workspace, stream) -> int:
+                          window, out, lse, workspace, workspace_bytes, stream) -> int:
     return load().nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table, table_width,
-                                        table_stride, scale, window, out, lse, workspace, stream)
+                                        table_stride, scale, window, out, lse, workspace, workspace_bytes, stream)
 
 
 def nvfp4_swizzled_scales_bytes(rows, cols) -> int:
@@ -416,36 +418,54 @@ def gemm(codes, scales, alpha, rows: int, cols: int, x, out=None, stream=None):
     return y
 
 
-def _on(stream, *tensors):
+def _on(device, stream, *made):
     """The stream to launch on; tensors made here for a stream other than the
     current one are kept from reuse until that stream has passed this point."""
     import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    for t in tensors:
+        return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
+    for t in made:
         if t is not None:
             t.record_stream(stream)
     return stream.cuda_stream
 
 
+def _current_raw():
+    # the current stream's handle without making a Stream object: 0.1 us instead of 3
+    try:
+        from torch._C import _cuda_getCurrentRawStream
+        return _cuda_getCurrentRawStream
+    except ImportError:
+        return None
+
+
 def _workspace(nbytes: int, device):
-    """A zeroed workspace (zeroed on the current stream, like any new tensor)."""
     import torch
     if nbytes < 0:
         raise ValueError("invalid shape, or no supported device")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
+def _space(workspace):
+    """Address and size of a caller's workspace, or nothing."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("a workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _rows_of(t, batch: int, width: int, what: str):
     import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.shape != (batch, width) or (width > 1 and t.stride(1) != 1):
+    strides = t.stride()
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.shape != (batch, width) or (width > 1 and strides[1] != 1):
         raise ValueError(f"{what} must be a bf16 CUDA tensor [{batch}, {width}] with contiguous rows")
-    return t.data_ptr(), t.stride(0) if batch > 1 and width > 0 else 8 * ((width + 7) // 8)
+    return t.data_ptr(), strides[0] if batch > 1 and width > 0 else (width + 7) // 8 * 8
 
 
 def linear_workspace(rows: int, cols: int, batch: int, device="cuda"):
-    """A workspace for linear() of this shape or smaller batches, kept by the
-    caller from call to call (one per stream that such calls run on)."""
+    """A workspace for linear() of this shape, kept by the caller from call to
+    call (one per stream that such calls run on)."""
     return _workspace(nvfp4_linear_workspace_bytes(rows, cols, batch), device)
 
 
@@ -453,9 +473,10 @@ def linear(codes, scales, alpha, rows: int, cols: int, x, bias=None, activation=
            out=None, workspace=None, stream=None):
     """The W4A16 product with its epilogue: bf16 y [batch, rows] =
     residual + gate * activation(W x + bias), W = q * Delta * alpha, for bf16 x
-    [batch, cols]; bias [rows], gate and residual [batch, rows] bf16 or None.
-    x, gate, residual and out may have rows further apart than their width;
-    out may be the residual.  See nvfp4_linear in include/nvfp4.h."""
+    [batch, cols]; bias [rows], gate and residual [batch, rows] bf16 or None;
+    activation: None, "relu", "gelu", "gelu_tanh" or "silu".  x, gate, residual
+    and out may have rows further apart than their width; out may be the
+    residual.  See nvfp4_linear in include/nvfp4.h."""
     import torch
     if x.dim() == 1:
         x = x.unsqueeze(0)
@@ -466,25 +487,24 @@ def linear(codes, scales, alpha, rows: int, cols: int, x, bias=None, activation=
         raise ValueError("codes and scales must be contiguous and hold [rows, cols] elements")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)}")
-    ep = nvfp4_epilogue(activation=ACTIVATIONS[activation])
+    bp = gp = rp = None
+    gs = rs = 0
     if bias is not None:
-        if bias.dtype != torch.bfloat16 or not bias.is_cuda or bias.shape != (rows,) or not bias.is_contiguous():
+        if bias.dtype is not torch.bfloat16 or not bias.is_cuda or bias.shape != (rows,) or not bias.is_contiguous():
             raise ValueError("bias must be a contiguous bf16 CUDA tensor [rows]")
-        ep.bias = bias.data_ptr()
+        bp = bias.data_ptr()
     if gate is not None:
-        ep.gate, ep.gate_stride = _rows_of(gate, batch, rows, "gate")
+        gp, gs = _rows_of(gate, batch, rows, "gate")
     if residual is not None:
-        ep.residual, ep.residual_stride = _rows_of(residual, batch, rows, "residual")
+        rp, rs = _rows_of(residual, batch, rows, "residual")
     made = None
     if out is None:
         out = made = torch.empty((batch, rows), dtype=torch.bfloat16, device=x.device)
     yp, ys = _rows_of(out, batch, rows, "out")
-    if workspace is not None and (not workspace.is_cuda or
-                                  workspace.nbytes < nvfp4_linear_workspace_bytes(rows, cols, batch)):
-        raise ValueError("workspace too small: make it with linear_workspace(rows, cols, batch)")
-    _check(nvfp4_linear(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, xp, xs, batch,
-                        ctypes.byref(ep), yp, ys, None if workspace is None else workspace.data_ptr(),
-                        _on(stream, made)), "nvfp4_linear")
+    wp, wb = _space(workspace)
+    ep = nvfp4_epilogue(bp, gp, gs, rp, rs, ACTIVATIONS[activation])
+    _check((_lib or load()).nvfp4_linear(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, xp, xs, batch,
+                                         ep, yp, ys, wp, wb, _on(x.device, stream, made)), "nvfp4_linear")
     return out
 
 
@@ -512,6 +532,7 @@ class KVCache:
                 raise ValueError("scales are for E4M3 caches: contiguous fp32 CUDA tensors [kv_heads]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, dim
+        self.device = k.device
         page = heads * size * dim
         self.desc = nvfp4_kv_cache(k.data_ptr(), v.data_ptr(), k.stride(0) if pages > 1 else page,
                                    v.stride(0) if pages > 1 else page, pages, size, heads, dim, kinds[k.dtype],
@@ -528,20 +549,22 @@ class KVCache:
         return cls(make(), make(), k_scale, v_scale)
 
 
-def _ints(t, shape, what: str):
+def _ints(t, n: int, what: str):
     import torch
-    if t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 CUDA tensor {list(shape)}")
+    if t.dtype is not torch.int32 or not t.is_cuda or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 CUDA tensor [{n}]")
     return t.data_ptr()
 
 
 def _table_of(table):
     import torch
-    if table.dtype != torch.int32 or not table.is_cuda or table.dim() != 2 or \
-            (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("table must be an int32 CUDA tensor [sequences, pages of a sequence] with contiguous rows")
+    if table.dtype is not torch.int32 or not table.is_cuda or table.dim() != 2:
+        raise ValueError("table must be an int32 CUDA tensor [sequences, pages of a sequence]")
     n, width = table.shape
-    return table.data_ptr(), n, width, table.stride(0) if n > 1 else width
+    step, one = table.stride()
+    if one != 1 and width > 1:
+        raise ValueError("table must have contiguous rows")
+    return table.data_ptr(), n, width, step if n > 1 else width
 
 
 def kv_append(cache: KVCache, qkv, q_heads: int, seq, pos, table, cos_sin=None, interleaved: bool = False, out=None,
@@ -553,34 +576,37 @@ def kv_append(cache: KVCache, qkv, q_heads: int, seq, pos, table, cos_sin=None, 
     [sequences, pages]; cos_sin: fp32 [positions, rotary_dim], cosines then
     sines (None: no rotation).  See nvfp4_kv_append in include/nvfp4.h."""
     import torch
-    width = (q_heads + 2 * cache.kv_heads) * cache.head_dim
-    if qkv.dtype not in (torch.bfloat16, torch.float32) or not qkv.is_cuda or qkv.dim() != 2 or \
+    dim = cache.head_dim
+    width = (q_heads + 2 * cache.kv_heads) * dim
+    kind = qkv.dtype
+    if (kind is not torch.bfloat16 and kind is not torch.float32) or not qkv.is_cuda or qkv.dim() != 2 or \
             qkv.shape[1] != width or qkv.stride(1) != 1:
         raise ValueError(f"qkv must be a bf16 or fp32 CUDA tensor [tokens, {width}] with contiguous rows")
     tokens = qkv.shape[0]
-    sp, pp = _ints(seq, (tokens,), "seq"), _ints(pos, (tokens,), "pos")
+    sp, pp = _ints(seq, tokens, "seq"), _ints(pos, tokens, "pos")
     tp, sequences, pages, stride = _table_of(table)
-    positions = rotary = 0
+    cp, positions, rotary = None, 0, 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        if cos_sin.dtype is not torch.float32 or not cos_sin.is_cuda or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
         positions, rotary = cos_sin.shape
-    shape, made = (tokens, q_heads, cache.head_dim), None
+        cp = cos_sin.data_ptr()
+    shape, made = (tokens, q_heads, dim), None
     if out is None:
-        out = made = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
-    elif out.dtype != torch.bfloat16 or not out.is_cuda or out.shape != shape or not out.is_contiguous():
+        out = made = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    elif out.dtype is not torch.bfloat16 or not out.is_cuda or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bf16 CUDA tensor {list(shape)}")
-    _check(nvfp4_kv_append(cache.desc, qkv.data_ptr(), DTYPE_FP32 if qkv.dtype == torch.float32 else DTYPE_BF16,
-                           qkv.stride(0) if tokens > 1 else width, tokens, q_heads, sp, pp, tp, sequences, pages,
-                           stride, None if cos_sin is None else cos_sin.data_ptr(), positions, rotary,
-                           int(interleaved), out.data_ptr(), _on(stream, made)), "nvfp4_kv_append")
+    _check((_lib or load()).nvfp4_kv_append(cache.desc, qkv.data_ptr(), DTYPE_FP32 if kind is torch.float32 else DTYPE_BF16,
+                                            qkv.stride(0) if tokens > 1 else width, tokens, q_heads, sp, pp, tp,
+                                            sequences, pages, stride, cp, positions, rotary, bool(interleaved),
+                                            out.data_ptr(), _on(cache.device, stream, made)), "nvfp4_kv_append")
     return out
 
 
 def attention_workspace(cache: KVCache, q_heads: int):
     """A workspace for paged_attention() over this cache, whatever the batch
     and the lengths, kept by the caller from call to call (one per stream)."""
-    return _workspace(nvfp4_paged_attention_workspace_bytes(cache.desc, q_heads), cache.k.device)
+    return _workspace(nvfp4_paged_attention_workspace_bytes(cache.desc, q_heads), cache.device)
 
 
 def paged_attention(cache: KVCache, q, table, lengths, scale=None, window: int = 0, out=None, return_lse: bool = False,
@@ -592,29 +618,27 @@ def paged_attention(cache: KVCache, q, table, lengths, scale=None, window: int =
     all); scale: head_dim ** -0.5 by default.  See nvfp4_paged_attention in
     include/nvfp4.h."""
     import torch
-    if q.dtype != torch.bfloat16 or not q.is_cuda or q.dim() != 3 or q.shape[2] != cache.head_dim or \
-            q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != cache.head_dim):
+    shape, strides, dim = q.shape, q.stride(), cache.head_dim
+    if q.dtype is not torch.bfloat16 or not q.is_cuda or len(shape) != 3 or shape[2] != dim or strides[2] != 1 or \
+            (shape[1] > 1 and strides[1] != dim):
         raise ValueError("q must be a bf16 CUDA tensor [sequences, q_heads, head_dim] with contiguous sequences")
-    n, heads, dim = q.shape
+    n, heads, _ = shape
     tp, sequences, pages, stride = _table_of(table)
     if sequences != n:
         raise ValueError("table must have one row per sequence")
-    lp = _ints(lengths, (n,), "lengths")
+    lp = _ints(lengths, n, "lengths")
     made = lse = None
     if out is None:
-        out = made = torch.empty((n, heads, dim), dtype=torch.bfloat16, device=q.device)
-    elif out.dtype != torch.bfloat16 or not out.is_cuda or out.shape != q.shape or not out.is_contiguous():
+        out = made = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    elif out.dtype is not torch.bfloat16 or not out.is_cuda or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 CUDA tensor shaped like q")
     if return_lse:
-        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
-    if workspace is not None and (not workspace.is_cuda or
-                                  workspace.nbytes < nvfp4_paged_attention_workspace_bytes(cache.desc, heads)):
-        raise ValueError("workspace too small: make it with attention_workspace(cache, q_heads)")
-    _check(nvfp4_paged_attention(cache.desc, q.data_ptr(), q.stride(0) if n > 1 else heads * dim, n, heads, lp, tp,
-                                 pages, stride, dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                                 None if lse is None else lse.data_ptr(),
-                                 None if workspace is None else workspace.data_ptr(), _on(stream, made, lse)),
-           "nvfp4_paged_attention")
+        lse = torch.empty((n, heads), dtype=torch.float32, device=cache.device)
+    wp, wb = _space(workspace)
+    _check((_lib or load()).nvfp4_paged_attention(
+        cache.desc, q.data_ptr(), strides[0] if n > 1 else heads * dim, n, heads, lp, tp, pages, stride,
+        dim ** -0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wb,
+        _on(cache.device, stream, made, lse)), "nvfp4_paged_attention")
     return (out, lse) if return_lse else out
 
 

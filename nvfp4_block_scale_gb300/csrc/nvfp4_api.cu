@@ -225,13 +225,21 @@ int kv_table(KvArgs *a, const int32_t *table, int64_t sequences, int64_t width, 
   return NVFP4_OK;
 }
 
-// A product's or an attention's workspace begins with counters that every
-// call finds and leaves zero; a workspace from the pool gets them cleared.
-cudaError_t take_workspace(void **ws, size_t bytes, const DevInfo &d, cudaStream_t stream) {
-  if (bytes == 0) return cudaSuccess;
-  cudaError_t e = pool_alloc(ws, bytes, d.pool, stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(*ws, 0, std::min<size_t>(bytes, kCounterBytes), stream);
-  return e;
+// Workspace of a product: the full slices' and the last one's.
+size_t linear_need(int64_t rows, int64_t cols, int64_t batch, int sms) {
+  size_t need = linear_workspace_bytes(rows, cols, (int)std::min<int64_t>(batch, kLinearSlice), sms);
+  if (batch > kLinearSlice && batch % kLinearSlice)
+    need = std::max(need, linear_workspace_bytes(rows, cols, (int)(batch % kLinearSlice), sms));
+  return need;
+}
+
+// A call's workspace: the caller's, or one from the pool that *own names.
+int take_workspace(void **ws, void **own, int64_t given, size_t need, const DevInfo &d, cudaStream_t stream) {
+  if (*ws) return given >= 0 && (uint64_t)given >= need ? NVFP4_OK : NVFP4_ERR_INVALID_ARG;
+  if (need == 0) return NVFP4_OK;
+  const cudaError_t e = pool_alloc(own, need, d.pool, stream);
+  *ws = *own;
+  return map_cuda(e);
 }
 
 // ---------------------------------------------------------------------------
@@ -577,17 +585,12 @@ int64_t nvfp4_linear_workspace_bytes(int64_t rows, int64_t cols, int64_t batch) 
   if (check_shape(rows, cols) != NVFP4_OK || batch < 0) return -1;
   DevInfo *d = nullptr;
   if (device_info(&d) != NVFP4_OK) return -1;
-  if (rows == 0 || cols == 0 || batch == 0) return 0;
-  // the largest slice and the last one
-  size_t need = linear_workspace_bytes(rows, cols, (int)std::min<int64_t>(batch, kLinearSlice), d->sms);
-  if (batch > kLinearSlice && batch % kLinearSlice)
-    need = std::max(need, linear_workspace_bytes(rows, cols, (int)(batch % kLinearSlice), d->sms));
-  return (int64_t)need;
+  return rows == 0 || cols == 0 || batch == 0 ? 0 : (int64_t)linear_need(rows, cols, batch, d->sms);
 }
 
 int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows, int64_t cols,
                  const void *x, int64_t x_stride, int64_t batch, const nvfp4_epilogue *epilogue, void *y,
-                 int64_t y_stride, void *workspace, cudaStream_t stream) {
+                 int64_t y_stride, void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
   int st = check_shape(rows, cols);
   if (st != NVFP4_OK) return st;
   const nvfp4_epilogue none = {};
@@ -609,9 +612,11 @@ int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha
   st = device_info(&d);
   if (st != NVFP4_OK) return st;
   if (!work) return NVFP4_OK;
-  const size_t bytes = cols == 0 ? 0 : (size_t)nvfp4_linear_workspace_bytes(rows, cols, batch);
   void *own = nullptr;
-  cudaError_t e = workspace ? cudaSuccess : take_workspace(&own, bytes, *d, stream);
+  st = take_workspace(&workspace, &own, workspace_bytes,
+                      cols == 0 ? 0 : linear_need(rows, cols, batch, d->sms), *d, stream);
+  if (st != NVFP4_OK) return st;
+  cudaError_t e = cudaSuccess;
   for (int64_t b = 0; b < batch && e == cudaSuccess; b += kLinearSlice) {
     auto at = [&](const void *p, int64_t stride) {
       return p ? static_cast<const char *>(p) + 2 * b * stride : nullptr;
@@ -621,7 +626,7 @@ int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha
                           ep.gate_stride, at(ep.residual, ep.residual_stride), ep.residual_stride, ep.activation,
                           const_cast<char *>(at(y, y_stride)), y_stride};
     TraceScope tr(kTrLinear, stream);
-    e = launch_linear(a, d->sms, workspace ? workspace : own, first_tries(), stream);
+    e = launch_linear(a, d->sms, workspace, first_tries(), stream);
   }
   const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);
@@ -681,7 +686,8 @@ int64_t nvfp4_paged_attention_workspace_bytes(const nvfp4_kv_cache *cache, int q
 
 int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_stride, int64_t sequences, int q_heads,
                           const int32_t *lengths, const int32_t *table, int64_t table_width, int64_t table_stride,
-                          float scale, int64_t window, void *out, float *lse, void *workspace, cudaStream_t stream) {
+                          float scale, int64_t window, void *out, float *lse, void *workspace,
+                          int64_t workspace_bytes, cudaStream_t stream) {
   AttendArgs a = {};
   int st = kv_args(cache, &a.kv);
   if (st == NVFP4_OK) st = kv_table(&a.kv, table, sequences, table_width, table_stride);
@@ -710,11 +716,12 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
   a.lse = lse;
   a.first_tries = first_tries();
   void *own = nullptr;
-  cudaError_t e = workspace ? cudaSuccess
-                            : take_workspace(&own, attend_workspace_bytes(a.kv, q_heads, d->sms), *d, stream);
-  if (e == cudaSuccess) {
+  st = take_workspace(&workspace, &own, workspace_bytes, attend_workspace_bytes(a.kv, q_heads, d->sms), *d, stream);
+  if (st != NVFP4_OK) return st;
+  cudaError_t e;
+  {
     TraceScope tr(kTrAttend, stream);
-    e = launch_attend(a, d->sms, workspace ? workspace : own, stream);
+    e = launch_attend(a, d->sms, workspace, stream);
   }
   const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);

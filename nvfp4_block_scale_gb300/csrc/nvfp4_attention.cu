@@ -11,7 +11,8 @@
 // Work split: an item is one sequence and one block of up to 8 NT query heads
 // that share a cache head.  Its visible tokens are cut into tiles of KT, and the
 // tiles of all items form one sequence; CTA c takes the contiguous range
-// [c T / G, (c + 1) T / G) of it, so ragged lengths balance without the host
+// [c T / G, (c + 1) T / G) of it (an item counts kAttItemCost tiles more than
+// it has), so ragged lengths balance without the host
 // knowing them.  The part of an item inside a CTA's range is a segment.  The
 // kAttWarps consuming warps take the CTA's tiles in turn, each with a running
 // maximum, sum and output of its own (no barrier inside a segment), and meet in
@@ -55,6 +56,7 @@ constexpr int kAttConsumers = kAttWarps * 32;
 constexpr int kAttThreads = kAttConsumers + 32;
 constexpr int kAttMinTiles = 4;      // tiles per CTA below which fewer CTAs take part
 constexpr int kAttMaxCtas = 1024;
+constexpr int kAttItemCost = 6;      // an item's cost apart from its tiles, in tiles
 constexpr int kAttTries = 2000;      // x 1 ms: bound of a wait for a copy
 
 template <int D, bool E4M3, int NT>
@@ -190,12 +192,16 @@ struct AttSplit {
 };
 
 // A position in a CTA's range: a segment (tiles [first, first + count) of
-// sequence b, head block hg) and the tiles left behind it.
+// sequence b, head block hg) and what is left behind it.  The split counts
+// units: an item's tiles and, before them, kAttItemCost more, which stand for
+// what an item costs apart from its tiles.
 struct AttSeg {
   int b, hg;
   int first, count;  // tiles, numbered from token 0
   int off, total;    // the segment's place among the item's tiles, and their number
-  int64_t left;      // tiles of the range behind this segment
+  int unit;          // the segment's place among the item's units
+  int units;         // the segment's units
+  int64_t left;      // units of the range behind this segment
   int n, lo;         // visible tokens [lo, n)
 };
 
@@ -207,25 +213,33 @@ __device__ __forceinline__ void att_visible(const AttendArgs &a, int b, int &n, 
 template <int KT>
 __device__ __forceinline__ int att_tiles(int n, int lo) { return n > 0 ? (n - 1) / KT - lo / KT + 1 : 0; }
 
-// The segment at tile `off` of item (b, hg), at most `left` tiles long.
+__device__ __forceinline__ int att_units(int tiles) { return tiles > 0 ? tiles + kAttItemCost : 0; }
+
+// The segment from unit `unit` of item (b, hg) on, at most `left` units long.
 template <int KT>
-__device__ __forceinline__ void att_segment(AttSeg &s, int off, int64_t left) {
-  s.off = off;
-  s.first = s.lo / KT + off;
-  s.count = (int)min((int64_t)(s.total - off), left);
-  s.left = left - s.count;
+__device__ __forceinline__ void att_segment(AttSeg &s, int unit, int64_t left) {
+  s.unit = unit;
+  s.units = (int)min((int64_t)(att_units(s.total) - unit), left);
+  s.left = left - s.units;
+  s.off = max(unit - kAttItemCost, 0);
+  s.count = max(unit + s.units - kAttItemCost, 0) - s.off;
+  s.first = s.lo / KT + s.off;
 }
-// Moves to the next segment; s.left > 0.
+// Moves to the next segment that has tiles; false: there is none.
 template <int KT>
-__device__ __forceinline__ void att_next(const AttendArgs &a, AttSeg &s, int groups) {
-  if (++s.hg == groups) {
-    s.hg = 0;
-    do {  // (a later sequence holds the tiles that are left)
-      att_visible(a, ++s.b, s.n, s.lo);
-    } while (s.n == 0);
-    s.total = att_tiles<KT>(s.n, s.lo);
-  }
-  att_segment<KT>(s, 0, s.left);
+__device__ __forceinline__ bool att_next(const AttendArgs &a, AttSeg &s, int groups) {
+  do {
+    if (s.left == 0) return false;
+    if (++s.hg == groups) {
+      s.hg = 0;
+      do {  // (a later sequence holds the units that are left)
+        att_visible(a, ++s.b, s.n, s.lo);
+      } while (s.n == 0);
+      s.total = att_tiles<KT>(s.n, s.lo);
+    }
+    att_segment<KT>(s, 0, s.left);
+  } while (s.count == 0);
+  return true;
 }
 
 // 14: the scale 2^14 of E4M3's weights, which the sums have too.
@@ -276,7 +290,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   for (int b = sb0; b < sb1; ++b) {
     int n, lo;
     att_visible(a, b, n, lo);
-    mine += att_tiles<KT>(n, lo);
+    mine += att_units(att_tiles<KT>(n, lo));
   }
   int64_t incl = mine;
 #pragma unroll
@@ -302,12 +316,13 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
     for (seg.b = sb0;; ++seg.b) {
       att_visible(a, seg.b, seg.n, seg.lo);
       seg.total = att_tiles<KT>(seg.n, seg.lo);
-      if (rem < (int64_t)seg.total * groups) break;
-      rem -= (int64_t)seg.total * groups;
+      const int64_t all = (int64_t)att_units(seg.total) * groups;
+      if (rem < all) break;
+      rem -= all;
     }
     s_start[0] = seg.b;
-    s_start[1] = (int)att_div(rem, seg.total);
-    s_start[2] = (int)(rem - (int64_t)s_start[1] * seg.total);
+    s_start[1] = (int)att_div(rem, att_units(seg.total));
+    s_start[2] = (int)(rem - (int64_t)s_start[1] * att_units(seg.total));
   }
   __syncthreads();
   if (g0 < g1) {
@@ -317,11 +332,12 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
     seg.total = att_tiles<KT>(seg.n, seg.lo);
     att_segment<KT>(seg, s_start[2], g1 - g0);
   }
+  const bool any = g0 < g1 && (seg.count > 0 || att_next<KT>(a, seg, groups));  // tiles in the range
 
   if (warp == kAttWarps) {
     // ---- loads: a consumer's u-th tile goes to stage u % S of its ring
     int given = 0;  // lane w: tiles given to consumer w
-    if (g0 < g1) {
+    if (any) {
       const int piece = 1 << p.piece_shift, pp = KT >> p.piece_shift;  // pieces (pages) per tile: 1, 2 or 4
       const int page_mask = (1 << a.kv.page_shift) - 1;
       int ids_b = -1, ids_base = 0, ids = -1;  // this lane's page number, for tiles of ids_b from ids_base on
@@ -382,8 +398,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
           if (lane == w) ++given;
           w = w + 1 == kAttWarps ? 0 : w + 1;
         }
-        if (seg.left == 0) break;
-        att_next<KT>(a, seg, groups);
+        if (!att_next<KT>(a, seg, groups)) break;
       }
     }
     __syncthreads();  // the consumers are done
@@ -406,7 +421,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
       for (int i = tid; i < a.q_heads; i += kAttConsumers) a.lse[(int64_t)b * a.q_heads + i] = -INFINITY;
   }
   AttShared shared = {0, 0, 0};
-  if (g0 >= g1) {
+  if (!any) {
     if (tid == 0) p.shared[c] = shared;
     __syncthreads();
     return;
@@ -717,11 +732,11 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
     if (!whole && seg.off == 0) {  // this CTA holds the item's first part: the range's last segment
       shared.row = (int64_t)seg.b * a.q_heads + h0;
       shared.heads = heads;
-      shared.parts = split.cta_of(g1 - seg.count + seg.total - 1) - c + 1;
+      // (the unit of the item's last tile)
+      shared.parts = split.cta_of(g1 - seg.left - seg.units - seg.unit + kAttItemCost + seg.total - 1) - c + 1;
     }
-    if (seg.left == 0) break;
     i0 = (i0 + seg.count) & (kAttWarps - 1);
-    att_next<KT>(a, seg, groups);
+    if (!att_next<KT>(a, seg, groups)) break;
     asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");  // red and s_ml are free again
   }
   if (tid == 0) p.shared[c] = shared;

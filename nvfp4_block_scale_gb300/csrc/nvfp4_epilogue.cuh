@@ -24,15 +24,6 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t c, uint32_t (&w)[4]) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // |e| <= 126
 
-// Counts an arrival at *c, by one thread after a barrier of its CTA: what the
-// CTA wrote before is visible to whoever sees the count, and what the counted
-// CTAs wrote to this one behind the next barrier.
-__device__ __forceinline__ uint32_t arrive_count(uint32_t *c) {
-  uint32_t before;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(c) : "memory");
-  return before;
-}
-
 // The activations by their formulas, with CUDA's own exp, tanh and erf.  One
 // branch for all values: a branch per value would put every function's code
 // between two values, and waiting for instructions then costs more than the

@@ -77,7 +77,6 @@ cudaError_t check_take_decoupled(uint32_t *site);
 cudaError_t launch_check_selftest(int64_t i, int64_t n, cudaStream_t st);
 constexpr int kLinearSlice = 256;        // vectors of one product launch at most
 constexpr int kMaxQHeads = 1024;
-constexpr size_t kCounterBytes = 8192;   // zeroed head of a product's or an attention's workspace
 // Launch arguments of the decode-step operators (checked by the C ABI).
 struct LinearArgs {
   const uint8_t *codes;

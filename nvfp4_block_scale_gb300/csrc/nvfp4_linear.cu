@@ -3,8 +3,7 @@
 //
 // Many vectors and large tensors go to the tcgen05 product
 // (nvfp4_linear_tc.cu).  The others are bound by latency, then by reading the
-// weights once (0.5625 B each), and run here, in one launch without tensor
-// memory:
+// weights once (0.5625 B each), and run here, without tensor memory:
 //
 // Products: mma.sync m16n8k16 (bf16 x bf16 -> fp32), 16 rows of W by 8 vectors.
 // q * Delta is formed in registers, exactly: six significant bits between
@@ -18,9 +17,8 @@
 // so no warp waits for another until the end.  A warp's sums of a tile go to
 // shared memory: to the tile's place if the warp took the tile's first step,
 // else (its run began inside the tile) to a place of the warp's own; after one
-// barrier they are added in warp order.  Rectangles that share rows meet in
-// the workspace, where the CTA that comes last (a counter per group of rows)
-// adds them in column order.
+// barrier they are added in warp order.  The sums of rectangles that share rows
+// meet in the workspace, where a second launch adds them in column order.
 //
 // Loads: a lane takes 16 consecutive code bytes (32 columns) of two rows per
 // step, kLinDepth steps ahead, straight into registers.  The order of the
@@ -46,7 +44,6 @@ constexpr int kLinVecs = 16, kLinBlocks8 = 32, kLinBlocks16 = 8;
 constexpr int kLinWarps = 8;
 constexpr int kLinThreads = kLinWarps * 32;
 constexpr int kLinDepth = 4;       // steps in flight per warp
-constexpr int kLinMaxGroups = (int)(kCounterBytes / 4);
 constexpr int kLinSmem = 88 * 1024;  // dynamic shared memory of one of two CTAs per SM
 
 // Shared memory of a rectangle: x, the tiles' sums, the warps' own.
@@ -63,7 +60,6 @@ struct LinPlan {
 struct LinLaunch {
   LinearArgs a;
   LinPlan p;
-  uint32_t *count;  // [groups], zero between calls
   float4 *part;     // [ranges][tiles][NT][32]: sums in the MMA's lane order
   int min_steps, long_ranges, min_tiles, long_groups;  // steps = min_steps * ranges + long_ranges, tiles likewise
 };
@@ -103,9 +99,9 @@ template <int NT, bool WIDE>
 __global__ void __launch_bounds__(kLinThreads, 2) k_linear(const __grid_constant__ LinLaunch p) {
   constexpr int N = 8 * NT;
   extern __shared__ uint4 dsm[];
-  __shared__ int s_last;
   const LinearArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
+  pdl_launch_dependents();  // k_linear_sum waits for the whole grid all the same
   // the first (steps mod ranges) ranges and (tiles mod groups) groups are one longer
   const int group = blockIdx.x / (uint32_t)p.p.ranges, range = blockIdx.x - group * p.p.ranges;
   const int nk = p.min_steps + (range < p.long_ranges), k0 = range * p.min_steps + min(range, p.long_ranges);
@@ -263,28 +259,23 @@ __global__ void __launch_bounds__(kLinThreads, 2) k_linear(const __grid_constant
       v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
     }
     if (p.p.ranges == 1) finish4(a, alpha, t0 + t, nt, l, v);
-    else __stcg(p.part + ((int64_t)range * p.p.tiles + t0) * NT * 32 + i, v);
+    else p.part[((int64_t)range * p.p.tiles + t0) * NT * 32 + i] = v;
   }
-  if (p.p.ranges == 1) return;
+}
 
-  // ---- the ranges of this group of rows
-  __syncthreads();
-  if (tid == 0) {
-    s_last = arrive_count(p.count + group) == (uint32_t)(p.p.ranges - 1);
-    if (s_last) p.count[group] = 0u;  // as the next call wants it
-  }
-  __syncthreads();
-  if (!s_last) return;
-  for (int i = tid; i < ntile * NT * 32; i += kLinThreads) {
-    const float4 *from = p.part + (int64_t)t0 * NT * 32 + i;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+// Adds the column ranges' sums in column order and finishes them.
+template <int NT>
+__global__ void __launch_bounds__(256) k_linear_sum(const __grid_constant__ LinLaunch p) {
+  pdl_wait();
+  const int64_t all = (int64_t)p.p.tiles * NT * 32, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= all) return;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-    for (int k = 0; k < p.p.ranges; ++k) {
-      const float4 o = __ldcg(from + (int64_t)k * p.p.tiles * NT * 32);
-      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-    }
-    finish4(a, alpha, t0 + i / (NT * 32), i % (NT * 32) >> 5, i & 31, v);
+  for (int k = 0; k < p.p.ranges; ++k) {
+    const float4 o = p.part[k * all + i];
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
   }
+  finish4(p.a, *p.a.alpha, i / (NT * 32), (int)(i % (NT * 32)) >> 5, (int)i & 31, v);
 }
 
 // cols == 0: the epilogue of a zero sum.
@@ -310,13 +301,13 @@ bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {
       steps * tiles > (int64_t)ctas * (batch <= 8 ? kLinBlocks8 : kLinBlocks16))
     return false;
   int64_t least = -1;
-  for (int64_t ranges = 1; ranges <= std::min<int64_t>(steps, 96); ++ranges) {
+  for (const int64_t ranges : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64, 96}) {
+    if (ranges > steps) break;
     const int64_t ms = (steps + ranges - 1) / ranges;
     const int64_t most = (kLinSmem - lin_smem(nt, ms, 0)) / (nt * 512);  // tiles that fit
     if (most < 1) continue;
     int64_t groups = std::min<int64_t>(tiles, std::max<int64_t>(1, ctas / ranges));
     if ((tiles + groups - 1) / groups > most) groups = (tiles + most - 1) / most;
-    if (ranges > 1 && groups > kLinMaxGroups) continue;
     const int64_t mt = (tiles + groups - 1) / groups, waves = (groups * ranges + ctas - 1) / ctas;
     const int64_t cost = waves * (mt * ms * 1152 + ms * batch * 500 + (ranges > 1 ? 44000 + mt * nt * 512 * (2 + ranges / 4) : 0));
     if (least < 0 || cost < least) {
@@ -333,7 +324,18 @@ cudaError_t lin_launch(const LinLaunch &p, bool wide, cudaStream_t st) {
   const int grid = p.p.ranges * p.p.groups;
   if (wide) k_linear<NT, true><<<grid, kLinThreads, smem, st>>>(p);
   else k_linear<NT, false><<<grid, kLinThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.p.ranges == 1) return e;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.p.tiles * NT * 32 + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_linear_sum<NT>, p);
 }
 
 }  // namespace
@@ -342,7 +344,7 @@ size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms) {
   LinPlan p;
   if (!lin_plan(rows, cols, batch, sms, &p))
     return linear_tc_workspace_bytes(rows, cols, batch, sms);
-  return p.ranges == 1 ? 0 : kCounterBytes + (size_t)p.ranges * p.tiles * lin_nt(batch) * 512;
+  return p.ranges == 1 ? 0 : (size_t)p.ranges * p.tiles * lin_nt(batch) * 512;
 }
 
 cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st) {
@@ -350,11 +352,10 @@ cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_trie
     k_linear_empty<<<(int)std::min<int64_t>((a.rows * a.batch + 255) / 256, 8 * sms), 256, 0, st>>>(a);
     return cudaGetLastError();
   }
-  void *part = static_cast<char *>(ws) + kCounterBytes;
   LinPlan plan;
   if (!lin_plan(a.rows, a.cols, a.batch, sms, &plan))
     return launch_linear_tc(a, sms, ws, first_tries, st);
-  const LinLaunch p = {a, plan, static_cast<uint32_t *>(ws), static_cast<float4 *>(part), plan.steps / plan.ranges,
+  const LinLaunch p = {a, plan, static_cast<float4 *>(ws), plan.steps / plan.ranges,
                        plan.steps % plan.ranges, plan.tiles / plan.groups, plan.tiles % plan.groups};
   const bool wide = a.cols % 32 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(a.scales) % 2 == 0;

@@ -731,7 +731,7 @@ LtPlan lt_plan(int64_t rows, int64_t cols, int batch, int sms) {
   const int64_t parts = std::max<int64_t>(1, (int64_t)(std::sqrt((double)p.K * step / part) + 0.5));
   p.G = std::min<int64_t>({p.tiles * p.K, sms, p.tiles * parts});
   p.bf = batch > 128 || p.tiles * p.K <= kLtBfSteps * p.G;
-  p.up = kCounterBytes;
+  p.up = 0;
   p.xf = p.up + kLinearSlice * sizeof(int);
   p.part = (p.xf + (p.bf ? 0 : (size_t)batch * cols * 2) + 255) / 256 * 256;
   p.bytes = p.part + 2 * (size_t)p.G * batch * kLtM * sizeof(float);

@@ -12,7 +12,7 @@ A = 0x100000  # fake, aligned device address: never dereferenced on these paths
 
 def _linear(**kw):
     d = dict(codes=A, scales=A, alpha=A, rows=4, cols=32, x=A, x_stride=32, batch=2, epilogue=None, y=A, y_stride=4,
-             workspace=None, stream=None)
+             workspace=None, workspace_bytes=0, stream=None)
     d.update(kw)
     return nv.nvfp4_linear(*d.values())
 
@@ -63,7 +63,7 @@ def _append(**kw):
 
 def _attend(**kw):
     d = dict(cache=_cache(), q=A, q_stride=4 * 64, sequences=2, q_heads=4, lengths=A, table=A, table_width=4,
-             table_stride=4, scale=0.125, window=0, out=A, lse=A, workspace=None, stream=None)
+             table_stride=4, scale=0.125, window=0, out=A, lse=A, workspace=None, workspace_bytes=0, stream=None)
     d.update(kw)
     return nv.nvfp4_paged_attention(*d.values())
 
