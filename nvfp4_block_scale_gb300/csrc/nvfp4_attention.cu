@@ -14,15 +14,19 @@
 // [c T / G, (c + 1) T / G) of it (an item counts kAttItemCost tiles more than
 // it has), so ragged lengths balance without the host
 // knowing them.  The part of an item inside a CTA's range is a segment.  The
-// kAttWarps consuming warps take the CTA's tiles in turn, each with a running
-// maximum, sum and output of its own (no barrier inside a segment), and meet in
-// shared memory at the segment's end.  An item inside one CTA is finished there; the parts of a longer one go to the workspace, where a second launch
+// kAttWarps consuming warps share a segment's tiles, each with a running maximum,
+// sum and output of its own (no barrier inside a segment), and meet in shared
+// memory at the segment's end, which costs about 4000 clocks; so an item of few
+// tiles is one warp's alone: of as many as its ring holds, because the loads of
+// more would hold up the other warps' (with up to 8 tiles in rings of 2, 61
+// ragged sequences took 73 us instead of 57).  An item inside one CTA is
+// finished there; the parts of a longer one go to the workspace, where a second launch
 // (k_attend_join) adds them in CTA order, so that results do not depend on
 // timing.  (When the CTA that came last added them, behind a fence and a
 // counter, it cost up to 14 us under load: 61 ragged sequences of up to 2048
 // tokens took 62 us.)
 //
-// Loads: a fifth warp fills a ring of S tiles per consuming warp by TMA, across
+// Loads: two more warps fill a ring of S tiles per consuming warp by TMA, across
 // segments (keys and values of a page as boxes of 128-byte rows, 128-byte
 // swizzle; pages outside the cache read as zeros), and the queries of each
 // segment.  When the consumers asked for their own tiles, that took 700 clocks
@@ -53,7 +57,8 @@ namespace nvfp4 {
 
 constexpr int kAttWarps = 4;
 constexpr int kAttConsumers = kAttWarps * 32;
-constexpr int kAttThreads = kAttConsumers + 32;
+constexpr int kAttLoaders = 2;       // warps, each for the rings of kAttWarps / kAttLoaders consumers
+constexpr int kAttThreads = kAttConsumers + 32 * kAttLoaders;
 constexpr int kAttMinTiles = 4;      // tiles per CTA below which fewer CTAs take part
 constexpr int kAttMaxCtas = 1024;
 constexpr int kAttItemCost = 6;      // an item's cost apart from its tiles, in tiles
@@ -71,12 +76,12 @@ struct AttCfg {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRedStride = D + 4;                     // floats; keeps the lanes of a store in distinct banks
   static constexpr int kRed = kAttWarps * kHeads * kRedStride * 4;
-  static constexpr int kQRow = D * 2 + 16;                     // bytes of a staged query head (ldmatrix without conflicts)
+  static constexpr int kQRow = D * 2;                          // bytes of a staged query head
   static constexpr int kQ = kHeads * kQRow;
-  static constexpr int NQ = 2;                                 // segments whose queries are staged ahead
+  static constexpr int NQ = NT == 1 && D < 256 ? 8 : 2;        // segments whose queries are staged ahead
   static constexpr int kBudget = 113 * 1024 - 2048;  // dynamic shared memory of one of the CTAs per SM
   static constexpr int S0 = (kBudget - 1024 - kRed - NQ * kQ) / (kAttWarps * kTile);
-  static constexpr int S = S0 >= 4 ? 4 : S0 >= 2 ? S0 : 2;
+  static constexpr int S = S0 >= 6 ? 6 : S0 >= 2 ? S0 : 2;
   static constexpr int kRing = kAttWarps * S * kTile;
   static constexpr size_t kSmem = 1024 + kRing + kRed + NQ * kQ;
   static_assert(kSmem <= 226 * 1024, "shared memory");
@@ -225,6 +230,31 @@ __device__ __forceinline__ void att_segment(AttSeg &s, int unit, int64_t left) {
   s.count = max(unit + s.units - kAttItemCost, 0) - s.off;
   s.first = s.lo / KT + s.off;
 }
+// Who takes a segment's tiles: one warp all of them, or tile j warp
+// (first + j) % 4, beginning with the warp that has been given least.  Loaders
+// and consumers each keep the same tally.
+struct AttTeam {
+  int load[kAttWarps] = {0, 0, 0, 0};
+  bool solo;
+  int first;
+  __device__ __forceinline__ void take(const AttSeg &s, int most) {
+    solo = s.count == s.total && s.count <= most;
+    first = 0;
+    int least = load[0];
+#pragma unroll
+    for (int w = 1; w < kAttWarps; ++w)
+      if (load[w] < least) {
+        least = load[w];
+        first = w;
+      }
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+      const int j = (w - first) & (kAttWarps - 1);
+      load[w] += solo ? (j == 0 ? s.count : 0) : (s.count - j + kAttWarps - 1) / kAttWarps;
+    }
+  }
+};
+
 // Moves to the next segment that has tiles; false: there is none.
 template <int KT>
 __device__ __forceinline__ bool att_next(const AttendArgs &a, AttSeg &s, int groups) {
@@ -257,7 +287,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   extern __shared__ uint8_t dsm[];
   // full: a tile has landed; empty: it has been read; q_*: the queries of a segment
   __shared__ __align__(8) uint64_t full[kAttWarps * S], empty[kAttWarps * S], q_full[C::NQ], q_empty[C::NQ];
-  __shared__ int64_t s_sum[kAttWarps + 1];
+  __shared__ int64_t s_sum[kAttThreads / 32];
   __shared__ int s_start[3], s_fail;
   __shared__ float s_ml[kAttWarps][C::kHeads][2];
   const AttendArgs &a = p.a;
@@ -302,7 +332,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   __syncthreads();
   int64_t T = 0;
 #pragma unroll
-  for (int w = 0; w <= kAttWarps; ++w) {
+  for (int w = 0; w < kAttThreads / 32; ++w) {
     if (w < warp) incl += s_sum[w];
     T += s_sum[w];
   }
@@ -334,30 +364,35 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   }
   const bool any = g0 < g1 && (seg.count > 0 || att_next<KT>(a, seg, groups));  // tiles in the range
 
-  if (warp == kAttWarps) {
+  AttTeam team;
+  if (warp >= kAttWarps) {
     // ---- loads: a consumer's u-th tile goes to stage u % S of its ring
+    constexpr int kMine = kAttWarps / kAttLoaders;  // consumers of this loader: kMine * loader ..
+    const int loader = warp - kAttWarps;
     int given = 0;  // lane w: tiles given to consumer w
     if (any) {
       const int piece = 1 << p.piece_shift, pp = KT >> p.piece_shift;  // pieces (pages) per tile: 1, 2 or 4
       const int page_mask = (1 << a.kv.page_shift) - 1;
       int ids_b = -1, ids_base = 0, ids = -1;  // this lane's page number, for tiles of ids_b from ids_base on
       bool ok = true;
-      int w = 0;  // whose turn it is
       for (int k = 0; ok; ++k) {  // segments
         const int kh = seg.hg / p.blocks, h0 = kh * group + (seg.hg % p.blocks) * C::kHeads;
         const int heads = min(C::kHeads, (kh + 1) * group - h0), qb = k % C::NQ;
-        if (!att_wait(att_smem(&q_empty[qb]), ((uint32_t)(k / C::NQ) & 1u) ^ 1u, kAttTries)) break;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + seg.b * a.q_stride + (int64_t)h0 * D;
-        const uint32_t q_bar = att_smem(&q_full[qb]);
-        if (lane == 0)
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(q_bar), "r"(heads * D * 2) : "memory");
-        __syncwarp();
-        if (lane < heads)
-          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                       ::"r"(qs_smem + qb * C::kQ + lane * C::kQRow), "l"(q + (int64_t)lane * D), "r"(D * 2), "r"(q_bar)
-                       : "memory");
+        if (loader == 0) {
+          if (!att_wait(att_smem(&q_empty[qb]), ((uint32_t)(k / C::NQ) & 1u) ^ 1u, kAttTries)) break;
+          if (att_elect()) {
+            const uint32_t q_bar = att_smem(&q_full[qb]);
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + seg.b * a.q_stride + (int64_t)h0 * D;
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(q_bar), "r"(heads * D * 2) : "memory");
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                         ::"r"(qs_smem + qb * C::kQ), "l"(q), "r"(heads * D * 2), "r"(q_bar) : "memory");
+          }
+          __syncwarp();
+        }
+        team.take(seg, S);
         for (int j = 0; j < seg.count; ++j) {
-          const int t = seg.first + j;
+          const int t = seg.first + j, w = team.solo ? team.first : (team.first + j) & (kAttWarps - 1);
+          if (w / kMine != loader) continue;
           if (ids_b != seg.b || t < ids_base || t >= ids_base + 32 / pp) {  // page numbers of 32 / pp tiles, a lane each
             ids_b = seg.b;
             ids_base = t;
@@ -396,14 +431,13 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
           }
           __syncwarp();
           if (lane == w) ++given;
-          w = w + 1 == kAttWarps ? 0 : w + 1;
         }
         if (!att_next<KT>(a, seg, groups)) break;
       }
     }
     __syncthreads();  // the consumers are done
     if (s_fail)       // copies that nothing waited for: let them land
-      for (int w = 0; w < kAttWarps; ++w) {
+      for (int w = kMine * loader; w < kMine * (loader + 1); ++w) {
         const int n = __shfl_sync(0xFFFFFFFFu, given, w);
         for (int u = max(0, n - S); u < n; ++u) att_wait(att_smem(&full[w * S + u % S]), (uint32_t)(u / S) & 1u, kAttTries);
       }
@@ -427,7 +461,6 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
     return;
   }
 
-  int i0 = 0;               // the warp that takes the segment's first tile
   int stage = 0;            // of this warp's next tile
   uint32_t full_ph = 0u;
   bool bad = false;         // a copy did not arrive in time: this warp's sums become NaN
@@ -443,13 +476,20 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   };
 
   for (int k = 0;; ++k) {
-    const int turn = (warp - i0) & (kAttWarps - 1);  // this warp's first tile of the segment
+    team.take(seg, S);
+    const int turn = (warp - team.first) & (kAttWarps - 1);  // this warp's first tile of the segment
     // (Every warp waits for and hands back the queries of every segment, with
     // tiles in it or not: a warp that skipped some could be two phases off the
     // mbarrier, which a parity cannot tell from none.)
     const int qb = k % C::NQ;
     if (!dead && !__all_sync(0xFFFFFFFFu, att_wait(att_smem(&q_full[qb]), (uint32_t)(k / C::NQ) & 1u, kAttTries)))
       bad = dead = true;
+    if (team.solo && turn != 0) {  // another warp's
+      if (lane == 0 && !dead)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&q_empty[qb])) : "memory");
+      if (!att_next<KT>(a, seg, groups)) break;
+      continue;
+    }
     const int kh = seg.hg / p.blocks, h0 = kh * group + (seg.hg % p.blocks) * C::kHeads;
     const int heads = min(C::kHeads, (kh + 1) * group - h0);
     const float sc = a.scale * (E4M3 && a.kv.k_scale ? __ldg(a.kv.k_scale + kh) : 1.0f) * 1.4426950408889634f;
@@ -519,7 +559,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
         for (int j = 0; j < 4; ++j) o[nt][d][j] = 0.0f;
     }
 
-    for (int t = seg.first + turn; t < seg.first + seg.count; t += kAttWarps) {
+    for (int t = seg.first + turn; t < seg.first + seg.count; t += team.solo ? 1 : kAttWarps) {
       const int at = warp * S + stage;
       if (!dead && !__all_sync(0xFFFFFFFFu, att_wait(att_smem(&full[at]), full_ph, tries))) {
         bad = true;  // (a stage goes back only once its copy has landed)
@@ -669,7 +709,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
     }
 
     // ---- the warps' parts meet: those of the segment's first tiles
-    const int parts = min(kAttWarps, seg.count);
+    const int parts = team.solo ? 1 : min(kAttWarps, seg.count);
     if (turn < parts) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -694,19 +734,20 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
         }
     }
     if (dead) s_fail = 1;
-    asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");
+    if (team.solo) __syncwarp();
+    else asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");
     const bool whole = seg.count == seg.total;
     // parts of an item: the first in its CTA's slot 2c + 1, the others in their CTAs' slots 2c
     const int64_t slot = 2 * c + (seg.off == 0 ? 1 : 0);
     const float vs = E4M3 && a.kv.v_scale ? __ldg(a.kv.v_scale + kh) : 1.0f;
     float2 *ml_all = reinterpret_cast<float2 *>(p.part + (int64_t)2 * gridDim.x * C::kHeads * D);
-    for (int i = tid; i < heads * (D / 8); i += kAttConsumers) {
+    for (int i = team.solo ? lane : tid; i < heads * (D / 8); i += team.solo ? 32 : kAttConsumers) {
       const int h = i / (D / 8), d = i % (D / 8) * 8;
       float mx = -INFINITY, sum = 0.0f, v[8] = {};
-      for (int j = 0; j < parts; ++j) mx = fmaxf(mx, s_ml[(i0 + j) & (kAttWarps - 1)][h][0]);
+      for (int j = 0; j < parts; ++j) mx = fmaxf(mx, s_ml[(team.first + j) & (kAttWarps - 1)][h][0]);
       const float ref = mx == -INFINITY ? 0.0f : mx;
       for (int j = 0; j < parts; ++j) {
-        const int w = (i0 + j) & (kAttWarps - 1);
+        const int w = (team.first + j) & (kAttWarps - 1);
         const float f = att_exp2(s_ml[w][h][0] - ref);
         sum += s_ml[w][h][1] * f;
         const float4 *x = reinterpret_cast<const float4 *>(red + (w * C::kHeads + h) * C::kRedStride + d);
@@ -735,9 +776,10 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
       // (the unit of the item's last tile)
       shared.parts = split.cta_of(g1 - seg.left - seg.units - seg.unit + kAttItemCost + seg.total - 1) - c + 1;
     }
-    i0 = (i0 + seg.count) & (kAttWarps - 1);
     if (!att_next<KT>(a, seg, groups)) break;
-    asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");  // red and s_ml are free again
+    // red and s_ml are free again
+    if (team.solo) __syncwarp();
+    else asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");
   }
   if (tid == 0) p.shared[c] = shared;
   __syncthreads();
