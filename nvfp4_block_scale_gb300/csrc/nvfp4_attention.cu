@@ -26,7 +26,7 @@
 // counter, it cost up to 14 us under load: 61 ragged sequences of up to 2048
 // tokens took 62 us.)
 //
-// Loads: two more warps fill a ring of S tiles per consuming warp by TMA, across
+// Loads: two or four more warps fill a ring of S tiles per consuming warp by TMA, across
 // segments (keys and values of a page as boxes of 128-byte rows, 128-byte
 // swizzle; pages outside the cache read as zeros), and the queries of each
 // segment.  When the consumers asked for their own tiles, that took 700 clocks
@@ -57,8 +57,6 @@ namespace nvfp4 {
 
 constexpr int kAttWarps = 4;
 constexpr int kAttConsumers = kAttWarps * 32;
-constexpr int kAttLoaders = 2;       // warps, each for the rings of kAttWarps / kAttLoaders consumers
-constexpr int kAttThreads = kAttConsumers + 32 * kAttLoaders;
 constexpr int kAttMinTiles = 4;      // tiles per CTA below which fewer CTAs take part
 constexpr int kAttMaxCtas = 1024;
 constexpr int kAttItemCost = 6;      // an item's cost apart from its tiles, in tiles
@@ -74,6 +72,13 @@ struct AttCfg {
   static constexpr int kHalf = KT * kRow;                      // bytes of a tile's keys
   static constexpr int kTile = 2 * kHalf;
   static constexpr int kHeads = 8 * NT;
+  // Loading warps, each for the rings of kAttWarps / kLoaders consumers.  A
+  // consumer each takes 256 x 300 tokens (window 128, E4M3, heads of 64) from
+  // 34.6 to 31.9 us; where registers are short, the threads of four would cost
+  // more than they give (16 x 8192 tokens, E4M3, heads of 256: 34.5 -> 42.4 us,
+  // 12 heads per cache head of 64: 26.4 -> 28.2 us).
+  static constexpr int kLoaders = NT == 1 && D < 256 ? 4 : 2;
+  static constexpr int kThreads = kAttConsumers + 32 * kLoaders;
   static constexpr int kRedStride = D + 4;                     // floats; keeps the lanes of a store in distinct banks
   static constexpr int kRed = kAttWarps * kHeads * kRedStride * 4;
   static constexpr int kQRow = D * 2;                          // bytes of a staged query head
@@ -99,10 +104,10 @@ template <bool TRANS>
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   if (TRANS)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
   else
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
 // c += a b, 16 x 8 x 16, fp32 accumulators; f16 or bf16 operands.
@@ -279,7 +284,7 @@ __device__ __forceinline__ float att_lse(float ref, float sum) {
 }
 
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const __grid_constant__ CUtensorMap kmap,
                                                         const __grid_constant__ CUtensorMap vmap,
                                                         const __grid_constant__ AttLaunch p) {
   using C = AttCfg<D, E4M3, NT>;
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   extern __shared__ uint8_t dsm[];
   // full: a tile has landed; empty: it has been read; q_*: the queries of a segment
   __shared__ __align__(8) uint64_t full[kAttWarps * S], empty[kAttWarps * S], q_full[C::NQ], q_empty[C::NQ];
-  __shared__ int64_t s_sum[kAttThreads / 32];
+  __shared__ int64_t s_sum[C::kThreads / 32];
   __shared__ int s_start[3], s_fail;
   __shared__ float s_ml[kAttWarps][C::kHeads][2];
   const AttendArgs &a = p.a;
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   // ---- all tiles, this CTA's range of them, and the item where it begins: a
   // run of sequences per thread
   const int c = blockIdx.x;
-  const int per = (a.sequences + kAttThreads - 1) / kAttThreads;
+  const int per = (a.sequences + C::kThreads - 1) / C::kThreads;
   const int sb0 = min(tid * per, a.sequences), sb1 = min(sb0 + per, a.sequences);
   int64_t mine = 0;
   for (int b = sb0; b < sb1; ++b) {
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   __syncthreads();
   int64_t T = 0;
 #pragma unroll
-  for (int w = 0; w < kAttThreads / 32; ++w) {
+  for (int w = 0; w < C::kThreads / 32; ++w) {
     if (w < warp) incl += s_sum[w];
     T += s_sum[w];
   }
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
   AttTeam team;
   if (warp >= kAttWarps) {
     // ---- loads: a consumer's u-th tile goes to stage u % S of its ring
-    constexpr int kMine = kAttWarps / kAttLoaders;  // consumers of this loader: kMine * loader ..
+    constexpr int kMine = kAttWarps / C::kLoaders;  // consumers of this loader: kMine * loader ..
     const int loader = warp - kAttWarps;
     int given = 0;  // lane w: tiles given to consumer w
     if (any) {
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
         const uint32_t at = qs_smem + qb * C::kQ + (8 * nt + (lane >> 2)) * C::kQRow + 8 * (lane & 3);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(qf[nt][ks][0]), "=r"(qf[nt][ks][1]) : "r"(at + 32 * ks));
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(qf[nt][ks][0]), "=r"(qf[nt][ks][1]) : "r"(at + 32 * ks) : "memory");
       } else {
 #pragma unroll
         for (int ks = 0; ks < KS; ks += 2) {
@@ -543,10 +548,6 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
         }
       }
     }
-
-    __syncwarp();
-    if (lane == 0 && !dead)
-      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&q_empty[qb])) : "memory");
 
     float o[NT][KS][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -707,6 +708,13 @@ __global__ void __launch_bounds__(kAttThreads) k_attend(const __grid_constant__ 
         full_ph ^= 1u;
       }
     }
+
+    // The queries go back only once products have used them: handed back right
+    // behind the loads, 16 heads of 256 of a one-tile item were still being read
+    // when the next copy landed.
+    __syncwarp();
+    if (lane == 0 && !dead)
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&q_empty[qb])) : "memory");
 
     // ---- the warps' parts meet: those of the segment's first tiles
     const int parts = team.solo ? 1 : min(kAttWarps, seg.count);
@@ -878,7 +886,7 @@ int att_nt(int head_dim, int group) {
 template <int D, bool E4M3, int NT>
 int att_ctas_per_sm() {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_attend<D, E4M3, NT>, kAttThreads,
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_attend<D, E4M3, NT>, AttCfg<D, E4M3, NT>::kThreads,
                                                     AttCfg<D, E4M3, NT>::kSmem) != cudaSuccess || n < 1)
     n = 1;
   return n;
@@ -944,7 +952,7 @@ struct AttRun {
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     }
-    k_attend<D, E4M3, NT><<<grid, kAttThreads, C::kSmem, st>>>(m[0], m[1], p);
+    k_attend<D, E4M3, NT><<<grid, C::kThreads, C::kSmem, st>>>(m[0], m[1], p);
     const cudaError_t e = cudaGetLastError();
     // the parts of split items; one CTA, or a CTA for every item's tiles, splits none
     if (e != cudaSuccess || grid == 1) return e;

@@ -99,6 +99,22 @@ def test_long_and_short_together(kind, hq, hk, dim):
     assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hk,dim", [(8, 1, 128), (24, 1, 256), (16, 1, 256), (48, 1, 128), (32, 1, 64), (6, 2, 64)])
+def test_short_items_between_long_ones(kind, hq, hk, dim):
+    """CTAs that hold several short items, each one warp's, between parts of
+    long ones: the queries of one must not reach another."""
+    rng = np.random.default_rng(hq)
+    lengths = []
+    for i in range(24):
+        lengths += [int(rng.integers(2500, 6000))] + [int(n) for n in rng.integers(0, 40, int(rng.integers(1, 9)))]
+    cache, q, table, n = _setup(lengths, hq, hk, dim, 64, kind, 21)
+    out = nv.paged_attention(cache, q, table, n, return_lse=True)
+    _check(cache, q, table, n, *out, which={i for i, m in enumerate(lengths) if m < 40} | {0, len(lengths) - 1})
+    again = nv.paged_attention(cache, q, table, n, return_lse=True)
+    assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+
+
 def test_many_sequences():
     rng = np.random.default_rng(3)
     lengths = rng.integers(0, 60, 1500)
