@@ -207,6 +207,7 @@ struct AttSplit {
 // what an item costs apart from its tiles.
 struct AttSeg {
   int b, hg;
+  int kh, blk;       // hg = kh * blocks + blk
   int first, count;  // tiles, numbered from token 0
   int off, total;    // the segment's place among the item's tiles, and their number
   int unit;          // the segment's place among the item's units
@@ -236,37 +237,32 @@ __device__ __forceinline__ void att_segment(AttSeg &s, int unit, int64_t left) {
   s.first = s.lo / KT + s.off;
 }
 // Who takes a segment's tiles: one warp all of them, or tile j warp
-// (first + j) % 4, beginning with the warp that has been given least.  Loaders
-// and consumers each keep the same tally.
+// (first + j) % 4; the next segment begins with the warp after the last one.
+// Loaders and consumers each count along.  (Handing out by the tiles that each
+// warp has been given balances no better, and every warp pays for it at every
+// segment.)
 struct AttTeam {
-  int load[kAttWarps] = {0, 0, 0, 0};
+  int next = 0;
   bool solo;
   int first;
   __device__ __forceinline__ void take(const AttSeg &s, int most) {
     solo = s.count == s.total && s.count <= most;
-    first = 0;
-    int least = load[0];
-#pragma unroll
-    for (int w = 1; w < kAttWarps; ++w)
-      if (load[w] < least) {
-        least = load[w];
-        first = w;
-      }
-#pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      const int j = (w - first) & (kAttWarps - 1);
-      load[w] += solo ? (j == 0 ? s.count : 0) : (s.count - j + kAttWarps - 1) / kAttWarps;
-    }
+    first = next;
+    next = (next + (solo ? 1 : s.count)) & (kAttWarps - 1);
   }
 };
 
 // Moves to the next segment that has tiles; false: there is none.
 template <int KT>
-__device__ __forceinline__ bool att_next(const AttendArgs &a, AttSeg &s, int groups) {
+__device__ __forceinline__ bool att_next(const AttendArgs &a, AttSeg &s, int groups, int blocks) {
   do {
     if (s.left == 0) return false;
+    if (++s.blk == blocks) {
+      s.blk = 0;
+      ++s.kh;
+    }
     if (++s.hg == groups) {
-      s.hg = 0;
+      s.hg = s.kh = 0;
       do {  // (a later sequence holds the units that are left)
         att_visible(a, ++s.b, s.n, s.lo);
       } while (s.n == 0);
@@ -363,11 +359,13 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
   if (g0 < g1) {
     seg.b = s_start[0];
     seg.hg = s_start[1];
+    seg.kh = seg.hg / p.blocks;
+    seg.blk = seg.hg - seg.kh * p.blocks;
     att_visible(a, seg.b, seg.n, seg.lo);
     seg.total = att_tiles<KT>(seg.n, seg.lo);
     att_segment<KT>(seg, s_start[2], g1 - g0);
   }
-  const bool any = g0 < g1 && (seg.count > 0 || att_next<KT>(a, seg, groups));  // tiles in the range
+  const bool any = g0 < g1 && (seg.count > 0 || att_next<KT>(a, seg, groups, p.blocks));  // tiles in the range
 
   AttTeam team;
   if (warp >= kAttWarps) {
@@ -381,7 +379,7 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
       int ids_b = -1, ids_base = 0, ids = -1;  // this lane's page number, for tiles of ids_b from ids_base on
       bool ok = true;
       for (int k = 0; ok; ++k) {  // segments
-        const int kh = seg.hg / p.blocks, h0 = kh * group + (seg.hg % p.blocks) * C::kHeads;
+        const int kh = seg.kh, h0 = kh * group + seg.blk * C::kHeads;
         const int heads = min(C::kHeads, (kh + 1) * group - h0), qb = k % C::NQ;
         if (loader == 0) {
           if (!att_wait(att_smem(&q_empty[qb]), ((uint32_t)(k / C::NQ) & 1u) ^ 1u, kAttTries)) break;
@@ -437,7 +435,7 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
           __syncwarp();
           if (lane == w) ++given;
         }
-        if (!att_next<KT>(a, seg, groups)) break;
+        if (!att_next<KT>(a, seg, groups, p.blocks)) break;
       }
     }
     __syncthreads();  // the consumers are done
@@ -492,10 +490,10 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
     if (team.solo && turn != 0) {  // another warp's
       if (lane == 0 && !dead)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&q_empty[qb])) : "memory");
-      if (!att_next<KT>(a, seg, groups)) break;
+      if (!att_next<KT>(a, seg, groups, p.blocks)) break;
       continue;
     }
-    const int kh = seg.hg / p.blocks, h0 = kh * group + (seg.hg % p.blocks) * C::kHeads;
+    const int kh = seg.kh, h0 = kh * group + seg.blk * C::kHeads;
     const int heads = min(C::kHeads, (kh + 1) * group - h0);
     const float sc = a.scale * (E4M3 && a.kv.k_scale ? __ldg(a.kv.k_scale + kh) : 1.0f) * 1.4426950408889634f;
 
@@ -784,7 +782,7 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
       // (the unit of the item's last tile)
       shared.parts = split.cta_of(g1 - seg.left - seg.units - seg.unit + kAttItemCost + seg.total - 1) - c + 1;
     }
-    if (!att_next<KT>(a, seg, groups)) break;
+    if (!att_next<KT>(a, seg, groups, p.blocks)) break;
     // red and s_ml are free again
     if (team.solo) __syncwarp();
     else asm volatile("bar.sync 1, %0;" ::"n"(kAttConsumers) : "memory");
