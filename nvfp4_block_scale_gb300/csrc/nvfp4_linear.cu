@@ -37,10 +37,11 @@ namespace nvfp4 {
 
 // This kernel takes up to 16 vectors, and W up to so many blocks of 16 x 128
 // per CTA of a full wave.  Measured against the tcgen05 product (us): 1 vector
-// 4096 x 4096 (27 blocks) 10.2 against 12.1, 14336 x 4096 (94) 17.5 against
-// 17.9; 8 vectors 24 against 17.9 there; 16 vectors 1024 x 4096 (7) 9.2 against
-// 9.4, 4096 x 4096 14.5 against 12.4.
-constexpr int kLinVecs = 16, kLinBlocks8 = 32, kLinBlocks16 = 8;
+// 4096 x 4096 (27 blocks) 9.0 against 12.1, 8192 x 4096 (54) 13.0 against 13.9,
+// 14336 x 4096 (94) 17.9 against 17.6; 8 vectors 4096 x 11008 (72) 16.3 against
+// 16.2; 16 vectors 2048 x 4096 (13) 9.0 against 11.0, 4096 x 6144 (40) 13.3 either
+// way, 8192 x 4096 14.8 against 14.2.
+constexpr int kLinVecs = 16, kLinBlocks8 = 72, kLinBlocks16 = 40;
 constexpr int kLinWarps = 8;
 constexpr int kLinThreads = kLinWarps * 32;
 constexpr int kLinDepth = 4;       // steps in flight per warp
@@ -290,26 +291,35 @@ namespace {
 
 int lin_nt(int batch) { return batch <= 8 ? 1 : 2; }
 
-// The cut into rectangles with the least estimated time per wave of 2 CTAs per
-// SM, in bytes of weights that a CTA reads meanwhile: the rectangle itself, x
-// (read by every CTA), and, with several ranges, their sums' way through
-// L2.  false: the tcgen05 product runs.
+// The cut into rectangles, for one wave of 2 CTAs per SM where it fits: whole
+// rows, or eight column ranges (more where those would leave three quarters of
+// the CTAs without work, or x of a range does not fit).  Both have an estimated
+// cost in bytes of weights that a CTA reads meanwhile: the rectangle itself, x
+// (which all CTAs read through one L2), and the second launch that adds the
+// ranges' sums.  Measured (us): 8 vectors 4096 x 1024 8.4 as whole rows, 6.2 as
+// eight ranges; 1 vector 2048 x 8192 12.2 and 9.0; 8 vectors 1000 x 1008 4.2 and
+// 5.0; 1 vector 11008 x 1024 7.7 and 8.7.  Other numbers of ranges lie within 3 %
+// of the better of the two or behind it (4 vectors 4096 x 4096: 1, 2, 4, 6, 8, 12
+// and 16 ranges take 11.7, 10.4, 9.5, 10.4, 9.2, 11.3 and 10.9).  false: the
+// tcgen05 product runs.
 bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {
   const int nt = lin_nt(batch), ctas = 2 * sms;
   const int64_t steps = (cols + 127) / 128, tiles = (rows + 15) / 16;
   if (batch > kLinVecs || tiles > (int64_t)ctas * kLinBlocks8 ||
       steps * tiles > (int64_t)ctas * (batch <= 8 ? kLinBlocks8 : kLinBlocks16))
     return false;
+  int64_t many = 8;
+  while (lin_smem(nt, (steps + many - 1) / many, 1) > kLinSmem || (4 * tiles * many <= ctas && 4 * many <= steps)) many *= 2;
   int64_t least = -1;
-  for (const int64_t ranges : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64, 96}) {
-    if (ranges > steps) break;
+  for (const int64_t ranges : {int64_t(1), std::min(many, steps)}) {
     const int64_t ms = (steps + ranges - 1) / ranges;
     const int64_t most = (kLinSmem - lin_smem(nt, ms, 0)) / (nt * 512);  // tiles that fit
     if (most < 1) continue;
     int64_t groups = std::min<int64_t>(tiles, std::max<int64_t>(1, ctas / ranges));
     if ((tiles + groups - 1) / groups > most) groups = (tiles + most - 1) / most;
     const int64_t mt = (tiles + groups - 1) / groups, waves = (groups * ranges + ctas - 1) / ctas;
-    const int64_t cost = waves * (mt * ms * 1152 + ms * batch * 500 + (ranges > 1 ? 44000 + mt * nt * 512 * (2 + ranges / 4) : 0));
+    const int64_t cost = waves * (mt * ms * 1152 + ms * batch * 1000 * std::min<int64_t>(groups * ranges, ctas) / ctas) +
+                         (ranges > 1 ? 22000 : 0);
     if (least < 0 || cost < least) {
       least = cost;
       *best = LinPlan{(int)steps, (int)tiles, (int)ranges, (int)groups, (int)ms, (int)mt};
