@@ -6,7 +6,12 @@
 //
 // Bound: HBM.  Every visible key and value is read once; the products are
 // 4 flop per element and query head of the group, far below the tensor cores'
-// rate, so the work is to keep enough copies in flight.
+// rate, so the work is to keep enough copies in flight.  Measured: 16 x 32768
+// tokens (64 heads on 8 of 128, bf16) 308 us, 7.0 TB/s; 3 x 65536 (E4M3) 70 us, 5.8
+// TB/s; 61 ragged sequences of up to 2048 (32 heads on 8, bf16) 48 us, 5.4 TB/s.
+// Short items are bound by their instructions and their latency instead: 256
+// sequences, window 128, 16 E4M3 heads of 64 take 29 us, where an item of 4 tiles is
+// 3000 warp instructions over all roles; one sequence of 517 tokens takes 8.6 us.
 //
 // Work split: an item is one sequence and one block of up to 8 NT query heads
 // that share a cache head.  Its visible tokens are cut into tiles of KT, and the
@@ -18,11 +23,11 @@
 // sum and output of its own (no barrier inside a segment), and meet in shared
 // memory at the segment's end, which costs about 4000 clocks; so an item of few
 // tiles is one warp's alone: of as many as its ring holds, because the loads of
-// more would hold up the other warps' (with up to 8 tiles in rings of 2, 61
-// ragged sequences took 73 us instead of 57).  An item inside one CTA is
-// finished there; the parts of a longer one go to the workspace, where a second launch
-// (k_attend_join) adds them in CTA order, so that results do not depend on
-// timing.  (When the CTA that came last added them, behind a fence and a
+// more would hold up the other warps' where two share a loading warp, and leave
+// them idle at a range's end (with up to 12 tiles in rings of 2, 256 x 300 tokens of
+// bf16 heads of 128 took 45 us instead of 40).  An item inside one CTA is finished
+// there; the parts of a longer one go to the workspace, where a second launch
+// (k_attend_join) adds them in CTA order, so that results do not depend on timing.  (When the CTA that came last added them, behind a fence and a
 // counter, it cost up to 14 us under load: 61 ragged sequences of up to 2048
 // tokens took 62 us.)
 //
@@ -189,16 +194,19 @@ __device__ __forceinline__ int64_t att_div(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The even split of T tiles over G CTAs: c T / G.
+// The even split of T tiles over G CTAs (at most T): the first T mod G take one more.
 struct AttSplit {
-  int64_t q, T;  // T / G
-  int r, G;      // T mod G
-  __device__ __forceinline__ AttSplit(int64_t T_, int G_) : T(T_), G(G_) {
+  int64_t q;  // T / G
+  int r;      // T mod G
+  __device__ __forceinline__ AttSplit(int64_t T, int G) {
     q = att_div(T, G);
     r = (int)(T - q * G);
   }
-  __device__ __forceinline__ int64_t first(int c) const { return c * q + c * r / G; }
-  __device__ __forceinline__ int cta_of(int64_t g) const { return (int)att_div((g + 1) * G - 1, T); }
+  __device__ __forceinline__ int64_t first(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int cta_of(int64_t g) const {
+    const int64_t longer = r * (q + 1);
+    return (int)(g < longer ? att_div(g, q + 1) : r + att_div(g - longer, q));
+  }
 };
 
 // A position in a CTA's range: a segment (tiles [first, first + count) of
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
   // full: a tile has landed; empty: it has been read; q_*: the queries of a segment
   __shared__ __align__(8) uint64_t full[kAttWarps * S], empty[kAttWarps * S], q_full[C::NQ], q_empty[C::NQ];
   __shared__ int64_t s_sum[C::kThreads / 32];
-  __shared__ int s_start[3], s_fail;
+  __shared__ int s_start[6], s_fail;
   __shared__ float s_ml[kAttWarps][C::kHeads][2];
   const AttendArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -299,18 +307,16 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
   const uint32_t qs_smem = base + C::kRing + C::kRed;
   pdl_launch_dependents();  // k_attend_join waits for the whole grid all the same
 
-  if (tid == 0) {
-    for (int i = 0; i < kAttWarps * S; ++i) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&full[i])) : "memory");
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&empty[i])) : "memory");
-    }
-    for (int i = 0; i < C::NQ; ++i) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&q_full[i])) : "memory");
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(att_smem(&q_empty[i])), "r"(kAttWarps) : "memory");
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_fail = 0;
+  for (int i = tid; i < kAttWarps * S; i += C::kThreads) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&full[i])) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&empty[i])) : "memory");
   }
+  if (tid < C::NQ) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(att_smem(&q_full[tid])) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(att_smem(&q_empty[tid])), "r"(kAttWarps) : "memory");
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (tid == 0) s_fail = 0;
 
   // ---- all tiles, this CTA's range of them, and the item where it begins: a
   // run of sequences per thread
@@ -354,6 +360,9 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
     s_start[0] = seg.b;
     s_start[1] = (int)att_div(rem, att_units(seg.total));
     s_start[2] = (int)(rem - (int64_t)s_start[1] * att_units(seg.total));
+    s_start[3] = seg.n;
+    s_start[4] = seg.lo;
+    s_start[5] = seg.total;
   }
   __syncthreads();
   if (g0 < g1) {
@@ -361,8 +370,9 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
     seg.hg = s_start[1];
     seg.kh = seg.hg / p.blocks;
     seg.blk = seg.hg - seg.kh * p.blocks;
-    att_visible(a, seg.b, seg.n, seg.lo);
-    seg.total = att_tiles<KT>(seg.n, seg.lo);
+    seg.n = s_start[3];
+    seg.lo = s_start[4];
+    seg.total = s_start[5];
     att_segment<KT>(seg, s_start[2], g1 - g0);
   }
   const bool any = g0 < g1 && (seg.count > 0 || att_next<KT>(a, seg, groups, p.blocks));  // tiles in the range

@@ -9,7 +9,7 @@
 // Bound: HBM.  Each input is read once and each output written once with 16-
 // or 8-byte accesses; the cosines and sines of a token are loaded once per
 // thread and serve all of the heads that it handles.  8192 tokens (bf16 rows of
-// 32 + 2 x 8 heads of 128 into an E4M3 cache) take 54.6 us, 5.9 TB/s; 3001 (bf16,
+// 64 + 2 x 8 heads of 128 into an E4M3 cache) take 54.6 us, 5.9 TB/s; 3001 (bf16,
 // heads of 256) 14.9 us, 5.0 TB/s; one 1.9 us, which is a launch.
 //
 // Work split: a thread handles one 16-dimension unit of several heads of one

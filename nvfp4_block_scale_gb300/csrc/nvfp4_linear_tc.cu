@@ -16,6 +16,13 @@
 //     weights in flight meanwhile.
 //   - bf16 weights take five, and x is read as it is, in one launch.
 //
+// Bound: up to 64 vectors nominally HBM, in fact the set-up and a step's fixed
+// cost; at 256 vectors the tensor pipe.  Measured: 13 vectors 14336 x 4096 17.7 us
+// (1.9 TB/s; of a CTA's 28000 clocks 2200 pass until it has its tensor memory,
+// 6000 until the first codes are there, 16000 over 24 steps, 2000 from the last
+// MMA to its end); 16 vectors 8192 x 28672 37 us (3.6 TB/s, 540 clocks a step); 128
+// vectors 50 us; 256 vectors 80 us (1.50 PFLOP/s, the tensor pipe 78 % busy).
+//
 // Work: row tiles of 128 by column steps of 128.  With `tiles` tiles on G CTAs
 // (one per SM), each CTA takes floor(tiles / G) whole tiles; the steps of the
 // tiles left over are cut into G equal contiguous ranges, which a CTA does
@@ -62,7 +69,12 @@ constexpr int kLtGroups = 4;       // of producers
 // by the producers 80 B per row: 64 of codes, 12 of scales
 constexpr uint32_t kLtSlot = 10240;
 constexpr int kLtDyn = 227 * 1024 - 2048;
-constexpr int kLtBfSteps = 24;     // steps per CTA up to which bf16 operands are faster (see lt_plan)
+// Steps per CTA up to which the operands are bf16.  24 vectors take (us, f16 and
+// bf16) 4096 x 4096 (7 steps) 12.3 and 12.3, 14336 x 4096 (24) 17.6 and 18.5, 8192 x
+// 8192 (27) 18.2 and 19.3, 8192 x 28672 (94) 38.3 and 43.3; f16 is a launch more, which
+// costs a program that does not capture its calls 2 us.  (Above 128 vectors
+// the MMAs hide the producers, and it is always bf16.)
+constexpr int kLtBfSteps = 24;
 
 // CAP: vectors that a launch's shared and tensor memory are laid out for.
 template <int CAP>
