@@ -25,8 +25,8 @@
 //
 // Work: row tiles of 128 by column steps of 128.  With `tiles` tiles on G CTAs
 // (one per SM), each CTA takes floor(tiles / G) whole tiles; the steps of the
-// tiles left over are cut into G equal contiguous ranges, which a CTA does
-// first.  The part of a tile inside a CTA is a segment with an accumulator of
+// tiles left over are cut into equal contiguous ranges of at least one step, one
+// per CTA, which does it first.  The part of a tile inside a CTA is a segment with an accumulator of
 // its own.  A whole tile is finished by its CTA; the parts of a shared one meet
 // in the workspace, where a second launch (k_linear_join) adds them in CTA
 // order with all SMs: when the last CTA of a tile did it, four parts of a tile
@@ -238,15 +238,19 @@ __device__ __forceinline__ void lt_weights(const uint4 &c, uint32_t s, uint32_t 
   }
 }
 
+// CTAs 0 .. lt_sharers - 1 have steps of the shared tiles, each at least one
+// (so that every part that the join adds has been written).
+__host__ __device__ __forceinline__ int64_t lt_sharers(const LtArgs &p, int64_t G) { return p.R * p.K < G ? p.R * p.K : G; }
+
 // The CTAs c0 .. c0 + n - 1 that share tile t.
 struct LtParts {
   int64_t c0;
   int n;
 };
-__device__ __forceinline__ LtParts lt_parts(const LtArgs &p, int64_t t, int64_t T, int64_t G) {
+__device__ __forceinline__ LtParts lt_parts(const LtArgs &p, int64_t t, int64_t T, int64_t GS) {
   LtParts q;
-  q.c0 = tc_cta_of(t * p.K, T, G);
-  q.n = (int)(tc_cta_of((t + 1) * p.K - 1, T, G) - q.c0) + 1;
+  q.c0 = tc_cta_of(t * p.K, T, GS);
+  q.n = (int)(tc_cta_of((t + 1) * p.K - 1, T, GS) - q.c0) + 1;
   return q;
 }
 // Adds the parts of rows r8 .. r8 + 7 of tile t and vector b in CTA order
@@ -294,8 +298,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = tc_smem(dsm), base = (raw + 1023u) & ~1023u;  // swizzle atoms need 1024-byte alignment
   uint8_t *ring = dsm + (base - raw) + SX * C::kXStage;
-  const int64_t G = gridDim.x, c = blockIdx.x, T = p.R * p.K;
-  const int64_t g0 = tc_first_step(c, T, G), g1 = tc_first_step(c + 1, T, G);  // of the shared tiles' steps
+  const int64_t G = gridDim.x, c = blockIdx.x, T = p.R * p.K, GS = lt_sharers(p, G);
+  const int64_t g0 = c < GS ? tc_first_step(c, T, GS) : T, g1 = c < GS ? tc_first_step(c + 1, T, GS) : T;  // of the shared tiles' steps
   const int nr = (int)(g1 - g0), n = nr + p.W * p.K;                           // steps: shared ones first
   const int64_t t_first = g0 / p.K;
   const int nsh = nr > 0 ? (int)((g1 - 1) / p.K - t_first + 1) : 0, nseg = nsh + p.W;
@@ -706,7 +710,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
 }
 
 // The parts of the shared tiles, added in CTA order and finished.
-__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ LtArgs p, int64_t G) {
+__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ LtArgs p, int64_t GS) {
   pdl_wait();
   const int64_t T = p.R * p.K, per = (int64_t)p.a.batch * (kLtM / 8);
   const float alpha = *p.a.alpha;
@@ -714,7 +718,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ LtA
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.R * per; i += (int64_t)gridDim.x * 256) {
     const int64_t t = i / per;
     const int j = (int)(i - t * per), b = j / (kLtM / 8);
-    const LtParts q = lt_parts(p, t, T, G);
+    const LtParts q = lt_parts(p, t, T, GS);
     if (q.n > 1) lt_join(p, alpha, vec, q, t, b, j % (kLtM / 8) * 8, p.up ? __ldg(p.up + b) : 0);
   }
 }
@@ -777,7 +781,7 @@ cudaError_t lt_launch(const CUtensorMap &xm, const CUtensorMap &cm, const CUtens
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_linear_join, p, (int64_t)grid);
+  return cudaLaunchKernelEx(&cfg, k_linear_join, p, lt_sharers(p, grid));
 }
 
 template <int CAP, bool BF>

@@ -93,6 +93,23 @@ def test_codes_and_scales_off_their_natural_alignment(batch):
     _check(nv.linear(c8, s1, a, rows, cols, x), (c, s, a), x)
 
 
+@pytest.mark.parametrize("rows,cols", [(301, 32), (301, 96), (130, 160), (301, 416), (129, 1056), (301, 2112), (200, 4224),
+                                       (70, 9632), (20500, 288), (39000, 32), (20500, 1056)])
+@pytest.mark.parametrize("batch,offset", [(24, 0), (33, 1), (70, 8), (130, 3)])
+def test_rows_of_scales_of_any_length(rows, cols, batch, offset):
+    """Rows of scales that begin at any byte, partial last steps, tiles shared
+    and whole; NaN bytes on both sides of the scales, where nothing may look."""
+    w, x = _weights(rows, cols, rows + cols + offset), _bf16((batch, cols), batch)
+    n = rows * cols // 16
+    around = torch.full((offset + n + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+    around[offset:offset + n] = w[1].view(torch.uint8).flatten()
+    w = (w[0], around[offset:offset + n].view(rows, cols // 16), w[2])
+    bias = _bf16((rows,), 5)
+    y = nv.linear(*w, rows, cols, x, bias=bias)
+    _check(y, w, x, bias=bias)
+    assert torch.equal(y, nv.linear(*w, rows, cols, x, bias=bias))
+
+
 def test_more_vectors_than_one_slice():
     rows, cols, batch = 136, 256, 600
     w, x, res = _weights(rows, cols, 50), _bf16((batch, cols), 51), _bf16((batch, rows), 52)
