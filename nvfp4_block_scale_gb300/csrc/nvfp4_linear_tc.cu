@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
   asm volatile("tcgen05.fence::after_thread_sync;");
   const uint32_t tmem = tmem_slot;
 
+  int hi = 0;  // loaders: stages or steps asked for, [0, hi)
   if (warp < kLtProducers / 32) {
     // ---- dequantize: step i to half i % P of A stage (i / P) % SA
     const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::kA + 64u * (grp % P);
@@ -569,7 +570,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
       if (!BF) pdl_wait();  // x in f16 is there
       const uint64_t tmap = reinterpret_cast<uint64_t>(&xmap);
       Place q = start;
-      int hi = 0;  // stages requested: [0, hi)
       const int stages = C::kOne ? (n + P - 1) / P : 2 * n;
 #pragma unroll 1
       for (int x = 0; x < stages; ++x) {
@@ -587,9 +587,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         }
         hi = x + 1;
       }
-      if (*vfail)  // let the loads that nothing has waited for land
-        for (int x = hi - SX > 0 ? hi - SX : 0; x < hi; ++x)  // (a shared phase may never complete: then the bounded wait outlasts the copy)
-          tc_drain(tc_smem(C::kOne ? &full_a[x % SX] : &full_x[x % SX]), (uint32_t)((x / SX) & 1));
     }
     __syncwarp();
   } else if (warp == kLtCodeWarp) {
@@ -597,7 +594,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     if (p.tma && lt_elect()) {
       const uint64_t cm = reinterpret_cast<uint64_t>(&cmap), sm = reinterpret_cast<uint64_t>(&smap);
       Place q = start;
-      int hi = 0;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, advance(q, 1)) {
         const int slot = i % D;
@@ -612,8 +608,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
                      ::"r"(dst + 8192u), "l"(sm), "r"((q.ks * 8) & ~15), "r"((int)(q.t * kLtM)), "r"(mb) : "memory");
         hi = i + 1;
       }
-      if (*vfail)
-        for (int i = hi - D > 0 ? hi - D : 0; i < hi; ++i) tc_drain(tc_smem(&ring_full[i % D]), (uint32_t)((i / D) & 1));
     }
     __syncwarp();
   }
@@ -697,7 +691,15 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
   asm volatile("tcgen05.fence::after_thread_sync;");
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   if (!BF) pdl_wait();
-  if (*vfail) {  // report the failure through every output of this CTA
+  if (*vfail) {
+    // Copies that nothing has waited for land first, whichever role gave up
+    // and when (a shared phase may never complete: then the bounded wait outlasts
+    // the copy).
+    if (warp == kLtXWarp)
+      for (int x = max(0, hi - SX); x < hi; ++x) tc_drain(tc_smem(C::kOne ? &full_a[x % SX] : &full_x[x % SX]), (uint32_t)((x / SX) & 1));
+    if (warp == kLtCodeWarp)
+      for (int i = max(0, hi - D); i < hi; ++i) tc_drain(tc_smem(&ring_full[i % D]), (uint32_t)((i / D) & 1));
+    // report the failure through every output of this CTA
     const float nan = __int_as_float(0x7FC00000);
     for (int k = 0; k < nseg; ++k)
       for (int i = tid; i < a.batch * kLtM; i += kLtThreads) {
