@@ -157,6 +157,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return r;
 }
 
+// Orders this thread's reads of shared memory before copies into it that other
+// threads start once they have been told: without it the last loads of a tile
+// could still be on their way when the next tile landed (one tile in a million
+// took dimensions 112 .. 127 of its values from the next one).
+__device__ __forceinline__ void att_reads_done() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // One thread of a converged warp, known as such to the compiler.
 __device__ __forceinline__ bool att_elect() {
   uint32_t e;
@@ -708,6 +714,7 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
           }
         }
       }
+      att_reads_done();
       __syncwarp();  // every lane has read the stage
       if (lane == 0 && !dead)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&empty[at])) : "memory");
@@ -720,6 +727,7 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
     // The queries go back only once products have used them: handed back right
     // behind the loads, 16 heads of 256 of a one-tile item were still being read
     // when the next copy landed.
+    att_reads_done();
     __syncwarp();
     if (lane == 0 && !dead)
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(att_smem(&q_empty[qb])) : "memory");

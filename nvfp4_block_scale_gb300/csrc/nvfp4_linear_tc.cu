@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
           lt_weights<BF>(*reinterpret_cast<const uint4 *>(src + ((j ^ sw) << 4)), (j < 2 ? sc.x : sc.y) >> (16 * (j & 1)), w);
           lt_st16(ta + 64u * P * st + 16u * j, w);
         }
-        // the slot just read takes step i + D
+        // the slot just read takes step i + D (its reads are ordered before the copy, which is another proxy's)
+        if (p.tma) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (p.tma) {
           if (lane == 0) mbar_arrive(tc_smem(&ring_empty[slot]));

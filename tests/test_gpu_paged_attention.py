@@ -115,6 +115,24 @@ def test_short_items_between_long_ones(kind, hq, hk, dim):
     assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
 
 
+@pytest.mark.parametrize("hk,dim,kind", [(3, 128, "bf16"), (8, 128, "bf16"), (5, 64, "bf16"), (8, 128, "e4m3")])
+def test_short_contexts_repeat_over_many_calls(hk, dim, kind):
+    """Tiles that follow one another quickly in the same shared memory: what a
+    warp still reads must not be the next tile (which took one call in 300)."""
+    rng = np.random.default_rng(hk)
+    lengths = rng.integers(0, 80, 330).tolist()
+    cache, q, table, n = _setup(lengths, hk, hk, dim, 64, kind, 31)
+    first = nv.paged_attention(cache, q, table, n, return_lse=True)
+    _check(cache, q, table, n, *first, which=set(range(0, 330, 11)))
+    wrong = torch.zeros(2, dtype=torch.int64, device="cuda")
+    space = nv.attention_workspace(cache, hk)
+    for _ in range(2000):
+        out, lse = nv.paged_attention(cache, q, table, n, return_lse=True, workspace=space)
+        wrong[0] += (out != first[0]).any()
+        wrong[1] += (lse != first[1]).any()
+    assert wrong.tolist() == [0, 0]
+
+
 def test_many_sequences():
     rng = np.random.default_rng(3)
     lengths = rng.integers(0, 60, 1500)
