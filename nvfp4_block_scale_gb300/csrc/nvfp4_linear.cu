@@ -4,9 +4,9 @@
 // Many vectors and large tensors go to the tcgen05 product
 // (nvfp4_linear_tc.cu).  The others are bound by latency, then by reading the
 // weights once (0.5625 B each), and run here, without tensor memory (1 vector
-// 4096 x 4096: 8.0 us, 1.2 TB/s; 2048 x 8192: 8.9 us; 8 vectors 4096 x 6144: 11.7 us;
-// a second launch in a stream costs 1 to 2 us of these, the first bytes' way
-// from HBM and a CTA's set-up another 3):
+// 4096 x 4096: 8.3 us, 1.1 TB/s, 9.6 with cold weights; 2048 x 8192: 8.9 us; 8
+// vectors 4096 x 6144: 11.7 us; a second launch in a stream costs 1 to 2 us of
+// these, the first bytes' way from HBM and a CTA's set-up another 3):
 //
 // Products: mma.sync m16n8k16 (bf16 x bf16 -> fp32), 16 rows of W by 8 vectors.
 // q * Delta is formed in registers, exactly: six significant bits between
@@ -299,12 +299,13 @@ int lin_nt(int batch) { return batch <= 8 ? 1 : 2; }
 // the CTAs without work, or x of a range does not fit).  Both have an estimated
 // cost in bytes of weights that a CTA reads meanwhile: the rectangle itself, x
 // (which all CTAs read through one L2), and the second launch that adds the
-// ranges' sums.  Measured (us): 8 vectors 4096 x 1024 8.4 as whole rows, 6.2 as
-// eight ranges; 1 vector 2048 x 8192 12.2 and 9.0; 8 vectors 1000 x 1008 4.2 and
-// 5.0; 1 vector 11008 x 1024 7.7 and 8.7.  Other numbers of ranges lie within 3 %
-// of the better of the two or behind it (4 vectors 4096 x 4096: 1, 2, 4, 6, 8, 12
-// and 16 ranges take 11.7, 10.4, 9.5, 10.4, 9.2, 11.3 and 10.9).  false: the
-// tcgen05 product runs.
+// ranges' sums, counted as the 2 us that it takes a program which does not
+// capture its calls (on the GPU it takes 1).  Measured (us on the GPU, whole rows
+// and eight ranges): 8 vectors 4096 x 1024 8.4 and 6.2; 1 vector 2048 x 8192 12.2
+// and 9.0, 4096 x 4096 9.6 and 9.1, 11008 x 1024 7.7 and 8.7; 8 vectors 1000 x 1008
+// 4.2 and 5.0.  Other numbers of ranges lie within 3 % of the better of the two or
+// behind it (4 vectors 4096 x 4096: 1, 2, 4, 6, 8, 12 and 16 ranges take 11.7,
+// 10.4, 9.5, 10.4, 9.2, 11.3 and 10.9).  false: the tcgen05 product runs.
 bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {
   const int nt = lin_nt(batch), ctas = 2 * sms;
   const int64_t steps = (cols + 127) / 128, tiles = (rows + 15) / 16;
@@ -322,7 +323,7 @@ bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {
     if ((tiles + groups - 1) / groups > most) groups = (tiles + most - 1) / most;
     const int64_t mt = (tiles + groups - 1) / groups, waves = (groups * ranges + ctas - 1) / ctas;
     const int64_t cost = waves * (mt * ms * 1152 + ms * batch * 1000 * std::min<int64_t>(groups * ranges, ctas) / ctas) +
-                         (ranges > 1 ? 22000 : 0);
+                         (ranges > 1 ? 44000 : 0);
     if (least < 0 || cost < least) {
       least = cost;
       *best = LinPlan{(int)steps, (int)tiles, (int)ranges, (int)groups, (int)ms, (int)mt};
