@@ -951,7 +951,7 @@ struct AttRun {
     while ((1 << p.piece_shift) < piece) ++p.piece_shift;
     // the tiles that the longest possible lengths have bound the grid
     const int64_t cap = a.kv.table_width << a.kv.page_shift;
-    const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, a.window + C::KT) : cap;
+    const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, std::min<int64_t>(a.window, cap) + C::KT) : cap;
     const int64_t tiles = (seen / C::KT + 1) * a.sequences * a.kv.kv_heads * p.blocks;
     const int grid = (int)std::min<int64_t>(grid_max, (tiles + kAttMinTiles - 1) / kAttMinTiles);
     p.shared = static_cast<AttShared *>(ws);

@@ -87,6 +87,17 @@ def test_windows(kind, window):
     _check(cache, q, table, n, *nv.paged_attention(cache, q, table, n, window=window, return_lse=True), window=window)
 
 
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 33, 2 ** 63 - 1])
+@pytest.mark.parametrize("hq,hk,dim,count", [(8, 8, 64, 601), (16, 2, 128, 81), (24, 1, 256, 7)])
+def test_windows_wider_than_any_context(hq, hk, dim, count, window):
+    """Any window >= 0 is accepted, and one that holds every token is none."""
+    lengths = np.random.default_rng(count).integers(0, 200, count)
+    cache, q, table, n = _setup(lengths, hq, hk, dim, 32, "bf16", 41)
+    want = nv.paged_attention(cache, q, table, n, return_lse=True)
+    got = nv.paged_attention(cache, q, table, n, window=window, return_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("hq,hk,dim", [(32, 8, 128), (4, 4, 64), (24, 1, 256)])
 def test_long_and_short_together(kind, hq, hk, dim):
