@@ -949,11 +949,12 @@ struct AttRun {
     p.blocks = (group + C::kHeads - 1) / C::kHeads;
     p.piece_shift = 0;
     while ((1 << p.piece_shift) < piece) ++p.piece_shift;
-    // the tiles that the longest possible lengths have bound the grid
+    // The units of the longest possible lengths bound the grid; so it never limits
+    // the kernel's G, and the order of the additions does not depend on the table's width.
     const int64_t cap = a.kv.table_width << a.kv.page_shift;
     const int64_t seen = a.window > 0 ? std::min<int64_t>(cap, std::min<int64_t>(a.window, cap) + C::KT) : cap;
-    const int64_t tiles = (seen / C::KT + 1) * a.sequences * a.kv.kv_heads * p.blocks;
-    const int grid = (int)std::min<int64_t>(grid_max, (tiles + kAttMinTiles - 1) / kAttMinTiles);
+    const int64_t items = (int64_t)a.sequences * a.kv.kv_heads * p.blocks, units = (seen / C::KT + 1 + kAttItemCost) * items;
+    const int grid = (int)std::min<int64_t>(grid_max, (units + kAttMinTiles - 1) / kAttMinTiles);
     p.shared = static_cast<AttShared *>(ws);
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + kAttMaxCtas * sizeof(AttShared));
     CUtensorMap m[2];
@@ -970,7 +971,7 @@ struct AttRun {
     }
     k_attend<D, E4M3, NT><<<grid, C::kThreads, C::kSmem, st>>>(m[0], m[1], p);
     const cudaError_t e = cudaGetLastError();
-    // the parts of split items; one CTA, or a CTA for every item's tiles, splits none
+    // the parts of split items; one CTA splits none
     if (e != cudaSuccess || grid == 1) return e;
     cudaLaunchAttribute at = {};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -982,8 +983,9 @@ struct AttRun {
     cfg.numAttrs = 1;
     // Small blocks fit beside the attention's CTAs and start at once; where
     // items are cut into many parts, large ones share the parts of a head
-    // (1 x 8192 tokens, 38 parts: 6 us with 256 threads, 4.5 with 1024)
-    const bool many = grid > 8 * a.sequences * a.kv.kv_heads * p.blocks;
+    // (1 x 8192 tokens, 38 parts: 6 us with 256 threads, 4.5 with 1024).  They
+    // add in different orders: the choice goes by the device and the number of items.
+    const bool many = grid_max > 8 * items;
     cfg.blockDim = dim3(many ? 1024 : 256);
     return cudaLaunchKernelEx(&cfg, many ? k_attend_join<E4M3, 1024> : k_attend_join<E4M3, 256>, p, D, C::kHeads, grid);
   }

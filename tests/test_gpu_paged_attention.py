@@ -237,6 +237,22 @@ def test_strided_pages_queries_and_tables():
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
+@pytest.mark.parametrize("count,n0,hq,hk,dim,page", [(1, 517, 32, 8, 128, 16), (1, 300, 8, 8, 64, 16), (3, 150, 8, 2, 128, 16),
+                                                     (2, 900, 16, 2, 256, 32), (5, 64, 8, 8, 128, 16), (40, 20, 8, 8, 128, 16),
+                                                     (1, 8192, 40, 1, 64, 64)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 100])
+def test_results_do_not_depend_on_the_tables_width(count, n0, hq, hk, dim, page, kind, window):
+    """The order of the additions goes by the lengths and the device only."""
+    cache, q, table, n = _setup([n0] * count, hq, hk, dim, page, kind, 42)
+    want = nv.paged_attention(cache, q, table[:, :-(-n0 // page)], n, window=window, return_lse=True)
+    for more in (1, 7, 60, 5000):
+        wide = torch.full((count, -(-n0 // page) + more), -1, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table[:, :wide.shape[1]]
+        got = nv.paged_attention(cache, q, wide, n, window=window, return_lse=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_lengths_beyond_the_table_are_clipped():
     cache, q, table, n = _setup([32, 32], 4, 2, 64, 16, "bf16", 19)
     cut = table[:, :2].contiguous()
