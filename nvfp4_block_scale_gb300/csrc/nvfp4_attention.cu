@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
         const int kh = seg.kh, h0 = kh * group + seg.blk * C::kHeads;
         const int heads = min(C::kHeads, (kh + 1) * group - h0), qb = k % C::NQ;
         if (loader == 0) {
-          if (!att_wait(att_smem(&q_empty[qb]), ((uint32_t)(k / C::NQ) & 1u) ^ 1u, kAttTries)) break;
+          // (a warp gives up as a whole: its lanes meet in the shuffles and elections below)
+          if (!__all_sync(0xFFFFFFFFu, att_wait(att_smem(&q_empty[qb]), ((uint32_t)(k / C::NQ) & 1u) ^ 1u, kAttTries))) break;
           if (att_elect()) {
             const uint32_t q_bar = att_smem(&q_full[qb]);
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + seg.b * a.q_stride + (int64_t)h0 * D;
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(AttCfg<D, E4M3, NT>::kThreads) k_attend(const 
           for (int x = 0; x < 4; ++x)
             if (x == 0 || pp > 1) page[x] = __shfl_sync(0xFFFFFFFFu, ids, ((t - ids_base) * pp + x) & 31);
           const int u = __shfl_sync(0xFFFFFFFFu, given, w), at = w * S + u % S;
-          if (!att_wait(att_smem(&empty[at]), ((uint32_t)(u / S) & 1u) ^ 1u, kAttTries)) {
+          if (!__all_sync(0xFFFFFFFFu, att_wait(att_smem(&empty[at]), ((uint32_t)(u / S) & 1u) ^ 1u, kAttTries))) {
             ok = false;
             break;
           }
