@@ -324,6 +324,20 @@ def _stream_ptr(stream):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream` (None: the current one): memory that this
+    stream itself last gave up, since work still running on another one may
+    hold what that one gave up; and kept from reuse until the current stream,
+    on which the caller goes on, has passed the point where it is dropped."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _check(status: int, what: str):
     if status != NVFP4_OK:
         raise Nvfp4Error(status, what)
@@ -342,9 +356,9 @@ def quantize(W, mode=MAX, iters: int = 0, out=None, stream=None):
         raise ValueError("W must be a contiguous 2-D bf16 CUDA tensor")
     rows, cols = W.shape
     if out is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=W.device)
-        scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=W.device)
-        alpha = torch.empty(1, dtype=torch.float32, device=W.device)
+        codes = _empty((rows, cols // 2), torch.uint8, W.device, stream)
+        scales = _empty((rows, cols // 16), torch.uint8, W.device, stream)
+        alpha = _empty(1, torch.float32, W.device, stream)
     else:
         codes, scales, alpha = out
     st = nvfp4_quantize(W.data_ptr(), rows, cols, int(mode), int(iters), codes.data_ptr(), scales.data_ptr(),
@@ -366,9 +380,9 @@ def quantize_grouped(Ws, mode=MAX, iters: int = 0, outs=None, stream=None):
             raise ValueError("every W must be a contiguous 2-D bf16 CUDA tensor")
         rows, cols = W.shape
         if outs is None:
-            o = (torch.empty((rows, cols // 2), dtype=torch.uint8, device=W.device),
-                 torch.empty((rows, cols // 16), dtype=torch.uint8, device=W.device),
-                 torch.empty(1, dtype=torch.float32, device=W.device))
+            o = (_empty((rows, cols // 2), torch.uint8, W.device, stream),
+                 _empty((rows, cols // 16), torch.uint8, W.device, stream),
+                 _empty(1, torch.float32, W.device, stream))
         else:
             o = outs[i]
         arr[i] = nvfp4_tensor(W.data_ptr(), rows, cols, o[0].data_ptr(), o[1].data_ptr(), o[2].data_ptr())
@@ -382,7 +396,7 @@ def dequantize(codes, scales, alpha, rows: int, cols: int, out=None, stream=None
     """Returns the bf16 CUDA tensor [rows, cols] that the NVFP4 tensor encodes."""
     import torch
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=codes.device)
+        out = _empty((rows, cols), torch.bfloat16, codes.device, stream)
     st = nvfp4_dequantize(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, out.data_ptr(),
                           _stream_ptr(stream))
     _check(st, "nvfp4_dequantize")
@@ -398,7 +412,7 @@ def gemv(codes, scales, alpha, rows: int, cols: int, x, out=None, stream=None):
     if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.shape[1] != cols:
         raise ValueError("x must be a contiguous bf16 CUDA tensor [batch, cols]")
     batch = x.shape[0]
-    y = out if out is not None else torch.empty((batch, rows), dtype=torch.float32, device=x.device)
+    y = out if out is not None else _empty((batch, rows), torch.float32, x.device, stream)
     _check(nvfp4_gemv(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, x.data_ptr(), batch,
                       y.data_ptr(), _stream_ptr(stream)), "nvfp4_gemv")
     return y
@@ -412,21 +426,17 @@ def gemm(codes, scales, alpha, rows: int, cols: int, x, out=None, stream=None):
     if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.shape[1] != cols:
         raise ValueError("x must be a contiguous bf16 CUDA tensor [batch, cols]")
     batch = x.shape[0]
-    y = out if out is not None else torch.empty((batch, rows), dtype=torch.float32, device=x.device)
+    y = out if out is not None else _empty((batch, rows), torch.float32, x.device, stream)
     _check(nvfp4_gemm(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, x.data_ptr(), batch,
                       y.data_ptr(), _stream_ptr(stream)), "nvfp4_gemm")
     return y
 
 
-def _on(device, stream, *made):
-    """The stream to launch on; tensors made here for a stream other than the
-    current one are kept from reuse until that stream has passed this point."""
+def _on(device, stream):
+    """The handle of the stream to launch on."""
     import torch
     if stream is None:
         return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -497,14 +507,13 @@ def linear(codes, scales, alpha, rows: int, cols: int, x, bias=None, activation=
         gp, gs = _rows_of(gate, batch, rows, "gate")
     if residual is not None:
         rp, rs = _rows_of(residual, batch, rows, "residual")
-    made = None
     if out is None:
-        out = made = torch.empty((batch, rows), dtype=torch.bfloat16, device=x.device)
+        out = _empty((batch, rows), torch.bfloat16, x.device, stream)
     yp, ys = _rows_of(out, batch, rows, "out")
     wp, wb = _space(workspace)
     ep = nvfp4_epilogue(bp, gp, gs, rp, rs, ACTIVATIONS[activation])
     _check((_lib or load()).nvfp4_linear(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, xp, xs, batch,
-                                         ep, yp, ys, wp, wb, _on(x.device, stream, made)), "nvfp4_linear")
+                                         ep, yp, ys, wp, wb, _on(x.device, stream)), "nvfp4_linear")
     return out
 
 
@@ -591,15 +600,15 @@ def kv_append(cache: KVCache, qkv, q_heads: int, seq, pos, table, cos_sin=None, 
             raise ValueError("cos_sin must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
         positions, rotary = cos_sin.shape
         cp = cos_sin.data_ptr()
-    shape, made = (tokens, q_heads, dim), None
+    shape = (tokens, q_heads, dim)
     if out is None:
-        out = made = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        out = _empty(shape, torch.bfloat16, cache.device, stream)
     elif out.dtype is not torch.bfloat16 or not out.is_cuda or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous bf16 CUDA tensor {list(shape)}")
     _check((_lib or load()).nvfp4_kv_append(cache.desc, qkv.data_ptr(), DTYPE_FP32 if kind is torch.float32 else DTYPE_BF16,
                                             qkv.stride(0) if tokens > 1 else width, tokens, q_heads, sp, pp, tp,
                                             sequences, pages, stride, cp, positions, rotary, bool(interleaved),
-                                            out.data_ptr(), _on(cache.device, stream, made)), "nvfp4_kv_append")
+                                            out.data_ptr(), _on(cache.device, stream)), "nvfp4_kv_append")
     return out
 
 
@@ -627,25 +636,25 @@ def paged_attention(cache: KVCache, q, table, lengths, scale=None, window: int =
     if sequences != n:
         raise ValueError("table must have one row per sequence")
     lp = _ints(lengths, n, "lengths")
-    made = lse = None
+    lse = None
     if out is None:
-        out = made = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        out = _empty(shape, torch.bfloat16, cache.device, stream)
     elif out.dtype is not torch.bfloat16 or not out.is_cuda or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 CUDA tensor shaped like q")
     if return_lse:
-        lse = torch.empty((n, heads), dtype=torch.float32, device=cache.device)
+        lse = _empty((n, heads), torch.float32, cache.device, stream)
     wp, wb = _space(workspace)
     _check((_lib or load()).nvfp4_paged_attention(
         cache.desc, q.data_ptr(), strides[0] if n > 1 else heads * dim, n, heads, lp, tp, pages, stride,
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wb,
-        _on(cache.device, stream, made, lse)), "nvfp4_paged_attention")
+        _on(cache.device, stream)), "nvfp4_paged_attention")
     return (out, lse) if return_lse else out
 
 
 def swizzle_scales(scales, rows: int, cols: int, stream=None):
     """The [rows, cols/16] scales in the tensor-core tile layout (flat uint8)."""
     import torch
-    out = torch.empty(nvfp4_swizzled_scales_bytes(rows, cols), dtype=torch.uint8, device=scales.device)
+    out = _empty(nvfp4_swizzled_scales_bytes(rows, cols), torch.uint8, scales.device, stream)
     _check(nvfp4_swizzle_scales(scales.data_ptr(), rows, cols, out.data_ptr(), _stream_ptr(stream)),
            "nvfp4_swizzle_scales")
     return out
@@ -653,13 +662,13 @@ def swizzle_scales(scales, rows: int, cols: int, stream=None):
 
 def encode_e2m1(v, stream=None):
     import torch
-    out = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
+    out = _empty(v.shape, torch.uint8, v.device, stream)
     _check(nvfp4_encode_e2m1(v.data_ptr(), v.numel(), out.data_ptr(), _stream_ptr(stream)), "nvfp4_encode_e2m1")
     return out
 
 
 def encode_e4m3(v, stream=None):
     import torch
-    out = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
+    out = _empty(v.shape, torch.uint8, v.device, stream)
     _check(nvfp4_encode_e4m3(v.data_ptr(), v.numel(), out.data_ptr(), _stream_ptr(stream)), "nvfp4_encode_e4m3")
     return out
