@@ -224,9 +224,9 @@ int nvfp4_gemm(const uint8_t *codes, const uint8_t *scales, const float *alpha, 
  *          elements apart (>= rows).  y may be the residual or the gate
  *          itself (same address and stride).
  *   workspace  device, 256-byte aligned, of workspace_bytes >=
- *          nvfp4_linear_workspace_bytes(rows, cols, batch) bytes, or NULL:
- *          then the library's pool provides it.  A caller's workspace needs no
- *          preparation and holds nothing from one call to the next; calls that
+ *          nvfp4_linear_workspace_bytes(rows, cols, batch) bytes, which serve
+ *          every smaller batch of the shape too, or NULL: then the library's
+ *          pool provides it.  A caller's workspace needs no preparation and holds nothing from one call to the next; calls that
  *          may overlap on the GPU need workspaces of their own.
  *   stream cudaStream_t.
  * Returns an nvfp4_status.  nvfp4_linear_workspace_bytes returns -1 for an

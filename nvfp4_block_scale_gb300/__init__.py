@@ -474,8 +474,8 @@ def _rows_of(t, batch: int, width: int, what: str):
 
 
 def linear_workspace(rows: int, cols: int, batch: int, device="cuda"):
-    """A workspace for linear() of this shape, kept by the caller from call to
-    call (one per stream that such calls run on)."""
+    """A workspace for linear() of this shape and up to `batch` vectors, kept by
+    the caller from call to call (one per stream that such calls run on)."""
     return _workspace(nvfp4_linear_workspace_bytes(rows, cols, batch), device)
 
 

@@ -585,7 +585,13 @@ int64_t nvfp4_linear_workspace_bytes(int64_t rows, int64_t cols, int64_t batch) 
   if (check_shape(rows, cols) != NVFP4_OK || batch < 0) return -1;
   DevInfo *d = nullptr;
   if (device_info(&d) != NVFP4_OK) return -1;
-  return rows == 0 || cols == 0 || batch == 0 ? 0 : (int64_t)linear_need(rows, cols, batch, d->sms);
+  if (rows == 0 || cols == 0) return 0;
+  // Fewer vectors may need more (their tiles are cut into more parts), and a
+  // program sizes one workspace for its largest batch.
+  size_t need = 0;
+  for (int b = 1; b <= std::min<int64_t>(batch, kLinearSlice); ++b)
+    need = std::max(need, linear_workspace_bytes(rows, cols, b, d->sms));
+  return (int64_t)need;
 }
 
 int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t rows, int64_t cols,

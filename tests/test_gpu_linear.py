@@ -175,3 +175,17 @@ def test_workspace_serves_calls_of_several_shapes_and_capture():
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, p[3]) for o, p in zip(outs, plain + plain))
+
+
+@pytest.mark.parametrize("rows,cols,largest", [(1024, 4096, 64), (2048, 2048, 32), (1024, 28672, 64), (4096, 1024, 20),
+                                               (300, 2064, 300), (8192, 8192, 129), (28672, 8192, 256)])
+def test_a_workspace_for_the_largest_batch_serves_every_smaller_one(rows, cols, largest):
+    space = nv.linear_workspace(rows, cols, largest)
+    w = _weights(rows, cols, 90)
+    x = _bf16((largest, cols), 91)
+    need = [nv.nvfp4_linear_workspace_bytes(rows, cols, b) for b in range(largest + 1)]
+    assert need == sorted(need) and need[-1] <= space.numel()
+    for batch in range(1, largest + 1):
+        y = nv.linear(*w, rows, cols, x[:batch], workspace=space)
+        if batch in (1, 9, 17, largest // 2, largest):
+            assert torch.equal(y, nv.linear(*w, rows, cols, x[:batch]))
