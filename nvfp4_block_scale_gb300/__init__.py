@@ -456,12 +456,12 @@ def _workspace(nbytes: int, device):
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
-def _space(workspace):
+def _space(workspace, device):
     """Address and size of a caller's workspace, or nothing."""
     if workspace is None:
         return None, 0
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("a workspace must be a contiguous CUDA tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"a workspace must be a contiguous tensor on {device}")
     return workspace.data_ptr(), workspace.nbytes
 
 
@@ -493,8 +493,11 @@ def linear(codes, scales, alpha, rows: int, cols: int, x, bias=None, activation=
     batch = x.shape[0]
     xp, xs = _rows_of(x, batch, cols, "x")
     if codes.numel() * 2 != rows * cols or scales.numel() * 16 != rows * cols or not codes.is_contiguous() or \
-            not scales.is_contiguous():
-        raise ValueError("codes and scales must be contiguous and hold [rows, cols] elements")
+            not scales.is_contiguous() or codes.element_size() != 1 or scales.element_size() != 1 or \
+            not codes.is_cuda or not scales.is_cuda:
+        raise ValueError("codes and scales must be contiguous CUDA tensors of bytes that hold [rows, cols] elements")
+    if alpha.dtype is not torch.float32 or not alpha.is_cuda or alpha.numel() < 1:
+        raise ValueError("alpha must be an fp32 CUDA tensor [1]")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)}")
     bp = gp = rp = None
@@ -510,7 +513,7 @@ def linear(codes, scales, alpha, rows: int, cols: int, x, bias=None, activation=
     if out is None:
         out = _empty((batch, rows), torch.bfloat16, x.device, stream)
     yp, ys = _rows_of(out, batch, rows, "out")
-    wp, wb = _space(workspace)
+    wp, wb = _space(workspace, x.device)
     ep = nvfp4_epilogue(bp, gp, gs, rp, rs, ACTIVATIONS[activation])
     _check((_lib or load()).nvfp4_linear(codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(), rows, cols, xp, xs, batch,
                                          ep, yp, ys, wp, wb, _on(x.device, stream)), "nvfp4_linear")
@@ -643,7 +646,7 @@ def paged_attention(cache: KVCache, q, table, lengths, scale=None, window: int =
         raise ValueError("out must be a contiguous bf16 CUDA tensor shaped like q")
     if return_lse:
         lse = _empty((n, heads), torch.float32, cache.device, stream)
-    wp, wb = _space(workspace)
+    wp, wb = _space(workspace, cache.device)
     _check((_lib or load()).nvfp4_paged_attention(
         cache.desc, q.data_ptr(), strides[0] if n > 1 else heads * dim, n, heads, lp, tp, pages, stride,
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wb,

@@ -189,3 +189,36 @@ def test_a_workspace_for_the_largest_batch_serves_every_smaller_one(rows, cols, 
         y = nv.linear(*w, rows, cols, x[:batch], workspace=space)
         if batch in (1, 9, 17, largest // 2, largest):
             assert torch.equal(y, nv.linear(*w, rows, cols, x[:batch]))
+
+
+WRONG_TYPES = {
+    "fp64 alpha": lambda c, s, a: (c, s, a.double()),
+    "16-bit alpha": lambda c, s, a: (c, s, a.half()),
+    "no alpha": lambda c, s, a: (c, s, a[:0]),
+    "wide codes": lambda c, s, a: (c.int(), s, a),
+    "fp32 scales": lambda c, s, a: (c, s.view(torch.float8_e4m3fn).float(), a),
+}
+ON_THE_HOST = {
+    "codes": lambda c, s, a: (c.cpu(), s, a),
+    "scales": lambda c, s, a: (c, s.cpu(), a),
+    "alpha": lambda c, s, a: (c, s, a.cpu()),
+}
+
+
+@pytest.mark.parametrize("case", [*WRONG_TYPES, *ON_THE_HOST])
+def test_weights_of_another_type_or_on_the_host_are_refused(case):
+    w, x = _weights(32, 64, 92), _bf16((3, 64), 93)
+    with pytest.raises(ValueError):
+        nv.linear(*(WRONG_TYPES | ON_THE_HOST)[case](*w), 32, 64, x)
+
+
+def test_weights_under_other_names_for_bytes_are_taken():
+    (c, s, a), x = _weights(32, 64, 94), _bf16((3, 64), 95)
+    y = nv.linear(c, s, a, 32, 64, x)
+    assert torch.equal(y, nv.linear(c.flatten().view(torch.int8), s.view(torch.float8_e4m3fn), a[0], 32, 64, x))
+
+
+def test_a_workspace_on_the_host_is_refused():
+    w, x = _weights(32, 64, 96), _bf16((3, 64), 97)
+    with pytest.raises(ValueError):
+        nv.linear(*w, 32, 64, x, workspace=torch.empty(1 << 20, dtype=torch.uint8))
