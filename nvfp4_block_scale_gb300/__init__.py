@@ -60,7 +60,7 @@ class Nvfp4Error(RuntimeError):
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Loads the CUDA library (building it first if it is absent or stale)."""
-    global _lib, _raw_stream
+    global _lib
     if _lib is not None:
         return _lib
     if path is None:
@@ -124,7 +124,6 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_check_selftest.restype = ci
     L.nvfp4_status_string.argtypes = [ci]
     L.nvfp4_status_string.restype = ctypes.c_char_p
-    _raw_stream = _current_raw()
     _lib = L
     return L
 
@@ -434,10 +433,12 @@ def gemm(codes, scales, alpha, rows: int, cols: int, x, out=None, stream=None):
 
 def _on(device, stream):
     """The handle of the stream to launch on."""
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
-    return stream.cuda_stream
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        _raw_stream = _current_raw()
+    return _raw_stream(device.index)
 
 
 def _current_raw():
@@ -446,7 +447,8 @@ def _current_raw():
         from torch._C import _cuda_getCurrentRawStream
         return _cuda_getCurrentRawStream
     except ImportError:
-        return None
+        import torch
+        return lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
 def _workspace(nbytes: int, device):

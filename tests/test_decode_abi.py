@@ -1,6 +1,9 @@
 """The decode-step operators' entry points on the host: what they refuse,
 with which status, before touching the device."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -116,3 +119,10 @@ def test_struct_layouts_match_the_header():
     assert ctypes.sizeof(nv.nvfp4_kv_cache) == 72
     assert nv.nvfp4_linear_workspace_bytes(4, 24, 1) == -1
     assert nv.nvfp4_linear_workspace_bytes(4, 32, -1) == -1
+
+
+def test_loading_the_library_does_not_load_torch():
+    code = "import sys, nvfp4_block_scale_gb300 as nv; nv.load(); assert nv.nvfp4_status_string(0) == 'ok'; " \
+           "sys.exit('torch' in sys.modules)"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(nv.__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root).returncode == 0
