@@ -248,14 +248,14 @@ int take_workspace(void **ws, void **own, int64_t given, size_t need, const DevI
 
 enum { kTrAmax = 0, kTrQuantMax, kTrQuantFos, kTrCjsoInit, kTrCjsoIter, kTrDecoupled, kTrDequant, kTrEncode,
        kTrGroupAmax, kTrGroupQuantMax, kTrGroupQuantFos, kTrGemv, kTrSwizzle, kTrAmaxLdg, kTrGemmTc,
-       kTrGemmTcReduce, kTrLinear, kTrKvAppend, kTrAttend, kTrKinds };
+       kTrGemmTcReduce, kTrLinear, kTrLinearTcF16, kTrLinearTcBf16, kTrKvAppend, kTrAttend, kTrKinds };
 const char *const kTraceNames[kTrKinds] = {"k_amax_bulk",        "k_quant_max_fos<max>", "k_quant_max_fos<fos>",
                                            "k_cjso_sweep<init>",  "k_cjso_sweep<iter>",   "k_decoupled",
                                            "k_dequant",           "k_encode",             "k_group_amax",
                                            "k_group_quant<max>",  "k_group_quant<fos>",   "k_gemv",
                                            "k_swizzle_scales",   "k_amax_partials",      "k_gemm_tc",
-                                           "k_gemm_tc_reduce",   "k_linear",             "k_kv_append",
-                                           "k_attend"};
+                                           "k_gemm_tc_reduce",   "k_linear",             "k_linear_tc<f16>",
+                                           "k_linear_tc<bf16>",  "k_kv_append",          "k_attend"};
 
 struct TraceRec {
   int kind;
@@ -632,7 +632,9 @@ int nvfp4_linear(const uint8_t *codes, const uint8_t *scales, const float *alpha
                           ep.gate_stride, at(ep.residual, ep.residual_stride), ep.residual_stride, ep.activation,
                           const_cast<char *>(at(y, y_stride)), y_stride};
     TraceScope tr(kTrLinear, stream);
-    e = launch_linear(a, d->sms, workspace, first_tries(), stream);
+    LinearKernel took = kLinearRegisters;
+    e = launch_linear(a, d->sms, workspace, first_tries(), &took, stream);
+    tr.kind = kTrLinear + took;
   }
   const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);

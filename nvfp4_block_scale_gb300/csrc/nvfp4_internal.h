@@ -130,11 +130,13 @@ struct AttendArgs {
   float *lse;
   int first_tries;  // < 0: normal (test hook)
 };
+// The kernel that took a product, for the tracer.
+enum LinearKernel { kLinearRegisters = 0, kLinearTcF16, kLinearTcBf16 };
 size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
 cudaError_t prepare_linear_kernels();
-cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st);
+cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_tries, LinearKernel *took, cudaStream_t st);
 size_t linear_tc_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
-cudaError_t launch_linear_tc(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st);
+cudaError_t launch_linear_tc(const LinearArgs &a, int sms, void *ws, int first_tries, LinearKernel *took, cudaStream_t st);
 cudaError_t prepare_linear_tc_kernels();
 cudaError_t launch_kv_append(const AppendArgs &a, int sms, cudaStream_t st);
 size_t attend_workspace_bytes(const KvArgs &kv, int q_heads, int sms);

@@ -361,14 +361,15 @@ size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms) {
   return p.ranges == 1 ? 0 : (size_t)p.ranges * p.tiles * lin_nt(batch) * 512;
 }
 
-cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st) {
+cudaError_t launch_linear(const LinearArgs &a, int sms, void *ws, int first_tries, LinearKernel *took, cudaStream_t st) {
+  *took = kLinearRegisters;
   if (a.cols == 0) {
     k_linear_empty<<<(int)std::min<int64_t>((a.rows * a.batch + 255) / 256, 8 * sms), 256, 0, st>>>(a);
     return cudaGetLastError();
   }
   LinPlan plan;
   if (!lin_plan(a.rows, a.cols, a.batch, sms, &plan))
-    return launch_linear_tc(a, sms, ws, first_tries, st);
+    return launch_linear_tc(a, sms, ws, first_tries, took, st);
   const LinLaunch p = {a, plan, static_cast<float4 *>(ws), plan.steps / plan.ranges,
                        plan.steps % plan.ranges, plan.tiles / plan.groups, plan.tiles % plan.groups};
   const bool wide = a.cols % 32 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0 &&

@@ -798,10 +798,11 @@ size_t linear_tc_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms)
   return lt_plan(rows, cols, batch, sms).bytes;
 }
 
-cudaError_t launch_linear_tc(const LinearArgs &a, int sms, void *ws, int first_tries, cudaStream_t st) {
+cudaError_t launch_linear_tc(const LinearArgs &a, int sms, void *ws, int first_tries, LinearKernel *took, cudaStream_t st) {
   if (!g_lt_encode) return cudaErrorInitializationError;
   if (a.cols >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // a TMA coordinate
   const LtPlan q = lt_plan(a.rows, a.cols, a.batch, sms);
+  *took = q.bf ? kLinearTcBf16 : kLinearTcF16;
   char *w = static_cast<char *>(ws);
   const int64_t whole = q.tiles / q.G;
   if (whole * q.K >= (int64_t(1) << 30)) return cudaErrorInvalidValue;  // steps of a CTA
