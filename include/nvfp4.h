@@ -331,7 +331,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const void *qkv, int qkv_dtype,
  *     s_t = scale * k_scale * (q . k_t),  m = max s_t,  l = sum exp(s_t - m),
  *     out = v_scale / l * sum exp(s_t - m) v_t,   lse = m + ln l.
  *   Scores, maxima, sums and outputs are fp32; the weights exp(s_t - m) enter
- *   the products with V rounded to the 16-bit type of the products.  The order
+ *   the products with V with 16 significant bits (bf16 caches) or 11 (E4M3
+ *   caches).  The order
  *   of the additions depends on the lengths and the device only, so results
  *   repeat bit for bit.  An empty row (n <= 0) gives out = 0, lse = -inf, as
  *   does a row whose scores are all -inf.

@@ -144,6 +144,28 @@ def test_short_contexts_repeat_over_many_calls(hk, dim, kind):
     assert wrong.tolist() == [0, 0]
 
 
+@pytest.mark.parametrize("kind,bits", [("bf16", 16), ("e4m3", 11)])
+@pytest.mark.parametrize("hq,hk,dim", [(4, 2, 64), (8, 1, 128), (3, 1, 256), (12, 1, 64), (24, 1, 128), (16, 1, 256)])
+def test_weights_keep_their_bits(kind, bits, hq, hk, dim):
+    """Scores so small that their own error is far below a weight's rounding:
+    decode_ref.attend's bound with 2^-bits in place of 2^-8 for the weights (half
+    a unit of as many bits; two bf16 numbers hold a weight to 2^-16)."""
+    lengths = [2, 3, 5, 9, 16, 33, 70, 130, 300]
+    cache, q, table, n = _setup(lengths, hq, hk, dim, 16, kind, 43, scaled=False)
+    q.mul_(2.0 ** -5 if kind == "bf16" else 2.0 ** -11)
+    out, lse = nv.paged_attention(cache, q, table, n, return_lse=True)
+    g = hq // hk
+    for i, m in enumerate(lengths):
+        ids = table[i, :-(-m // 16)].long()
+        for h in range(hk):
+            k, v = (t.float()[ids, h].double().cpu().numpy().reshape(-1, dim)[:m] for t in (cache.k, cache.v))
+            qh = q[i, h * g:(h + 1) * g].double().cpu().numpy()
+            ro, rl, bo, bl = ref.attend(qh, k, v, dim ** -0.5)
+            mag = ref.attend(qh, k, np.abs(v), dim ** -0.5)[0]
+            assert ref.within(out[i, h * g:(h + 1) * g].double().cpu().numpy(), ro, bo - (2.0 ** -8 - 2.0 ** -bits) * mag), (i, h)
+            assert np.all(np.abs(lse[i, h * g:(h + 1) * g].double().cpu().numpy() - rl) <= bl)
+
+
 def test_many_sequences():
     rng = np.random.default_rng(3)
     lengths = rng.integers(0, 60, 1500)
