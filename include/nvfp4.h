@@ -205,7 +205,10 @@ int nvfp4_gemm(const uint8_t *codes, const uint8_t *scales, const float *alpha, 
  *   with fp32 accumulation and an fp32 epilogue, rounded once.  Unlike
  *   nvfp4_gemv and nvfp4_gemm the weights are not rounded to bf16 first:
  *   q * Delta has at most six significant bits, so it enters the products
- *   exactly, and alpha multiplies the finished sum.  The order of the
+ *   exactly, and alpha multiplies the finished sum.  x enters as it is, but
+ *   for large tensors and up to 128 vectors in f16, each vector scaled by a
+ *   power of two: its entries are exact down to 2^-27 of its largest, and those
+ *   below are off by at most 2^-38 of it.  The order of the
  *   additions is fixed by the shape and the device, so results repeat bit for
  *   bit.  (The method's pages quantize weights for such products; this is a
  *   consumer of the path.)
@@ -332,8 +335,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const void *qkv, int qkv_dtype,
  *     out = v_scale / l * sum exp(s_t - m) v_t,   lse = m + ln l.
  *   Scores, maxima, sums and outputs are fp32; the weights exp(s_t - m) enter
  *   the products with V with 16 significant bits (bf16 caches) or 11 (E4M3
- *   caches).  The order
- *   of the additions depends on the lengths and the device only, so results
+ *   caches).  The order of the additions depends on the lengths, the heads,
+ *   the window and the device only (not on the table's width), so results
  *   repeat bit for bit.  An empty row (n <= 0) gives out = 0, lse = -inf, as
  *   does a row whose scores are all -inf.
  * Arguments:
@@ -347,7 +350,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const void *qkv, int qkv_dtype,
  *           included; clipped to [0, table_width * page_size].
  *   table   as for nvfp4_kv_append.  Entries behind a sequence's last page are
  *           not read; an entry outside [0, pages) reads as zeros.
- *   scale   the score's factor (finite).  window >= 0.
+ *   scale   the score's factor (finite).  window >= 0 (0, or as long as the
+ *           longest sequence: every token).
  *   out     device, bf16, 16-byte aligned, [sequences][q_heads][head_dim]
  *           (written).
  *   lse     device, fp32, 4-byte aligned, [sequences][q_heads] (written), or

@@ -10,8 +10,12 @@
 // tokens (64 heads on 8 of 128, bf16) 308 us, 7.0 TB/s; 3 x 65536 (E4M3) 70 us, 5.8
 // TB/s; 61 ragged sequences of up to 2048 (32 heads on 8, bf16) 48 us, 5.4 TB/s.
 // Short items are bound by their instructions and their latency instead: 256
-// sequences, window 128, 16 E4M3 heads of 64 take 29 us, where an item of 4 tiles is
-// 3000 warp instructions over all roles; one sequence of 517 tokens takes 8.6 us.
+// sequences, window 128, 16 E4M3 heads of 64 take 30 us, where an item of 4 tiles is
+// 3000 warp instructions over all roles; one sequence of 517 tokens takes 8.4 us.
+// So are the large head blocks that leave one CTA per SM, with one consuming warp
+// per scheduler: 16 x 8192 tokens with 32 heads on one of 128 take 36 us in bf16 and
+// 30 in E4M3 (2.2 TB/s), with 16 on one of 256 38 and 33.  Heads of 256 in groups of
+// up to 8 (16 x 8192, 16 heads on 4) take 88 us, 6.1 TB/s, and 51 in E4M3, 5.3 TB/s.
 //
 // Work split: an item is one sequence and one block of up to 8 NT query heads
 // that share a cache head.  Its visible tokens are cut into tiles of KT, and the
@@ -27,9 +31,10 @@
 // them idle at a range's end (with up to 12 tiles in rings of 2, 256 x 300 tokens of
 // bf16 heads of 128 took 45 us instead of 40).  An item inside one CTA is finished
 // there; the parts of a longer one go to the workspace, where a second launch
-// (k_attend_join) adds them in CTA order, so that results do not depend on timing.  (When the CTA that came last added them, behind a fence and a
-// counter, it cost up to 14 us under load: 61 ragged sequences of up to 2048
-// tokens took 62 us.)
+// (k_attend_join) adds them in CTA order, so that results do not depend on
+// timing.  (When the CTA that came last added them, behind a fence and a counter,
+// it cost up to 14 us under load: 61 ragged sequences of up to 2048 tokens took
+// 62 us.)
 //
 // Loads: two or four more warps fill a ring of S tiles per consuming warp by TMA, across
 // segments (keys and values of a page as boxes of 128-byte rows, 128-byte

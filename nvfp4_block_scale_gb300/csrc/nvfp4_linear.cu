@@ -4,8 +4,8 @@
 // Many vectors and large tensors go to the tcgen05 product
 // (nvfp4_linear_tc.cu).  The others are bound by latency, then by reading the
 // weights once (0.5625 B each), and run here, without tensor memory (1 vector
-// 4096 x 4096: 8.3 us, 1.1 TB/s, 9.6 with cold weights; 2048 x 8192: 8.9 us; 8
-// vectors 4096 x 6144: 11.7 us; a second launch in a stream costs 1 to 2 us of
+// 4096 x 4096: 8.3 us, 1.1 TB/s, 10.0 with cold weights; 2048 x 8192: 7.9 and 9.1; 8
+// vectors 4096 x 6144: 10.3 and 12.7; a second launch in a stream costs 1 to 2 us of
 // these, the first bytes' way from HBM and a CTA's set-up another 3):
 //
 // Products: mma.sync m16n8k16 (bf16 x bf16 -> fp32), 16 rows of W by 8 vectors.
@@ -302,8 +302,11 @@ int lin_nt(int batch) { return batch <= 8 ? 1 : 2; }
 // ranges' sums, counted as the 2 us that it takes a program which does not
 // capture its calls (on the GPU it takes 1).  Measured (us on the GPU, whole rows
 // and eight ranges): 8 vectors 4096 x 1024 8.4 and 6.2; 1 vector 2048 x 8192 12.2
-// and 9.0, 4096 x 4096 9.6 and 9.1, 11008 x 1024 7.7 and 8.7; 8 vectors 1000 x 1008
-// 4.2 and 5.0.  Other numbers of ranges lie within 3 % of the better of the two or
+// and 9.0, 11008 x 1024 7.7 and 8.7; 8 vectors 1000 x 1008 4.2 and 5.0.  Where the
+// count decides (cold weights on the GPU, then called back to back): 1 vector
+// 4096 x 4096 10.0 and 10.0, 12.4 and 12.3; 8192 x 4096 14.5 and 14.1, 16.3 and 16.5;
+// 1024 x 4096 6.9 and 6.0, 8.8 and 10.8; 4 vectors 4096 x 1024 7.3 and 6.5, 9.4 and
+// 10.7: what a captured step would gain the others would lose.  Other numbers of ranges lie within 3 % of the better of the two or
 // behind it (4 vectors 4096 x 4096: 1, 2, 4, 6, 8, 12 and 16 ranges take 11.7,
 // 10.4, 9.5, 10.4, 9.2, 11.3 and 10.9).  false: the tcgen05 product runs.
 bool lin_plan(int64_t rows, int64_t cols, int batch, int sms, LinPlan *best) {

@@ -11,7 +11,7 @@
 //   - f16 weights take two instructions per pair to form, but x has to be
 //     turned into f16 first (k_linear_x, each vector scaled by a power of two
 //     that takes its largest entry into [2^13, 2^14): 8 bits stay exact down
-//     to 2^-27 of that entry, an entry below is off by at most 2^-39 of it).
+//     to 2^-27 of that entry, an entry below is off by at most 2^-38 of it).
 //     The product starts early (programmatic dependent launch) and has its
 //     weights in flight meanwhile.
 //   - bf16 weights take five, and x is read as it is, in one launch.
@@ -20,8 +20,8 @@
 // cost; at 256 vectors the tensor pipe.  Measured: 13 vectors 14336 x 4096 17.7 us
 // (1.9 TB/s; of a CTA's 28000 clocks 2200 pass until it has its tensor memory,
 // 6000 until the first codes are there, 16000 over 24 steps, 2000 from the last
-// MMA to its end); 16 vectors 8192 x 28672 37 us (3.6 TB/s, 540 clocks a step); 128
-// vectors 50 us; 256 vectors 80 us (1.50 PFLOP/s, the tensor pipe 78 % busy).
+// MMA to its end); 16 vectors 8192 x 28672 37 us (3.6 TB/s, 540 clocks a step), 52 us
+// with 28640 columns (no TMA for the codes); 128 vectors 50 us; 256 vectors 80 us (1.50 PFLOP/s, the tensor pipe 78 % busy).
 //
 // Work: row tiles of 128 by column steps of 128.  With `tiles` tiles on G CTAs
 // (one per SM), each CTA takes floor(tiles / G) whole tiles; the steps of the
