@@ -205,11 +205,16 @@ def fp32_peak_derived(sms: int, mhz: float) -> float:
     return sms * 128 * 2 * mhz * 1e6 / 1e12
 
 
+# sources that take no part in any recorded call: the decode-step operators
+OTHER_SOURCES = {"nvfp4_attention.cu", "nvfp4_epilogue.cuh", "nvfp4_kv.cu", "nvfp4_linear.cu", "nvfp4_linear_tc.cu"}
+
+
 def source_digest() -> str:
-    """Of the sources that hold the kernels of the recorded captures."""
+    """Of the sources that a recorded capture depends on: the kernels, and the
+    host code that sets their grids and cuts grouped calls into parts."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "nvfp4_block_scale_gb300", "csrc")
-    for f in ("nvfp4_decoupled.cu", "nvfp4_device.cuh", "nvfp4_kernels.cu"):
+    for f in sorted(set(os.listdir(csrc)) - OTHER_SOURCES):
         h.update(open(os.path.join(csrc, f), "rb").read())
     return h.hexdigest()[:16]
 

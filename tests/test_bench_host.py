@@ -3,6 +3,7 @@ an oracle it is timed against for its `cpu_baseline` (also a run whose modes
 are all consumers or allocation-free calls), the roofline rules, and the
 launch counts it claims per call."""
 import os
+import shutil
 import sys
 
 import pytest
@@ -39,3 +40,22 @@ def test_rules_and_launch_counts():
     assert bench.algorithmic(3, 5, n, l2)[2] == 505 * n
     # kernels per call: amax + quantize; amax + T + 1 sweeps (+ search and deferred-block kernel)
     assert [bench.kernels_per_call(m, 5) for m in range(5)] == [2, 2, 7, 9, 1]
+
+
+def test_recorded_traffic_goes_by_every_source_of_the_recorded_calls(tmp_path, monkeypatch):
+    """A change to a kernel or to the host code that launches it voids the
+    recorded captures; one to the decode-step operators does not."""
+    csrc = os.path.join("nvfp4_block_scale_gb300", "csrc")
+    shutil.copytree(os.path.join(ROOT, csrc), tmp_path / csrc)
+    before = bench.source_digest()
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.source_digest() == before
+    for f in sorted(os.listdir(tmp_path / csrc)):
+        path = tmp_path / csrc / f
+        text = path.read_bytes()
+        path.write_bytes(text + b"\n")
+        assert (bench.source_digest() == before) == (f in bench.OTHER_SOURCES), f
+        path.write_bytes(text)
+    (tmp_path / csrc / "new.cu").write_bytes(b"x")
+    assert bench.source_digest() != before
+    assert bench.OTHER_SOURCES < set(os.listdir(os.path.join(ROOT, csrc)))
