@@ -371,6 +371,99 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
                           int64_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * nvfp4_moe_route -- the router of a mixture-of-experts layer: each token's
+ *   top_k experts and their weights.
+ *     l[e] = sum_c x[c] router[e][c]
+ *     NVFP4_SCORE_SOFTMAX: chosen by l,                    p = softmax over all experts of l
+ *     NVFP4_SCORE_SIGMOID: chosen by sigmoid(l) + bias,    p = sigmoid(l)
+ *     weight = scale * p  (renormalize: p divided by the sum over the chosen)
+ *   The logits carry about 46 bits (fp32 sums with their rounding errors kept
+ *   in a second fp32 sum) and the choice is made in fp64, so experts whose
+ *   scores agree in fp32 are still told apart; equal scores go to the lower
+ *   expert, and a NaN is below every number.  ids are in descending order of
+ *   the score.  Weights are fp32.  Results repeat bit for bit.
+ * Arguments:
+ *   x       device, bf16, 16-byte aligned, [tokens][hidden], rows x_stride
+ *           elements apart (>= hidden, a multiple of 8).
+ *   tokens  >= 0.  hidden >= 8, a multiple of 8, below 2^31.
+ *   router  device, 16-byte aligned, bf16 or fp32 (router_dtype), [experts]
+ *           [hidden], rows router_stride elements apart (a multiple of 8, or 4 for fp32).
+ *   experts 1 .. 1024.  top_k 1 .. min(32, experts).
+ *   bias    device, fp32, [experts], or NULL for 0 (sigmoid only).
+ *   renormalize  0 or 1.  scale finite.
+ *   ids     device, int32, [tokens][top_k] (written).
+ *   weights device, fp32, [tokens][top_k] (written).
+ * Returns an nvfp4_status.
+ */
+enum nvfp4_scoring { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };
+int nvfp4_moe_route(const void *x, int64_t x_stride, int64_t tokens, const void *router,
+                    int router_dtype, int64_t router_stride, int64_t hidden, int experts,
+                    const float *bias, int scoring, int renormalize, float scale, int top_k,
+                    int32_t *ids, float *weights, cudaStream_t stream);
+
+/*
+ * nvfp4_moe -- the experts' products of a mixture-of-experts layer, for the
+ *   tokens of a decode step.  For token t and slot s with expert e = ids[t][s]:
+ *     h = act(alpha_g sum q Delta x[t]) * (alpha_u sum q Delta x[t])   (no gate: act(alpha_u sum ..))
+ *     y[t] = bf16_rne( residual[t] + sum_s weights[t][s] * alpha_d sum q Delta h )
+ *   with fp32 sums.  The weights enter the products exactly, as in
+ *   nvfp4_linear.  x enters in f16, each vector scaled by a power of two: its
+ *   entries are exact down to 2^-31 of its largest, and those below are off by at
+ *   most 2^-39 of it.  h is rounded once, to the 11 bits of f16 under such a
+ *   scale (at most 2^-12 of an entry, or 2^-39 of the vector's largest).  A
+ *   slot whose id is outside [0, experts) adds nothing: padding tokens of a
+ *   captured batch carry -1.  An expert may be named any number of times, by
+ *   one token too.  The order of the additions is fixed by the shape, the ids
+ *   and the device, so results repeat bit for bit.
+ * Arguments:
+ *   experts host struct (read during the call only): gate and up hold a
+ *           [inner, hidden] matrix of each expert, down a [hidden, inner] one, as
+ *           nvfp4_quantize writes them: expert e's codes at codes + e * code_stride
+ *           (bytes, a multiple of 8; codes 8-byte aligned), its scales at scales +
+ *           e * scale_stride, its alpha at alpha[e * alpha_stride].  Strides >= 0
+ *           and below 2^40 (gate and up may be halves of one tensor).  gate.codes
+ *           NULL: no gate.  1 .. 1024 experts; hidden and inner positive multiples
+ *           of 16 whose vectors fit shared memory (98304 always do).
+ *   x       device, bf16, 16-byte aligned, [tokens][hidden], rows x_stride
+ *           elements apart (>= hidden, a multiple of 8).
+ *   tokens  >= 0.  More than 256, or 2048 / top_k, run in slices.
+ *   top_k   1 .. 32.
+ *   ids, weights  device, int32 and fp32, [tokens][top_k].
+ *   activation  an nvfp4_activation.
+ *   residual  device, bf16, 2-byte aligned, [tokens][hidden], rows
+ *           residual_stride elements apart, or NULL.
+ *   y       device, bf16, 2-byte aligned, [tokens][hidden], rows y_stride
+ *           elements apart (written).  y may be x or the residual itself (same
+ *           address and stride).
+ *   workspace, workspace_bytes  as for nvfp4_linear,
+ *           nvfp4_moe_workspace_bytes(experts, tokens, top_k) bytes, which serve
+ *           every smaller number of tokens too; or NULL.
+ * Returns an nvfp4_status.  nvfp4_moe_workspace_bytes returns -1 for invalid
+ * arguments or without a supported device.
+ */
+typedef struct nvfp4_expert_matrix {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  const float *alpha;
+  int64_t code_stride;
+  int64_t scale_stride;
+  int64_t alpha_stride;
+} nvfp4_expert_matrix;
+typedef struct nvfp4_experts {
+  nvfp4_expert_matrix gate;
+  nvfp4_expert_matrix up;
+  nvfp4_expert_matrix down;
+  int64_t hidden;
+  int64_t inner;
+  int experts;
+} nvfp4_experts;
+int64_t nvfp4_moe_workspace_bytes(const nvfp4_experts *experts, int64_t tokens, int top_k);
+int nvfp4_moe(const nvfp4_experts *experts, const void *x, int64_t x_stride, int64_t tokens, int top_k,
+              const int32_t *ids, const float *weights, int activation, const void *residual,
+              int64_t residual_stride, void *y, int64_t y_stride, void *workspace,
+              int64_t workspace_bytes, cudaStream_t stream);
+
+/*
  * nvfp4_swizzle_scales -- the E4M3 block scales of a quantized [rows, cols]
  *   tensor, from the linear [rows, cols/16] layout that nvfp4_quantize
  *   writes to the layout block-scaled tensor-core matrix multiplies read

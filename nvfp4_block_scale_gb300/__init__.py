@@ -46,6 +46,18 @@ class nvfp4_kv_cache(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
+class nvfp4_expert_matrix(ctypes.Structure):
+    """One matrix of every expert (include/nvfp4.h)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
+                ("code_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64), ("alpha_stride", ctypes.c_int64)]
+
+
+class nvfp4_experts(ctypes.Structure):
+    """The experts of nvfp4_moe (include/nvfp4.h)."""
+    _fields_ = [("gate", nvfp4_expert_matrix), ("up", nvfp4_expert_matrix), ("down", nvfp4_expert_matrix),
+                ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64), ("experts", ctypes.c_int)]
+
+
 class nvfp4_tensor(ctypes.Structure):
     """One descriptor of nvfp4_quantize_grouped (include/nvfp4.h)."""
     _fields_ = [("W", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
@@ -95,6 +107,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_paged_attention.argtypes = [ctypes.POINTER(nvfp4_kv_cache), vp, i64, i64, ci, vp, vp, i64, i64,
                                         ctypes.c_float, i64, vp, vp, vp, i64, vp]
     L.nvfp4_paged_attention.restype = ci
+    L.nvfp4_moe_workspace_bytes.argtypes = [ctypes.POINTER(nvfp4_experts), i64, ci]
+    L.nvfp4_moe_workspace_bytes.restype = i64
+    L.nvfp4_moe.argtypes = [ctypes.POINTER(nvfp4_experts), vp, i64, i64, ci, vp, vp, ci, vp, i64, vp, i64, vp, i64, vp]
+    L.nvfp4_moe.restype = ci
     L.nvfp4_swizzled_scales_bytes.argtypes = [i64, i64]
     L.nvfp4_swizzled_scales_bytes.restype = i64
     L.nvfp4_swizzle_scales.argtypes = [vp, i64, i64, vp, vp]
@@ -194,6 +210,17 @@ def nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table
                           window, out, lse, workspace, workspace_bytes, stream) -> int:
     return load().nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table, table_width,
                                         table_stride, scale, window, out, lse, workspace, workspace_bytes, stream)
+
+
+def nvfp4_moe_workspace_bytes(experts, tokens, top_k) -> int:
+    """`experts`: an nvfp4_experts (passed by reference)."""
+    return load().nvfp4_moe_workspace_bytes(experts, tokens, top_k)
+
+
+def nvfp4_moe(experts, x, x_stride, tokens, top_k, ids, weights, activation, residual, residual_stride, y, y_stride,
+              workspace, workspace_bytes, stream) -> int:
+    return load().nvfp4_moe(experts, x, x_stride, tokens, top_k, ids, weights, activation, residual, residual_stride, y,
+                            y_stride, workspace, workspace_bytes, stream)
 
 
 def nvfp4_swizzled_scales_bytes(rows, cols) -> int:
@@ -654,6 +681,95 @@ def paged_attention(cache: KVCache, q, table, lengths, scale=None, window: int =
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wb,
         _on(cache.device, stream)), "nvfp4_paged_attention")
     return (out, lse) if return_lse else out
+
+
+class Experts:
+    """The quantized experts of a mixture-of-experts layer: up, down and (None:
+    none) gate are each (codes, scales, alpha) of all experts: codes CUDA bytes
+    [experts, rows, cols/2] and scales [experts, rows, cols/16], contiguous
+    inside an expert (the experts may lie further apart), alpha fp32 [experts].
+    gate and up are [inner, hidden] matrices, down [hidden, inner].  The tensors
+    stay the caller's; this object is the handle that moe() takes."""
+
+    def __init__(self, up, down, gate=None):
+        import torch
+        codes = up[0]
+        if codes.dim() != 3 or not codes.is_cuda:
+            raise ValueError("codes must be CUDA tensors [experts, rows, cols / 2]")
+        n, inner, half = codes.shape
+        hidden = 2 * half
+
+        def matrix(m, rows, cols, what):
+            c, s, a = m
+            if c.shape != (n, rows, cols // 2) or s.shape != (n, rows, cols // 16) or c.element_size() != 1 or \
+                    s.element_size() != 1 or c.device != codes.device or s.device != codes.device or \
+                    (n > 0 and not (c[0].is_contiguous() and s[0].is_contiguous())):
+                raise ValueError(f"{what}: codes and scales must be CUDA bytes [{n}, {rows}, {cols // 2}] and "
+                                 f"[{n}, {rows}, {cols // 16}], contiguous inside an expert")
+            if a.dtype is not torch.float32 or a.device != codes.device or a.dim() < 1 or a.shape[0] != n or \
+                    a.numel() != n:
+                raise ValueError(f"{what}: alpha must be an fp32 tensor [{n}] on the codes' device")
+            return nvfp4_expert_matrix(c.data_ptr(), s.data_ptr(), a.data_ptr(), c.stride(0), s.stride(0), a.stride(0))
+
+        self.tensors = (up, down, gate)
+        self.experts, self.hidden, self.inner, self.device = n, hidden, inner, codes.device
+        self.desc = nvfp4_experts(nvfp4_expert_matrix() if gate is None else matrix(gate, inner, hidden, "gate"),
+                                  matrix(up, inner, hidden, "up"), matrix(down, hidden, inner, "down"), hidden, inner, n)
+
+    @classmethod
+    def quantize(cls, up, down, gate=None, mode=MAX, iters: int = 0, stream=None):
+        """Experts quantized from contiguous bf16 CUDA tensors up [experts, inner,
+        hidden], down [experts, hidden, inner] and gate like up (or None), all
+        in one grouped call."""
+        import torch
+        ws, outs, parts = [], [], []
+        for w in (up, down, gate):
+            if w is None:
+                parts.append(None)
+                continue
+            n, rows, cols = w.shape
+            part = (_empty((n, rows, cols // 2), torch.uint8, w.device, stream),
+                    _empty((n, rows, cols // 16), torch.uint8, w.device, stream), _empty(n, torch.float32, w.device, stream))
+            ws += list(w)
+            outs += [(part[0][i], part[1][i], part[2][i:i + 1]) for i in range(n)]
+            parts.append(part)
+        quantize_grouped(ws, mode, iters, outs, stream)
+        return cls(*parts)
+
+
+def moe_workspace(experts: Experts, tokens: int, top_k: int):
+    """A workspace for moe() of up to `tokens` tokens, kept by the caller from
+    call to call (one per stream that such calls run on)."""
+    return _workspace(nvfp4_moe_workspace_bytes(experts.desc, tokens, top_k), experts.device)
+
+
+def moe(experts: Experts, x, ids, weights, activation="silu", residual=None, out=None, workspace=None, stream=None):
+    """The experts' products of a mixture-of-experts layer: bf16 y [tokens,
+    hidden] = residual + sum over a token's slots of weights * down(act(gate x) *
+    up x) (without a gate: down(act(up x))), for bf16 x [tokens, hidden] and the
+    slots' experts and weights, int32 and fp32 [tokens, top_k], as moe_route
+    gives them; an id outside [0, experts) adds nothing (-1: padding).  x,
+    residual and out may have rows further apart than their width; out may be
+    the residual or x.  See nvfp4_moe in include/nvfp4.h."""
+    import torch
+    tokens, top_k = ids.shape
+    if ids.dtype is not torch.int32 or not ids.is_contiguous() or ids.device != experts.device or \
+            weights.dtype is not torch.float32 or weights.shape != ids.shape or not weights.is_contiguous() or \
+            weights.device != experts.device:
+        raise ValueError("ids and weights must be contiguous int32 and fp32 tensors [tokens, top_k] on the experts' device")
+    hidden = experts.hidden
+    xp, xs = _rows_of(x, tokens, hidden, "x")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)}")
+    rp, rs = (None, 0) if residual is None else _rows_of(residual, tokens, hidden, "residual")
+    if out is None:
+        out = _empty((tokens, hidden), torch.bfloat16, experts.device, stream)
+    yp, ys = _rows_of(out, tokens, hidden, "out")
+    wp, wb = _space(workspace, experts.device)
+    _check((_lib or load()).nvfp4_moe(experts.desc, xp, xs, tokens, top_k, ids.data_ptr(), weights.data_ptr(),
+                                      ACTIVATIONS[activation], rp, rs, yp, ys, wp, wb, _on(experts.device, stream)),
+           "nvfp4_moe")
+    return out
 
 
 def swizzle_scales(scales, rows: int, cols: int, stream=None):

@@ -118,6 +118,7 @@ int device_info(DevInfo **out) {
       if (e == cudaSuccess) e = prepare_linear_kernels();
       if (e == cudaSuccess) e = prepare_linear_tc_kernels();
       if (e == cudaSuccess) e = prepare_attention_kernels();
+      if (e == cudaSuccess) e = prepare_moe_kernels();
       if (e != cudaSuccess) return map_cuda(e);
       cudaMemPoolProps props = {};
       props.allocType = cudaMemAllocationTypePinned;
@@ -233,6 +234,34 @@ size_t linear_need(int64_t rows, int64_t cols, int64_t batch, int sms) {
   return need;
 }
 
+// The checks of experts, a number of slots and its tokens, and the experts'
+// translation for the kernels; tokens of a slice at most.
+int moe_args(const nvfp4_experts *x, int64_t tokens, int top_k, MoeArgs *a, int *slice) {
+  if (!x || tokens < 0 || top_k < 1 || top_k > kMaxTopK || x->experts < 1 || x->experts > kMaxExperts)
+    return NVFP4_ERR_INVALID_ARG;
+  if (x->hidden < 16 || x->inner < 16 || check_shape(x->hidden, x->inner) != NVFP4_OK ||
+      check_shape(x->inner, x->hidden) != NVFP4_OK)
+    return NVFP4_ERR_INVALID_ARG;
+  a->gated = x->gate.codes != nullptr;
+  bool odd = false;
+  auto matrix = [&](const nvfp4_expert_matrix &m, MoeMatrix *to) {
+    *to = MoeMatrix{m.codes, m.scales, m.alpha, m.code_stride, m.scale_stride, m.alpha_stride};
+    odd |= !aligned(m.codes, 8) || !aligned(m.alpha, 4) || m.code_stride % 8 != 0;
+    bool bad = !m.codes || !m.scales || !m.alpha;
+    for (const int64_t s : {m.code_stride, m.scale_stride, m.alpha_stride}) bad |= s < 0 || s >= kMaxElems;
+    return !bad;
+  };
+  if (!matrix(x->up, &a->up) || !matrix(x->down, &a->down) || (a->gated && !matrix(x->gate, &a->gate)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (odd) return NVFP4_ERR_MISALIGNED;
+  a->experts = x->experts;
+  a->hidden = x->hidden;
+  a->inner = x->inner;
+  a->top_k = top_k;
+  *slice = (int)std::min<int64_t>(std::min(kMoeSliceTokens, kMoeSlicePairs / top_k), std::max<int64_t>(tokens, 1));
+  return moe_fits(x->hidden, x->inner, x->experts, *slice * top_k) ? NVFP4_OK : NVFP4_ERR_INVALID_ARG;
+}
+
 // A call's workspace: the caller's, or one from the pool that *own names.
 int take_workspace(void **ws, void **own, int64_t given, size_t need, const DevInfo &d, cudaStream_t stream) {
   if (*ws) return given >= 0 && (uint64_t)given >= need ? NVFP4_OK : NVFP4_ERR_INVALID_ARG;
@@ -248,14 +277,16 @@ int take_workspace(void **ws, void **own, int64_t given, size_t need, const DevI
 
 enum { kTrAmax = 0, kTrQuantMax, kTrQuantFos, kTrCjsoInit, kTrCjsoIter, kTrDecoupled, kTrDequant, kTrEncode,
        kTrGroupAmax, kTrGroupQuantMax, kTrGroupQuantFos, kTrGemv, kTrSwizzle, kTrAmaxLdg, kTrGemmTc,
-       kTrGemmTcReduce, kTrLinear, kTrLinearTcF16, kTrLinearTcBf16, kTrKvAppend, kTrAttend, kTrKinds };
+       kTrGemmTcReduce, kTrLinear, kTrLinearTcF16, kTrLinearTcBf16, kTrKvAppend, kTrAttend, kTrMoe,
+       kTrKinds };
 const char *const kTraceNames[kTrKinds] = {"k_amax_bulk",        "k_quant_max_fos<max>", "k_quant_max_fos<fos>",
                                            "k_cjso_sweep<init>",  "k_cjso_sweep<iter>",   "k_decoupled",
                                            "k_dequant",           "k_encode",             "k_group_amax",
                                            "k_group_quant<max>",  "k_group_quant<fos>",   "k_gemv",
                                            "k_swizzle_scales",   "k_amax_partials",      "k_gemm_tc",
                                            "k_gemm_tc_reduce",   "k_linear",             "k_linear_tc<f16>",
-                                           "k_linear_tc<bf16>",  "k_kv_append",          "k_attend"};
+                                           "k_linear_tc<bf16>",  "k_kv_append",          "k_attend",
+                                           "k_moe"};
 
 struct TraceRec {
   int kind;
@@ -730,6 +761,56 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
   {
     TraceScope tr(kTrAttend, stream);
     e = launch_attend(a, d->sms, workspace, stream);
+  }
+  const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
+  return map_cuda(e != cudaSuccess ? e : ef);
+}
+
+int64_t nvfp4_moe_workspace_bytes(const nvfp4_experts *experts, int64_t tokens, int top_k) {
+  MoeArgs a = {};
+  int slice = 0;
+  DevInfo *d = nullptr;
+  if (moe_args(experts, tokens, top_k, &a, &slice) != NVFP4_OK || device_info(&d) != NVFP4_OK) return -1;
+  return (int64_t)moe_workspace_bytes(a.hidden, a.inner, slice * top_k);
+}
+
+int nvfp4_moe(const nvfp4_experts *experts, const void *x, int64_t x_stride, int64_t tokens, int top_k,
+              const int32_t *ids, const float *weights, int activation, const void *residual, int64_t residual_stride,
+              void *y, int64_t y_stride, void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  MoeArgs a = {};
+  int slice = 0;
+  int st = moe_args(experts, tokens, top_k, &a, &slice);
+  if (st != NVFP4_OK) return st;
+  if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_SILU) return NVFP4_ERR_INVALID_ARG;
+  auto bad_stride = [&](int64_t s) { return s < a.hidden || s >= kMaxElems || (tokens > 0 && s > INT64_MAX / 4 / tokens); };
+  if (bad_stride(x_stride) || bad_stride(y_stride) || (residual && bad_stride(residual_stride)) ||
+      tokens > INT64_MAX / 256)
+    return NVFP4_ERR_INVALID_ARG;
+  if (tokens > 0 && (!x || !ids || !weights || !y)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || x_stride % 8 != 0 || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(residual, 2) ||
+      !aligned(y, 2) || !aligned(workspace, 256))
+    return NVFP4_ERR_MISALIGNED;
+  DevInfo *d = nullptr;
+  st = device_info(&d);
+  if (st != NVFP4_OK) return st;
+  if (tokens == 0) return NVFP4_OK;
+  void *own = nullptr;
+  st = take_workspace(&workspace, &own, workspace_bytes, moe_workspace_bytes(a.hidden, a.inner, slice * top_k), *d, stream);
+  if (st != NVFP4_OK) return st;
+  a.act = activation;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.y_stride = y_stride;
+  cudaError_t e = cudaSuccess;
+  for (int64_t t = 0; t < tokens && e == cudaSuccess; t += slice) {
+    a.tokens = (int)std::min<int64_t>(tokens - t, slice);
+    a.x = static_cast<const char *>(x) + 2 * t * x_stride;
+    a.ids = ids + t * top_k;
+    a.weights = weights + t * top_k;
+    a.residual = residual ? static_cast<const char *>(residual) + 2 * t * residual_stride : nullptr;
+    a.y = static_cast<char *>(y) + 2 * t * y_stride;
+    TraceScope tr(kTrMoe, stream);
+    e = launch_moe(a, d->sms, workspace, stream);
   }
   const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);

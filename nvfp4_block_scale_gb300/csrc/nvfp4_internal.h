@@ -130,6 +130,56 @@ struct AttendArgs {
   float *lse;
   int first_tries;  // < 0: normal (test hook)
 };
+// An expert's matrix of every expert: codes, scales and alphas, and how far apart.
+struct MoeMatrix {
+  const uint8_t *codes, *scales;
+  const float *alpha;
+  int64_t code_stride, scale_stride, alpha_stride;  // bytes, bytes, floats
+};
+constexpr int kMoeSlicePairs = 2048, kMoeSliceTokens = 256;  // (token, slot) pairs and tokens of one launch at most
+constexpr int kMaxExperts = 1024, kMaxTopK = 32;
+struct MoeArgs {
+  MoeMatrix gate, up, down;
+  bool gated;
+  int experts;
+  int64_t hidden, inner;
+  int act;
+  const void *x;  // bf16
+  int64_t x_stride;
+  int tokens, top_k;
+  const int32_t *ids;
+  const float *weights;
+  const void *residual;
+  int64_t residual_stride;
+  void *y;
+  int64_t y_stride;
+};
+struct RouteArgs {
+  const void *x;  // bf16
+  int64_t x_stride, tokens;
+  const void *router;
+  bool fp32;
+  int64_t router_stride, hidden;
+  int experts, top_k;
+  const float *bias;
+  bool sigmoid, renormalize;
+  float scale;
+  int32_t *ids;
+  float *weights;
+};
+struct SampleArgs {
+  const void *logits;
+  bool fp32;
+  int64_t stride;
+  int rows, vocabulary;
+  const float *temperature, *top_p, *min_p;
+  const int32_t *top_k;
+  float temperature_all, top_p_all, min_p_all;
+  int top_k_all;
+  const float *uniform;
+  int32_t *token;
+  float *logprob;
+};
 // The kernel that took a product, for the tracer.
 enum LinearKernel { kLinearRegisters = 0, kLinearTcF16, kLinearTcBf16 };
 size_t linear_workspace_bytes(int64_t rows, int64_t cols, int batch, int sms);
@@ -142,6 +192,14 @@ cudaError_t launch_kv_append(const AppendArgs &a, int sms, cudaStream_t st);
 size_t attend_workspace_bytes(const KvArgs &kv, int q_heads, int sms);
 cudaError_t prepare_attention_kernels();
 cudaError_t launch_attend(const AttendArgs &a, int sms, void *ws, cudaStream_t st);
+bool moe_fits(int64_t hidden, int64_t inner, int experts, int pairs);
+size_t moe_workspace_bytes(int64_t hidden, int64_t inner, int pairs);
+cudaError_t prepare_moe_kernels();
+cudaError_t launch_moe(const MoeArgs &a, int sms, void *ws, cudaStream_t st);
+cudaError_t prepare_route_kernels();
+cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st);
+cudaError_t prepare_sample_kernels();
+cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t st);
 int64_t ffma_probe_fmas_per_thread(int packed, int64_t rounds);
 cudaError_t launch_ffma_probe(int packed, int64_t rounds, int grid, float *sink, cudaStream_t st);
 int ffma_probe_threads();
