@@ -409,8 +409,8 @@ int nvfp4_moe_route(const void *x, int64_t x_stride, int64_t tokens, const void 
  *   with fp32 sums.  The weights enter the products exactly, as in
  *   nvfp4_linear.  x enters in f16, each vector scaled by a power of two: its
  *   entries are exact down to 2^-31 of its largest, and those below are off by at
- *   most 2^-39 of it.  h is rounded once, to the 11 bits of f16 under such a
- *   scale (at most 2^-12 of an entry, or 2^-39 of the vector's largest).  A
+ *   most 2^-39 of it.  h is rounded to the 11 bits of f16 under such
+ *   scales (off by at most 2^-12 of an entry or 2^-38 of the vector's largest).  A
  *   slot whose id is outside [0, experts) adds nothing: padding tokens of a
  *   captured batch carry -1.  An expert may be named any number of times, by
  *   one token too.  The order of the additions is fixed by the shape, the ids
@@ -423,7 +423,7 @@ int nvfp4_moe_route(const void *x, int64_t x_stride, int64_t tokens, const void 
  *           e * scale_stride, its alpha at alpha[e * alpha_stride].  Strides >= 0
  *           and below 2^40 (gate and up may be halves of one tensor).  gate.codes
  *           NULL: no gate.  1 .. 1024 experts; hidden and inner positive multiples
- *           of 16 whose vectors fit shared memory (98304 always do).
+ *           of 16 whose vectors fit shared memory (up to 49152 always do).
  *   x       device, bf16, 16-byte aligned, [tokens][hidden], rows x_stride
  *           elements apart (>= hidden, a multiple of 8).
  *   tokens  >= 0.  More than 256, or 2048 / top_k, run in slices.

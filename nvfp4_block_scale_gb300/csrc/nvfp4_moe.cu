@@ -15,19 +15,24 @@
 // Jobs: every CTA sorts the call's (token, slot) pairs by expert in shared
 // memory; an expert with n pairs makes ceil(n / N) jobs of up to N pairs.  The
 // row tiles of all jobs, job after job, are cut into one contiguous range per
-// SM, and the (tile, column step) units of a range's part of one job into 16
+// SM, and the units (16 rows by 256 columns) of a range's part of one job into 16
 // contiguous runs, one per warp.  A warp that does a whole tile finishes it
 // from its registers; sums of a tile cut between warps meet in shared memory, in
-// warp order.  Loads run kMoeDepth units ahead, across jobs.
+// warp order.  Codes come by asynchronous copies, kMoeDepth units ahead, across
+// tiles and jobs.
 //
 // Products: mma.sync m16n8k16 (f16 x f16 -> fp32), 16 rows of W by 8 pairs.
 // q * Delta is formed in registers, exactly: six significant bits between 2^-10
 // and 2688.  The vectors go to f16 in shared memory, each scaled by a power of
 // two that puts its largest entry into [2^14, 2^15): x keeps its 8 bits down to
-// 2^-31 of its largest entry; h, fp32 until then, is rounded to 11 bits, an
-// eighth of what bf16 would lose.  With a gate the 16 rows are 8 of the gate's
+// 2^-31 of its largest entry.  h is rounded to f16's 11 bits, which loses an
+// eighth of what bf16 would, under a scale for each 8 entries (a whole vector's is
+// not known before all of them are), and then brought to one scale, exactly down
+// to 2^-29 of its largest entry.  With a gate the 16 rows are 8 of the gate's
 // and the 8 of up's that they multiply, so that h is formed in registers.
 #include <algorithm>
+#include <climits>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -39,25 +44,23 @@
 
 namespace nvfp4 {
 
-constexpr int kMoeWarps = 16;
-constexpr int kMoeThreads = kMoeWarps * 32;
-constexpr int kMoeDepth = 4;            // steps in flight per warp
-constexpr int kMoeSmem = 226 * 1024;    // dynamic shared memory of the one CTA per SM
+constexpr int kMoeDepth = 3;            // units of 256 columns in flight per warp
+constexpr int kMoeMaxWarps = 16;        // of a CTA
+constexpr int kMoeSmem = 226 * 1024;    // dynamic shared memory of a CTA that has an SM to itself
+constexpr int kMoeHalfSmem = 112 * 1024;  // of one of two
+constexpr int kMoeFewPairs = 32;        // a warp sorts so many by itself
 
 struct MoeLaunch {
   MoeArgs a;
-  float *h, *part;    // [pairs][inner], [pairs][hidden]
+  __half *h;          // [pairs][inner], each 8 entries times a power of two
+  int8_t *h_up;       // [pairs][up_pitch]: its exponent
+  float *part;        // [pairs][hidden]
+  int up_pitch;       // inner / 8, rounded up to 16
   int pairs;          // tokens * top_k
   int group;          // pairs of a job at most
-  int steps;          // of 128 columns
+  int steps;          // of 256 columns
   int tiles;          // of a job
   int64_t cols;       // of this launch's matrices
-};
-
-// One step of a lane: 32 columns (two blocks) of its two rows.
-struct MoeLoad {
-  uint4 c[2];
-  uint32_t s[2];
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -68,349 +71,511 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight consecutive entries of a vector, as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 r = reinterpret_cast<const float4 *>(p)[i];
-    v[4 * i] = r.x, v[4 * i + 1] = r.y, v[4 * i + 2] = r.z, v[4 * i + 3] = r.w;
-  }
+// The power of two (its exponent) that brings a largest magnitude of these bits
+// into [2^14, 2^15); for an infinity or a NaN one that leaves it what it is.
+__device__ __forceinline__ int f16_up(unsigned top) { return min(14 + 127 - (int)(top >> 23), 126); }
+
+__host__ __device__ constexpr int moe_slot(bool wide) { return wide ? 2304 : 2560; }  // a unit's codes and scales
+__host__ __device__ constexpr int moe_up_pitch(int64_t cols) { return (int)((cols / 8 + 15) / 16 * 16); }
+// Shared memory: the vectors (with h's exponents), the warps' units in flight
+// and partial sums, the vectors' scales, the plan.
+__host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, bool wide, int experts, int pairs) {
+  return (cols + 255) / 256 * 512 * group + (down ? (int64_t)group * moe_up_pitch(cols) : 0) +
+         (int64_t)warps * (kMoeDepth * moe_slot(wide) + (group + 7) / 8 * 512) + 512 +
+         (pairs > kMoeFewPairs ? (int64_t)experts * 8 : 0) + ((int64_t)pairs + 1) * 14 + 64;
 }
 
-// Shared memory besides the vectors: the plan, and a partial sum per warp.
-__host__ __device__ constexpr int64_t moe_fixed_smem(int experts, int pairs, int nt) {
-  return (int64_t)experts * 8 + (int64_t)pairs * 8 + 512 + (int64_t)kMoeWarps * nt * 512 + 128;
+// A job: an expert's pairs order[at .. at + n).
+__device__ __forceinline__ uint32_t moe_job(int expert, int at, int n) { return (uint32_t)expert << 17 | (uint32_t)at << 6 | (uint32_t)n; }
+static_assert(kMaxExperts <= 1024 && kMoeSlicePairs <= 2048, "a job's fields");
+// A tile's cost: its weights' way, and less for each further n-tile of pairs.
+__device__ __forceinline__ int moe_tile_cost(int pairs) { return 8 + (pairs - 1) / 8; }
+
+// The plan: the pairs that have an expert by expert, ascending, so that every
+// CTA cuts an expert's into the same jobs; the jobs, and the cost of those
+// before each.
+struct MoePlan {
+  uint32_t *jobs;   // [pairs]
+  int *start;       // [pairs + 1]
+  uint16_t *order;  // [pairs]
+  int *count, *end; // [experts]: pairs of an expert, and where they end (unused with few pairs)
+  uint16_t *named;  // [pairs]: their experts
+  uint16_t *found;  // [pairs]: by expert, as they came
+  int *total;       // jobs
+};
+
+// By one warp, one pair per lane.
+__device__ void moe_plan_few(const MoeLaunch &p, const MoePlan &o, int lane) {
+  const int N = p.group;
+  const int id = lane < p.pairs ? p.a.ids[lane] : -1;
+  const bool there = id >= 0 && id < p.a.experts;
+  const int e = there ? id : INT_MAX;
+  const uint32_t same = __match_any_sync(~0u, e), before = same & ((1u << lane) - 1u);
+  const int pos = __popc(before), n = min(N, __popc(same) - pos);  // pairs from here to the job's end, at a job's first
+  const bool first = there && pos % N == 0;
+  const int cost = first ? p.tiles * moe_tile_cost(n) : 0;
+  int rank = 0, job = 0, start = 0;
+#pragma unroll
+  for (int l = 0; l < 32; ++l) {
+    const int el = __shfl_sync(~0u, e, l), cl = __shfl_sync(~0u, cost, l);
+    if (el < e || (el == e && l < lane)) ++rank, job += cl > 0, start += cl;
+  }
+  if (there) o.order[rank] = (uint16_t)lane;
+  if (first) {
+    o.jobs[job] = moe_job(e, rank, n);
+    o.start[job] = start;
+  }
+  const int total = __popc(__ballot_sync(~0u, first)), all = __reduce_add_sync(~0u, cost);
+  if (lane == 0) o.start[total] = all, *o.total = total;
+}
+
+// By the whole CTA.
+__device__ void moe_plan(const MoeLaunch &p, const MoePlan &o, int tid, int threads, int (*scan)[kMoeMaxWarps]) {
+  const int N = p.group, E = p.a.experts, warp = tid >> 5, lane = tid & 31;
+  for (int e = tid; e < E; e += threads) o.count[e] = 0;
+  __syncthreads();
+  for (int i = tid; i < p.pairs; i += threads) {
+    const int e = p.a.ids[i];
+    const bool there = e >= 0 && e < E;
+    o.named[i] = there ? (uint16_t)e : (uint16_t)0xFFFFu;
+    if (there) atomicAdd(&o.count[e], 1);
+  }
+  __syncthreads();
+  int total = 0, named = 0, cost = 0;  // jobs; pairs that have an expert; the jobs' cost
+  for (int e0 = 0; e0 < E; e0 += threads) {
+    const int e = e0 + tid, n = e < E ? o.count[e] : 0, j = (n + N - 1) / N;
+    const int c = j > 0 ? p.tiles * ((j - 1) * moe_tile_cost(N) + moe_tile_cost(n - (j - 1) * N)) : 0;
+    int sn = n, sj = j, sc = c;  // inclusive sums over the warp, then over the warps
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int un = __shfl_up_sync(~0u, sn, d), uj = __shfl_up_sync(~0u, sj, d), uc = __shfl_up_sync(~0u, sc, d);
+      if (lane >= d) sn += un, sj += uj, sc += uc;
+    }
+    if (lane == 31) scan[0][warp] = sn, scan[1][warp] = sj, scan[2][warp] = sc;
+    __syncthreads();
+    int bn = named + sn - n, bj = total + sj - j, bc = cost + sc - c;
+    for (int w = 0; w < threads / 32; ++w) {
+      const int wn = scan[0][w], wj = scan[1][w], wc = scan[2][w];
+      if (w < warp) bn += wn, bj += wj, bc += wc;
+      named += wn, total += wj, cost += wc;
+    }
+    if (e < E) {
+      o.end[e] = bn;  // (its first pair, until they are found)
+      for (int i = 0; i < j; ++i) {
+        o.jobs[bj + i] = moe_job(e, bn + i * N, min(N, n - i * N));
+        o.start[bj + i] = bc + i * p.tiles * moe_tile_cost(N);
+      }
+    }
+    __syncthreads();
+  }
+  if (tid == 0) o.start[total] = cost, *o.total = total;
+  for (int i = tid; i < p.pairs; i += threads) {
+    const int e = o.named[i];
+    if (e != 0xFFFF) o.found[atomicAdd(&o.end[e], 1)] = (uint16_t)i;
+  }
+  __syncthreads();
+  for (int q = tid; q < named; q += threads) {
+    const int i = o.found[q], e = o.named[i], n = o.count[e], b = o.end[e] - n;
+    int to = q;
+    if (n > N) {  // (in one job a pair's place only decides which column of an MMA it takes)
+      to = b;
+      for (int f = b; f < b + n; ++f) to += o.found[f] < i;
+    }
+    o.order[to] = (uint16_t)i;
+  }
 }
 
 // DOWN: the second product (h -> part), else the first (x -> h).  GATED: the
 // first product's tiles hold 8 rows of gate and 8 of up.  WIDE: rows of codes
-// are whole multiples of 16 bytes and of scales of 2, and so aligned; otherwise
-// a block at a time.
+// are whole multiples of 16 bytes and of scales of 4, and so aligned.  NT:
+// n-tiles that the group's pairs fill at most.
 template <int NT, bool DOWN, bool GATED, bool WIDE>
-__global__ void __launch_bounds__(kMoeThreads, 1) k_moe(const __grid_constant__ MoeLaunch p) {
+__global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_constant__ MoeLaunch p) {
   extern __shared__ uint4 dsm[];
-  __shared__ int scan[2][kMoeWarps];
+  __shared__ int scan[3][kMoeMaxWarps], jobs_there;
   const MoeArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
-  const int nk = p.steps, N = p.group;
-  uint4 *xs = dsm;                                                        // [nk][4][N][4] 16-byte units of f16
-  float4 *own = reinterpret_cast<float4 *>(dsm + (size_t)nk * 16 * N);    // [warps][NT][32]
-  float *xdown = reinterpret_cast<float *>(own + kMoeWarps * NT * 32);    // [2][32]: the vectors' scales, undone
-  unsigned *xmax = reinterpret_cast<unsigned *>(xdown + 64);              // [2][32]: their largest entries
-  int *count = reinterpret_cast<int *>(xmax + 64);                        // [experts]
-  int *end = count + a.experts;                                           // [experts]: where its pairs end in `order`
-  uint32_t *jobs = reinterpret_cast<uint32_t *>(end + a.experts);       // [jobs]: expert << 16 | group
-  uint16_t *order = reinterpret_cast<uint16_t *>(jobs + p.pairs);         // [pairs], by expert
-  uint16_t *found = order + p.pairs;                                      // [pairs], by expert, as they came
+  const int threads = blockDim.x, warps = threads >> 5;
+  const int nk = p.steps, N = p.group, NB = (N + 7) / 8;
+  constexpr int kSlot = moe_slot(WIDE);
+  uint4 *xs = dsm;                                                        // [nk][8][N][4] 16-byte units of f16
+  uint4 *slots = dsm + (size_t)nk * 32 * N;                               // [warps][depth][kSlot / 16]: units in flight
+  float4 *own = reinterpret_cast<float4 *>(slots + warps * kMoeDepth * (kSlot / 16));  // [warps][NB][32]
+  slots += warp * kMoeDepth * (kSlot / 16);
+  int8_t *ups = reinterpret_cast<int8_t *>(own + warps * NB * 32);        // [N][up_pitch]
+  float *xdown = reinterpret_cast<float *>(ups + (DOWN ? N * p.up_pitch : 0));  // [2][32]: the vectors' scales, undone
+  int *xtop = reinterpret_cast<int *>(xdown + 64);                        // [2][32]: their largest entries' bits, or their scales' exponents
+  MoePlan o;
+  o.start = xtop + 64;
+  o.jobs = reinterpret_cast<uint32_t *>(o.start + p.pairs + 1);
+  o.count = reinterpret_cast<int *>(o.jobs + p.pairs);
+  o.end = o.count + (p.pairs > kMoeFewPairs ? a.experts : 0);
+  o.order = reinterpret_cast<uint16_t *>(o.end + (p.pairs > kMoeFewPairs ? a.experts : 0));
+  o.named = o.order + p.pairs;
+  o.found = o.named + p.pairs;
+  o.total = &jobs_there;
 
-  for (int e = tid; e < a.experts; e += kMoeThreads) count[e] = 0;
-  if (tid < 64) xmax[tid] = 0u;
-  pdl_launch_dependents();
-  pdl_wait();
+  // The second product waits for the first only where it needs h: ids and
+  // weights were there before the first began, since that lets the second start
+  // after its own wait only.
+  if constexpr (!DOWN) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+  if (tid < 64) xtop[tid] = INT_MIN;
+  if (p.pairs <= kMoeFewPairs) {
+    if (warp == 0) moe_plan_few(p, o, lane);
+  } else {
+    moe_plan(p, o, tid, threads, scan);
+  }
   __syncthreads();
 
-  // ---- the plan: pairs by expert, jobs
-  for (int i = tid; i < p.pairs; i += kMoeThreads) {
-    const int e = a.ids[i];
-    if (e >= 0 && e < a.experts) atomicAdd(&count[e], 1);
-  }
-  __syncthreads();
-  int total = 0, named = 0;  // jobs; pairs that have an expert
-  {
-    for (int e0 = 0; e0 < a.experts; e0 += kMoeThreads) {
-      const int e = e0 + tid, n = e < a.experts ? count[e] : 0, j = (n + N - 1) / N;
-      int sn = n, sj = j;  // inclusive sums over the warp, then over the warps
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int un = __shfl_up_sync(~0u, sn, o), uj = __shfl_up_sync(~0u, sj, o);
-        if (lane >= o) sn += un, sj += uj;
-      }
-      if (lane == 31) scan[0][warp] = sn, scan[1][warp] = sj;
-      __syncthreads();
-      int bn = named, bj = total;
-#pragma unroll
-      for (int w = 0; w < kMoeWarps; ++w) {
-        const int wn = scan[0][w], wj = scan[1][w];
-        if (w < warp) bn += wn, bj += wj;
-        named += wn, total += wj;
-      }
-      if (e < a.experts) {
-        end[e] = bn + sn - n;  // (its first pair, until they are put in order)
-        for (int i = 0; i < j; ++i) jobs[bj + sj - j + i] = (uint32_t)e << 16 | (uint32_t)i;
-      }
-      __syncthreads();
+  // ---- this CTA's tiles: the job and the tile at two places of the total cost
+  const int total = jobs_there, cost = o.start[total];
+  auto place = [&](int64_t at, int *job, int *tile) {
+    int lo = 0, hi = total;
+    while (lo < hi) {  // the last job that starts at `at` or before, or `total`
+      const int mid = (lo + hi + 1) / 2;
+      if (o.start[mid] <= at) lo = mid;
+      else hi = mid - 1;
     }
-  }
-  const int64_t tiles = (int64_t)total * p.tiles;
-  const int64_t T0 = blockIdx.x * tiles / gridDim.x, T1 = (blockIdx.x + 1) * tiles / gridDim.x;
-  if (T0 == T1) return;
-  const int j0 = (int)(T0 / p.tiles), j1 = (int)((T1 - 1) / p.tiles);
-  // Pairs by expert, ascending inside an expert that has several jobs: every CTA
-  // has to cut it alike.  (In one job a pair's place only decides which column of
-  // an MMA it takes.)
-  for (int i = tid; i < p.pairs; i += kMoeThreads) {
-    const int e = a.ids[i];
-    if (e >= 0 && e < a.experts) found[atomicAdd(&end[e], 1)] = (uint16_t)i;
-  }
-  __syncthreads();
-  for (int q = tid; q < named; q += kMoeThreads) {
-    const int i = found[q], e = a.ids[i], n = count[e], b = end[e] - n;
-    int to = q;
-    if (n > N) {
-      to = b;
-      for (int o = b; o < b + n; ++o) to += found[o] < i;
+    *job = lo;
+    *tile = lo < total ? (int)(at - o.start[lo]) / moe_tile_cost(o.jobs[lo] & 63u) : 0;
+  };
+  int j0, t0, j1, t1;
+  place((int64_t)blockIdx.x * cost / gridDim.x, &j0, &t0);
+  place((int64_t)(blockIdx.x + 1) * cost / gridDim.x, &j1, &t1);
+  if (j0 == j1 && t0 == t1) {
+    if constexpr (DOWN) {
+      pdl_wait();
+      pdl_launch_dependents();
     }
-    order[to] = (uint16_t)i;
+    return;
   }
-  __syncthreads();
+  if (t1 == 0) --j1, t1 = p.tiles;
 
   // ---- this warp's units: its run of the range's part of each job
   struct Run {
     int t0, u0, u1;  // the part's first tile; the warp's units, counted from there
   };
   auto run_of = [&](int j, int w) {
-    const int t0 = j == j0 ? (int)(T0 - (int64_t)j0 * p.tiles) : 0;
-    const int units = ((j == j1 ? (int)(T1 - (int64_t)j1 * p.tiles) : p.tiles) - t0) * nk;
-    return Run{t0, w * units / kMoeWarps, (w + 1) * units / kMoeWarps};
+    const int from = j == j0 ? t0 : 0, units = ((j == j1 ? t1 : p.tiles) - from) * nk;
+    return Run{from, w * units / warps, (w + 1) * units / warps};
   };
-  const int64_t nblk = p.cols / 16, tile_blk = (GATED && !DOWN ? 8 : 16) * nblk;  // blocks of a row, between tiles
-  int fj = j0 - 1, fk = 0, fleft = 0;  // next unit to load: its job, its step; units left of the run
-  const uint8_t *fc[2], *fs[2];        // its rows' codes and scales
-  fc[0] = fc[1] = fs[0] = fs[1] = nullptr;
-  auto fetch = [&](MoeLoad &d) {  // (nothing once the range's units are loaded)
-    while (fleft == 0) {
-      if (fj == j1) return;
-      const Run r = run_of(++fj, warp);
-      fleft = r.u1 - r.u0;
-      if (fleft == 0) continue;
-      const int e = (int)(jobs[fj] >> 16), t = r.t0 + r.u0 / nk;
-      fk = r.u0 % nk;
+  // Units go to the ring kMoeDepth ahead.  Codes: 16 rows of 128 bytes, the 16-byte
+  // chunk c of row r at place c ^ (r % 8), so that both the copies (full rows) and
+  // the reads (two chunks of each of eight rows at once) spread over the banks.
+  // A lane takes 64 columns (four blocks) of rows g and g + 8; it copies their
+  // scales itself, a word each, or (where a row need not begin on a word) the two
+  // words that hold them.
+  const int64_t nblk = p.cols / 16, pitch = 8 * nblk;     // blocks and code bytes of a row
+  constexpr int kTileRows = GATED && !DOWN ? 8 : 16;      // rows between tiles
+  constexpr int kPiece = WIDE ? 16 : 8, kRows = 4 * kPiece / 16, kCopies = 16 / kRows;  // of a copy by the warp
+  const int row0 = lane / (32 / kRows), byte0 = lane % (32 / kRows) * kPiece;
+  // bytes of the last step's piece and scales (past the end come zeros, from no address)
+  const int code_tail = max(0, min(kPiece, (int)(pitch - (int64_t)(nk - 1) * 128) - byte0));
+  const int scale_tail = max(0, min(4, (int)(nblk - (int64_t)(nk - 1) * 16) - 4 * cq));
+  const uint32_t slot_at = static_cast<uint32_t>(__cvta_generic_to_shared(slots)), scale_to = slot_at + 2048 + lane * 4;
+  // the lane's place in rows 0 .. 7: copies 0 and 1 of the wide form's two
+  const uint32_t code_to0 = slot_at + row0 * 128 + (((byte0 >> 4) ^ row0) << 4) + (byte0 & 15),
+                 code_to1 = slot_at + (row0 + 4) * 128 + (((byte0 >> 4) ^ (row0 + 4)) << 4);
+  struct {
+    int j, k, left;     // the next unit's job and step; units left of the run
+    uint32_t at;        // its scales' offset in the matrix (and an eighth of its codes')
+    const uint8_t *code[2], *scale[2];  // this lane's rows 0 and 8 of the matrix
+  } next = {j0 - 1, 0, 0, 0u, {nullptr, nullptr}, {nullptr, nullptr}};
+  const uint32_t rows4 = (uint32_t)(kRows * pitch), wrap = (uint32_t)(kTileRows * nblk - (int64_t)(nk - 1) * 16);
+  auto open_run = [&]() {  // the next unit's rows, in the next job with units for this warp
+    while (next.left == 0 && next.j < j1) {
+      const Run r = run_of(++next.j, warp);
+      next.left = r.u1 - r.u0;
+      const int e = (int)(o.jobs[next.j] >> 17), t = r.u0 / nk;
+      next.k = r.u0 - t * nk;
+      next.at = (uint32_t)((r.t0 + t) * kTileRows * nblk) + 16 * next.k;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const MoeMatrix &m = DOWN ? a.down : GATED && h == 0 ? a.gate : a.up;
-        const int64_t row = GATED && !DOWN ? (int64_t)t * 8 + g : (int64_t)t * 16 + 8 * h + g;
-        fc[h] = m.codes + e * m.code_stride + row * nblk * 8;
-        fs[h] = m.scales + e * m.scale_stride + row * nblk;
+        const int64_t row = GATED && !DOWN ? 0 : 8 * h;
+        next.code[h] = m.codes + e * m.code_stride + (row + row0) * pitch + byte0;
+        next.scale[h] = m.scales + e * m.scale_stride + (row + g) * nblk + 4 * cq;
       }
-    }
-    // columns past the end read the last blocks: the vectors are zero there
-    const int blk = fk * 8 + 2 * cq;
-    if (WIDE) {
-      const int64_t at = min((int64_t)blk, nblk - 2);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        d.c[h] = __ldcs(reinterpret_cast<const uint4 *>(fc[h] + 8 * at));
-        d.s[h] = __ldg(reinterpret_cast<const uint16_t *>(fs[h] + at));
-      }
-    } else {
-      const int64_t at = min((int64_t)blk, nblk - 1), at1 = min((int64_t)blk + 1, nblk - 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 lo = __ldcs(reinterpret_cast<const uint2 *>(fc[h]) + at), hi = __ldcs(reinterpret_cast<const uint2 *>(fc[h]) + at1);
-        d.c[h] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        d.s[h] = (uint32_t)__ldg(fs[h] + at) | (uint32_t)__ldg(fs[h] + at1) << 8;
-      }
-    }
-    --fleft;
-    if (++fk == nk) {
-      fk = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) fc[h] += 8 * tile_blk, fs[h] += tile_blk;
     }
   };
-  MoeLoad buf[kMoeDepth];
+  uint32_t fill = 0;  // the ring's place for the next unit
+  auto fetch = [&]() {
+    if (next.left == 0) open_run();
+    if (next.left > 0) {
+      const bool last = next.k == nk - 1;
+      const int cb = last ? code_tail : kPiece, sb = last ? scale_tail : 4;
 #pragma unroll
-  for (int i = 0; i < kMoeDepth; ++i) fetch(buf[i]);
-
-  // ---- the jobs.  xmax and xdown alternate between two places: a warp may
-  // still finish a job's sums while others take in the next one's vectors.
-  int par = 0, turn = 0;  // turn: the buffer that holds the next unit
-  for (int j = j0; j <= j1; ++j, par ^= 1) {
-    const int e = (int)(jobs[j] >> 16), at0 = end[e] - count[e] + (int)(jobs[j] & 0xFFFFu) * N;
-    const int np = min(N, end[e] - at0);  // pairs of this job
-    const uint16_t *pair = order + at0;
-
-    // vectors into shared memory, 8 columns at a time: first the largest entry
-    // of each, then (from L1 or L2) the scaled f16.  A vector's columns are
-    // shared by several warps where there are fewer vectors than warps.
-    const int nu = nk * 16, wide = (int)(p.cols / 8);
-    const int share = kMoeWarps / np > 0 ? kMoeWarps / np : 1;
-    auto vector = [&](int n) {
-      const int i = pair[n];
-      if constexpr (DOWN) return (const float *)p.h + (int64_t)i * p.cols;
-      else return static_cast<const __nv_bfloat16 *>(a.x) + (int64_t)(i / a.top_k) * a.x_stride;
-    };
-    for (int i = warp; i < np * share; i += kMoeWarps) {
-      const int n = i / share, s = i - n * share;
-      const auto *v = vector(n);
-      float top = 0.0f;
-      bool nan = false;
-      for (int u = s * 32 + lane; u < wide; u += share * 32) {
-        float x[8];
-        load8(v + 8 * u, x);
-#pragma unroll
-        for (int b = 0; b < 8; ++b) top = fmaxf(top, fabsf(x[b])), nan |= x[b] != x[b];
-      }
-      const unsigned m = __reduce_max_sync(~0u, nan ? 0x7F800000u : __float_as_uint(top));
-      if (lane == 0) atomicMax(&xmax[par * 32 + n], m);
-    }
-    __syncthreads();
-    for (int i = warp; i < np * share; i += kMoeWarps) {
-      const int n = i / share, s = i - n * share;
-      const auto *v = vector(n);
-      const int up = min(14 + 127 - (int)(xmax[par * 32 + n] >> 23), 126);
-      if (s == 0 && lane == 0) xdown[par * 32 + n] = pow2(-up);
-      for (int u = s * 32 + lane; u < nu; u += share * 32) {
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-        if (u < wide) {
-          float x[8];
-          load8(v + 8 * u, x);
-          uint32_t w[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const __half2 f = __floats2half2_rn(x[2 * b] * pow2(up), x[2 * b + 1] * pow2(up));
-            w[b] = *reinterpret_cast<const uint32_t *>(&f);
-          }
-          o = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        // unit u: step u / 16, lane quarter (u / 4) % 4, pair of k-steps u % 4
-        xs[(((u >> 4) * 4 + (u & 3)) * N + n) * 4 + ((u >> 2) & 3)] = o;
-      }
-    }
-    if (tid < 32) xmax[(par ^ 1) * 32 + tid] = 0u;
-    __syncthreads();
-
-    // ---- the run
-    const Run r = run_of(j, warp);
-    float acc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-    // a tile's finished sums
-    auto finish_tile = [&](int t) {
-      float av = 0.0f, ag = 0.0f;  // (read here: once per tile, from L1)
-      if constexpr (DOWN) av = a.down.alpha[e * a.down.alpha_stride];
-      else av = a.up.alpha[e * a.up.alpha_stride];
-      if constexpr (GATED && !DOWN) ag = a.gate.alpha[e * a.gate.alpha_stride];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int n0 = 8 * nt + 2 * cq;
-        if (n0 >= np) continue;
-        const bool two = n0 + 1 < np;
-        const int p0 = pair[n0], p1 = pair[two ? n0 + 1 : n0];
-        const float d0 = xdown[par * 32 + n0], d1 = xdown[par * 32 + (two ? n0 + 1 : n0)];
-        if constexpr (DOWN) {
-          float *q = p.part + (int64_t)t * 16 + g;
-          q[p0 * a.hidden] = acc[nt][0] * av * d0;
-          q[p0 * a.hidden + 8] = acc[nt][2] * av * d0;
-          if (two) {
-            q[p1 * a.hidden] = acc[nt][1] * av * d1;
-            q[p1 * a.hidden + 8] = acc[nt][3] * av * d1;
-          }
-        } else if constexpr (GATED) {
-          float v[2] = {acc[nt][0] * ag * d0, acc[nt][1] * ag * d1};
-          activate(v, a.act);
-          float *q = p.h + (int64_t)t * 8 + g;
-          q[p0 * a.inner] = v[0] * (acc[nt][2] * av * d0);
-          if (two) q[p1 * a.inner] = v[1] * (acc[nt][3] * av * d1);
+      for (int i = 0; i < kCopies; ++i) {
+        const uint8_t *from = next.code[i / (kCopies / 2)] + (uint64_t)next.at * 8 + (i % (kCopies / 2)) * rows4;
+        if (WIDE) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                       ::"r"((i & 1 ? code_to1 : code_to0) + (i >> 1) * 1024 + fill), "l"(from), "r"(cb) : "memory");
         } else {
-          float v[4] = {acc[nt][0] * av * d0, acc[nt][1] * av * d1, acc[nt][2] * av * d0, acc[nt][3] * av * d1};
-          activate(v, a.act);
-          float *q = p.h + (int64_t)t * 16 + g;
-          q[p0 * a.inner] = v[0];
-          q[p0 * a.inner + 8] = v[2];
-          if (two) {
-            q[p1 * a.inner] = v[1];
-            q[p1 * a.inner + 8] = v[3];
-          }
+          const int r = i * kRows + row0;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                       ::"r"(slot_at + r * 128 + (((byte0 >> 4) ^ (r & 7)) << 4) + (byte0 & 15) + fill), "l"(from), "r"(cb) : "memory");
         }
       }
-    };
-    int ct = r.u0 / nk, ck = r.u0 - ct * nk;  // counted from the part's first tile
-    bool mine = ck == 0;  // this warp takes the current tile's first step
-    const uint4 *xl[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xl[nt] = xs + min(8 * nt + g, np - 1) * 4 + cq;
-    auto unit = [&](MoeLoad &d) {
-      uint32_t sc[2][2];  // f16 pairs {Delta, Delta} of the lane's two blocks, of both rows
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t f;
-        asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(f) : "r"(d.s[h]));
-        sc[h][0] = __byte_perm(f, 0u, 0x1010);
-        sc[h][1] = __byte_perm(f, 0u, 0x3232);
-      }
-      const uint32_t cw[2][4] = {{d.c[0].x, d.c[0].y, d.c[0].z, d.c[0].w}, {d.c[1].x, d.c[1].y, d.c[1].z, d.c[1].w}};
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {  // a word of codes: 8 columns, two k-steps
-        uint32_t w[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          e2m1x8_f16(cw[h][jj], w[h]);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) w[h][b] = mul_f16x2(w[h][b], sc[h][jj >> 1]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (nt > 0 && 8 * nt >= np) break;
-          const uint4 xb = xl[nt][(ck * 4 + jj) * (4 * N)];
-          mma_f16(acc[nt], w[0][0], w[1][0], w[0][1], w[1][1], xb.x, xb.y);
-          mma_f16(acc[nt], w[0][2], w[1][2], w[0][3], w[1][3], xb.z, xb.w);
-        }
-      }
-      fetch(d);
-      if (++ck == nk) {  // the tile's last step
-        if (mine) {
-          finish_tile(r.t0 + ct);
+        const uint8_t *from = next.scale[h] + next.at;
+        if (WIDE) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(scale_to + h * 128 + fill), "l"(from), "r"(sb) : "memory");
         } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) own[(warp * NT + nt) * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+          const int off = (int)(reinterpret_cast<uintptr_t>(from) & 3u), end = sb ? off + sb : 0;  // bytes of the two words
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(scale_to + h * 256 + fill), "l"(from - off), "r"(min(end, 4)) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                       ::"r"(scale_to + h * 256 + 128 + fill), "l"(from - off + 4), "r"(max(end - 4, 0)) : "memory");
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-        ck = 0;
-        ++ct;
-        mine = true;
       }
-    };
-    // the buffers take turns: this run begins with the one that follows the last run's last
-    int left = r.u1 - r.u0;
-    while (left > 0) {
-#pragma unroll
-      for (int i = 0; i < kMoeDepth; ++i)
-        if (left > 0 && turn == i) {
-          unit(buf[i]);
-          --left;
-          turn = (i + 1) % kMoeDepth;
-        }
+      --next.left;
+      next.k = last ? 0 : next.k + 1;
+      next.at += last ? wrap : 16;
     }
-    if (ck > 0 && r.u1 > r.u0 && !mine) {  // the run lies inside a tile
+    fill = fill == (kMoeDepth - 1) * kSlot ? 0 : fill + kSlot;
+    asm volatile("cp.async.commit_group;" ::: "memory");  // (one per unit, empty after the last, for the waits to count)
+  };
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) own[(warp * NT + nt) * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+  for (int i = 0; i < kMoeDepth; ++i) fetch();
+  if constexpr (DOWN) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+
+  // ---- the jobs.  xtop and xdown alternate between two places: a warp may
+  // still finish a job's sums while others take in the next one's vectors.
+  int par = 0, take = 0;  // take: the ring's place of the next unit
+  for (int j = j0; j <= j1; ++j, par ^= 1) {
+    const int e = (int)(o.jobs[j] >> 17), np = (int)(o.jobs[j] & 63u);
+    const uint16_t *pair = o.order + (o.jobs[j] >> 6 & 2047u);
+
+    // Vectors into shared memory, 8 columns (a unit) at a time: copies of what
+    // lies in memory, bf16 or f16 of eighths, to their places; the scale of each
+    // vector; and, in place, f16 of that scale.
+    const int wide = (int)(p.cols / 8);  // units of a vector (nk * 32 with those past the end)
+    // unit u: step u / 32, lane quarter (u / 8) % 4, pair of k-steps u % 8
+    auto unit_at = [&](int n, int u) { return xs + (((u >> 5) * 8 + (u & 7)) * N + n) * 4 + ((u >> 3) & 3); };
+    if constexpr (DOWN) {
+      const int pieces = p.up_pitch / 16;
+      for (int i = tid; i < np * pieces; i += threads) {
+        const int n = i / pieces, q = i - n * pieces;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(ups + n * p.up_pitch + 16 * q))),
+                     "l"(p.h_up + (int64_t)pair[n] * p.up_pitch + 16 * q) : "memory");
+      }
+    }
+    for (int i = warp; i < np * nk; i += warps) {
+      const int n = i / nk, u = (i - n * nk) * 32 + lane, from = pair[n];
+      const void *v = DOWN ? (const void *)(p.h + (int64_t)from * p.cols)
+                           : (const void *)(static_cast<const __nv_bfloat16 *>(a.x) + (int64_t)(from / a.top_k) * a.x_stride);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                   ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(unit_at(n, u)))),
+                   "l"(static_cast<const uint4 *>(v) + (u < wide ? u : 0)), "r"(u < wide ? 16 : 0) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (DOWN) {
+      __syncthreads();
+      for (int n = warp; n < np; n += warps) {
+        int low = INT8_MAX;
+        for (int u = lane; u < wide; u += 32) low = min(low, (int)ups[n * p.up_pitch + u]);
+        low = __reduce_min_sync(~0u, low);
+        if (lane == 0) xtop[par * 32 + n] = low;
+      }
+    } else {
+      for (int i = warp; i < np * nk; i += warps) {  // (a thread reads the units that it copied)
+        const int n = i / nk, u = (i - n * nk) * 32 + lane;
+        const uint4 r = *unit_at(n, u);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        uint32_t m = 0u;  // (magnitudes of bf16 are in the order of their bits, NaN above infinity)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) m = __vmaxu2(m, w[b] & 0x7FFF7FFFu);
+        const unsigned top = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
+        if (lane == 0) atomicMax(&xtop[par * 32 + n], (int)(top << 16));
+      }
     }
     __syncthreads();
-    if (ck > 0 && r.u1 > r.u0 && mine) {  // the run ends inside a tile that it began: the next warps have the rest
-      for (int w = warp + 1; w < kMoeWarps; ++w) {
-        const Run o = run_of(j, w);
-        if (o.u0 >= (ct + 1) * nk) break;
-        if (o.u0 == o.u1) continue;
+    for (int i = warp; i < np * nk; i += warps) {
+      const int n = i / nk, u = (i - n * nk) * 32 + lane;
+      const int up = DOWN ? xtop[par * 32 + n] : f16_up((unsigned)xtop[par * 32 + n]);
+      if (u == 0) xdown[par * 32 + n] = pow2(-up);
+      // h: 2^(up of the vector - up of the unit), at least 2^-126, where nothing is left of 16 bits
+      const float f = pow2(DOWN ? max(up - (u < wide ? (int)ups[n * p.up_pitch + u] : up), -126) : up);
+      uint4 *to = unit_at(n, u);
+      const uint4 r = *to;
+      uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float4 v = own[(w * NT + nt) * 32 + lane];
-          acc[nt][0] += v.x, acc[nt][1] += v.y, acc[nt][2] += v.z, acc[nt][3] += v.w;
+      for (int b = 0; b < 4; ++b) {
+        float2 x;
+        if constexpr (DOWN) x = __half22float2(*reinterpret_cast<const __half2 *>(&w[b]));
+        else x = make_float2(__uint_as_float(w[b] << 16), __uint_as_float(w[b] & 0xFFFF0000u));
+        const __half2 y = __floats2half2_rn(x.x * f, x.y * f);
+        w[b] = *reinterpret_cast<const uint32_t *>(&y);
+      }
+      *to = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (tid < 32) xtop[(par ^ 1) * 32 + tid] = INT_MIN;
+    __syncthreads();
+
+    // ---- the run, with as many n-tiles as the job's pairs fill
+    auto products = [&](auto tiles_of_pairs) {
+      constexpr int A = decltype(tiles_of_pairs)::value;
+      const Run r = run_of(j, warp);
+      float acc[A][4];
+      auto clear = [&] {
+#pragma unroll
+        for (int nt = 0; nt < A; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+      };
+      clear();
+      const MoeMatrix &mv = DOWN ? a.down : a.up;
+      const float av = mv.alpha[e * mv.alpha_stride];
+      [[maybe_unused]] const float ag = GATED && !DOWN ? a.gate.alpha[e * a.gate.alpha_stride] : 0.0f;
+      // a tile's finished sums
+      auto finish_tile = [&](int t) {
+#pragma unroll
+        for (int nt = 0; nt < A; ++nt) {
+          const int n0 = 8 * nt + 2 * cq, m0 = min(n0, np - 1), m1 = min(n0 + 1, np - 1);
+          const bool one = n0 < np, two = n0 + 1 < np;
+          const int64_t p0 = pair[m0], p1 = pair[m1];
+          const float d0 = xdown[par * 32 + m0], d1 = xdown[par * 32 + m1];
+          if constexpr (DOWN) {
+            float *q = p.part + (int64_t)t * 16 + g;
+            if (one) {
+              q[p0 * a.hidden] = acc[nt][0] * av * d0;
+              q[p0 * a.hidden + 8] = acc[nt][2] * av * d0;
+            }
+            if (two) {
+              q[p1 * a.hidden] = acc[nt][1] * av * d1;
+              q[p1 * a.hidden + 8] = acc[nt][3] * av * d1;
+            }
+          } else {
+            // h of eight rows (this lane's and those of the other g): a common power of two
+            auto put = [&](float v, int64_t pr, int64_t row8, bool there) {
+              unsigned top = __float_as_uint(v) & 0x7FFFFFFFu;
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+              const int up = f16_up(top);
+              if (!there) return;
+              p.h[pr * a.inner + row8 * 8 + g] = __float2half_rn(v * pow2(up));
+              if (g == 0) p.h_up[pr * p.up_pitch + row8] = (int8_t)up;
+            };
+            if constexpr (GATED) {
+              float v[2] = {acc[nt][0] * ag * d0, acc[nt][1] * ag * d1};
+              activate(v, a.act);
+              put(v[0] * (acc[nt][2] * av * d0), p0, t, one);
+              put(v[1] * (acc[nt][3] * av * d1), p1, t, two);
+            } else {
+              float v[4] = {acc[nt][0] * av * d0, acc[nt][1] * av * d1, acc[nt][2] * av * d0, acc[nt][3] * av * d1};
+              activate(v, a.act);
+              put(v[0], p0, 2 * (int64_t)t, one);
+              put(v[1], p1, 2 * (int64_t)t, two);
+              put(v[2], p0, 2 * (int64_t)t + 1, one);
+              put(v[3], p1, 2 * (int64_t)t + 1, two);
+            }
+          }
+        }
+      };
+      int ct = r.u0 / nk, ck = r.u0 - ct * nk;  // counted from the part's first tile
+      bool mine = ck == 0;  // this warp takes the current tile's first step
+      auto put_own = [&] {
+#pragma unroll
+        for (int nt = 0; nt < A; ++nt)
+          if (8 * nt < np) own[(warp * NB + nt) * 32 + lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+      };
+      const uint4 *xl[A], *xk[A];  // this lane's column of the vectors, and its place in the current step
+#pragma unroll
+      for (int nt = 0; nt < A; ++nt) {
+        xl[nt] = xs + min(8 * nt + g, np - 1) * 4 + cq;
+        xk[nt] = xl[nt] + ck * 32 * N;
+      }
+      const int chunk0 = g * 8 + ((2 * cq) ^ g), chunk1 = g * 8 + ((2 * cq + 1) ^ g);
+      for (int left = r.u1 - r.u0; left > 0; --left) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth - 1) : "memory");
+        __syncwarp();
+        const uint4 *here = slots + take;
+        take = take == (kMoeDepth - 1) * (kSlot / 16) ? 0 : take + kSlot / 16;
+        uint32_t sc[2][2][2];  // [half][row][block]: f16 pairs {Delta, Delta}
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t *words = reinterpret_cast<const uint32_t *>(here + 128) + lane;
+          uint32_t word;
+          if constexpr (WIDE) {
+            word = words[h * 32];
+          } else {
+            const MoeMatrix &m = DOWN ? a.down : GATED && h == 0 ? a.gate : a.up;
+            const int64_t row = (int64_t)(r.t0 + ct) * kTileRows + (GATED && !DOWN ? 0 : 8 * h) + g;
+            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(m.scales) + e * m.scale_stride + row * nblk) & 3u;
+            word = __funnelshift_r(words[h * 64], words[h * 64 + 32], 8 * off);
+          }
+          uint32_t f[2];
+          asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+              : "=r"(f[0]), "=r"(f[1]) : "r"(word));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            sc[half][h][0] = __byte_perm(f[half], 0u, 0x1010);
+            sc[half][h][1] = __byte_perm(f[half], 0u, 0x3232);
+          }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint4 c0 = here[half ? chunk1 : chunk0], c1 = here[64 + (half ? chunk1 : chunk0)];
+          const uint32_t cw[2][4] = {{c0.x, c0.y, c0.z, c0.w}, {c1.x, c1.y, c1.z, c1.w}};
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {  // a word of codes: 8 columns, two k-steps
+            uint32_t w[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              e2m1x8_f16(cw[h][jj], w[h]);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) w[h][b] = mul_f16x2(w[h][b], sc[half][h][jj >> 1]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < A; ++nt) {
+              const uint4 xb = xk[nt][(half * 4 + jj) * (4 * N)];
+              mma_f16(acc[nt], w[0][0], w[1][0], w[0][1], w[1][1], xb.x, xb.y);
+              mma_f16(acc[nt], w[0][2], w[1][2], w[0][3], w[1][3], xb.z, xb.w);
+            }
+          }
+        }
+        __syncwarp();
+        fetch();  // into the place just read
+#pragma unroll
+        for (int nt = 0; nt < A; ++nt) xk[nt] += 32 * N;
+        if (++ck == nk) {  // the tile's last step
+          if (mine) finish_tile(r.t0 + ct);
+          else put_own();
+          clear();
+#pragma unroll
+          for (int nt = 0; nt < A; ++nt) xk[nt] = xl[nt];
+          ck = 0;
+          ++ct;
+          mine = true;
         }
       }
-      finish_tile(r.t0 + ct);
+      const bool open = ck > 0 && r.u1 > r.u0;  // the run ends inside a tile
+      if (open && !mine) put_own();
+      __syncthreads();
+      if (open && mine) {  // that it began: the next warps have the rest
+        for (int w = warp + 1; w < warps; ++w) {
+          const Run o = run_of(j, w);
+          if (o.u0 >= (ct + 1) * nk) break;
+          if (o.u0 == o.u1) continue;
+#pragma unroll
+          for (int nt = 0; nt < A; ++nt) {
+            if (8 * nt >= np) break;
+            const float4 v = own[(w * NB + nt) * 32 + lane];
+            acc[nt][0] += v.x, acc[nt][1] += v.y, acc[nt][2] += v.z, acc[nt][3] += v.w;
+          }
+        }
+        finish_tile(r.t0 + ct);
+      }
+    };
+    if (np <= 8) products(std::integral_constant<int, 1>());
+    else if constexpr (NT > 1) {
+      if (np <= 16) products(std::integral_constant<int, 2>());
+      else products(std::integral_constant<int, 4>());
     }
   }
 }
@@ -447,13 +612,10 @@ __global__ void __launch_bounds__(256) k_moe_join(const __grid_constant__ MoeLau
 
 namespace {
 
-// Pairs of a job: as many as the vectors' room in shared memory allows, up to
-// 32 (four n-tiles of accumulators), no more than the call has.
-int moe_group(int64_t cols, int experts, int pairs) {
-  for (int n = std::min(pairs, 32); n > 0; --n) {
-    const int nt = n <= 8 ? 1 : n <= 16 ? 2 : 4;
-    if ((cols + 127) / 128 * 256 * n + moe_fixed_smem(experts, pairs, nt) <= kMoeSmem) return n;
-  }
+// Pairs of a job at most, of those wanted, for the vectors' room in shared memory.
+int moe_group(int wanted, int64_t cols, bool down, int warps, bool wide, int experts, int pairs, int64_t room) {
+  for (int n = wanted; n > 0; --n)
+    if (moe_smem(n, cols, down, warps, wide, experts, pairs) <= room) return n;
   return 0;
 }
 
@@ -465,8 +627,7 @@ auto with_kernel(int nt, bool down, bool gated, bool wide, F f) {
     return down ? f(k_moe<N, true, false, W>) : gated ? f(k_moe<N, false, true, W>) : f(k_moe<N, false, false, W>);
   };
   auto pick_nt = [&](auto w) {
-    return nt == 1 ? pick_wide(w, std::integral_constant<int, 1>()) : nt == 2 ? pick_wide(w, std::integral_constant<int, 2>())
-                                                                             : pick_wide(w, std::integral_constant<int, 4>());
+    return nt == 1 ? pick_wide(w, std::integral_constant<int, 1>()) : pick_wide(w, std::integral_constant<int, 4>());
   };
   return wide ? pick_nt(std::true_type()) : pick_nt(std::false_type());
 }
@@ -489,36 +650,52 @@ cudaError_t launch_dependent(K *k, int grid, int threads, size_t smem, const Moe
 cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
   const MoeArgs &a = p.a;
   p.cols = down ? a.inner : a.hidden;
-  p.steps = (int)((p.cols + 127) / 128);
+  p.steps = (int)((p.cols + 255) / 256);
   p.tiles = (int)(down ? a.hidden / 16 : a.gated ? a.inner / 8 : a.inner / 16);
-  p.group = moe_group(p.cols, a.experts, p.pairs);
-  const int nt = p.group <= 8 ? 1 : p.group <= 16 ? 2 : 4;
-  const size_t smem = (size_t)p.steps * 256 * p.group + moe_fixed_smem(a.experts, p.pairs, nt);
   auto wide_matrix = [&](const MoeMatrix &m) {
-    return ((reinterpret_cast<uintptr_t>(m.codes) | m.code_stride) % 16 | (reinterpret_cast<uintptr_t>(m.scales) | m.scale_stride) % 2) == 0;
+    return ((reinterpret_cast<uintptr_t>(m.codes) | m.code_stride) % 16 | (reinterpret_cast<uintptr_t>(m.scales) | m.scale_stride) % 4) == 0;
   };
-  const bool wide = p.cols % 32 == 0 && (down ? wide_matrix(a.down) : wide_matrix(a.up) && (!a.gated || wide_matrix(a.gate)));
-  return with_kernel(nt, down, a.gated, wide, [&](auto *k) { return launch_dependent(k, sms, kMoeThreads, smem, p, st); });
+  const bool wide = p.cols % 64 == 0 && (down ? wide_matrix(a.down) : wide_matrix(a.up) && (!a.gated || wide_matrix(a.gate)));
+  // Pairs that a job should take: few experts have more than three times the mean and four.
+  const int wanted = std::min({p.pairs, 32, 4 + 3 * p.pairs / a.experts});
+  int warps = 8, ctas = 2 * sms;
+  p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, kMoeHalfSmem);
+  if (p.group < wanted) {
+    warps = kMoeMaxWarps, ctas = sms;
+    p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, kMoeSmem);
+  }
+  if (p.group == 0) {  // vectors too long for that many units in flight
+    warps = 8;
+    p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, kMoeSmem);
+  }
+  const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, wide, a.experts, p.pairs);
+  return with_kernel(p.group <= 8 ? 1 : 4, down, a.gated, wide,
+                     [&](auto *k) { return launch_dependent(k, ctas, warps * 32, smem, p, st); });
 }
 
-size_t moe_h_bytes(int64_t inner, int pairs) { return ((size_t)pairs * inner * 4 + 255) / 256 * 256; }
+size_t moe_h_bytes(int64_t inner, int pairs) { return ((size_t)pairs * inner * 2 + 255) / 256 * 256; }
+size_t moe_up_bytes(int64_t inner, int pairs) { return ((size_t)pairs * moe_up_pitch(inner) + 255) / 256 * 256; }
 
 }  // namespace
 
 bool moe_fits(int64_t hidden, int64_t inner, int experts, int pairs) {
-  return moe_group(hidden, experts, pairs) > 0 && moe_group(inner, experts, pairs) > 0;
+  return moe_group(1, hidden, false, 8, false, experts, pairs, kMoeSmem) > 0 &&
+         moe_group(1, inner, true, 8, false, experts, pairs, kMoeSmem) > 0;
 }
 
 size_t moe_workspace_bytes(int64_t hidden, int64_t inner, int pairs) {
-  return moe_h_bytes(inner, pairs) + (size_t)pairs * hidden * 4;
+  return moe_h_bytes(inner, pairs) + moe_up_bytes(inner, pairs) + (size_t)pairs * hidden * 4;
 }
 
 cudaError_t launch_moe(const MoeArgs &a, int sms, void *ws, cudaStream_t st) {
   MoeLaunch p = {};
   p.a = a;
   p.pairs = a.tokens * a.top_k;
-  p.h = static_cast<float *>(ws);
-  p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + moe_h_bytes(a.inner, p.pairs));
+  p.up_pitch = moe_up_pitch(a.inner);
+  char *at = static_cast<char *>(ws);
+  p.h = reinterpret_cast<__half *>(at);
+  p.h_up = reinterpret_cast<int8_t *>(at += moe_h_bytes(a.inner, p.pairs));
+  p.part = reinterpret_cast<float *>(at += moe_up_bytes(a.inner, p.pairs));
   cudaError_t e = launch_product(p, false, sms, st);
   if (e == cudaSuccess) e = launch_product(p, true, sms, st);
   if (e != cudaSuccess) return e;
@@ -527,7 +704,7 @@ cudaError_t launch_moe(const MoeArgs &a, int sms, void *ws, cudaStream_t st) {
 
 cudaError_t prepare_moe_kernels() {
   cudaError_t e = cudaSuccess;
-  for (int nt : {1, 2, 4})
+  for (int nt : {1, 4})
     for (int form : {0, 1, 2})
       for (bool wide : {false, true})
         if (e == cudaSuccess)

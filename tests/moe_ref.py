@@ -31,8 +31,8 @@ def moe(up, down, gate, x, ids, wts, act, residual=None):
     """(y, bound): the layer's output, and how far it may be off before its
     rounding to bf16.  x enters the products off by at most 2^-39 of its largest
     entry; no activation is steeper than 1.13, their functions are good to
-    2^-20 of their argument; h is rounded to 11 bits (2^-12 of an entry, or
-    2^-39 of the largest); the slots' sum rounds top_k + 2 times."""
+    2^-20 of their argument; h is rounded to 11 bits (2^-12 of an entry),
+    and twice to a grid of 2^-38 of a largest entry at most (2^-39 each); the slots' sum rounds top_k + 2 times."""
     tokens, k = ids.shape
     hidden = x.shape[1]
     y, err = np.zeros((tokens, hidden)), np.zeros((tokens, hidden))
@@ -59,7 +59,7 @@ def moe(up, down, gate, x, ids, wts, act, residual=None):
             else:
                 h, eh = activation(h, act), 1.13 * eh + 2.0 ** -20 * np.abs(h)
             eh = eh + 2.0 ** -24 * np.abs(h)
-            eh = eh + 2.0 ** -12 * (np.abs(h) + eh) + 2.0 ** -39 * (np.abs(h) + eh).max()
+            eh = eh + 2.0 ** -12 * (np.abs(h) + eh) + 2.0 ** -38 * (np.abs(h) + eh).max()
             o, eo = _product(*matrix("down", down, e), h, eh)
             w = float(wts[t, s])
             y[t] += w * o
