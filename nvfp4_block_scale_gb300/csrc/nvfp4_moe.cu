@@ -44,7 +44,7 @@
 
 namespace nvfp4 {
 
-constexpr int kMoeDepth = 3;            // units of 256 columns in flight per warp
+constexpr int kMoeDepth = 2, kMoeDeep = 5;  // units of 256 columns in flight per warp
 constexpr int kMoeMaxWarps = 16;        // of a CTA
 constexpr int kMoeSmem = 226 * 1024;    // dynamic shared memory of a CTA that has an SM to itself
 constexpr int kMoeHalfSmem = 112 * 1024;  // of one of two
@@ -59,7 +59,9 @@ struct MoeLaunch {
   int pairs;          // tokens * top_k
   int group;          // pairs of a job at most
   int steps;          // of 256 columns
+  int depth;          // units in flight per warp: kMoeDepth or kMoeDeep
   int tiles;          // of a job
+  int job_cost;       // of a job of four besides its tiles
   int64_t cols;       // of this launch's matrices
 };
 
@@ -79,17 +81,22 @@ __host__ __device__ constexpr int moe_slot(bool wide) { return wide ? 2304 : 256
 __host__ __device__ constexpr int moe_up_pitch(int64_t cols) { return (int)((cols / 8 + 15) / 16 * 16); }
 // Shared memory: the vectors (with h's exponents), the warps' units in flight
 // and partial sums, the vectors' scales, the plan.
-__host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, bool wide, int experts, int pairs) {
+__host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, int depth, bool wide, int experts, int pairs) {
   return (cols + 255) / 256 * 512 * group + (down ? (int64_t)group * moe_up_pitch(cols) : 0) +
-         (int64_t)warps * (kMoeDepth * moe_slot(wide) + (group + 7) / 8 * 512) + 512 +
+         (int64_t)warps * (depth * moe_slot(wide) + (group + 7) / 8 * 512) + 512 +
          (pairs > kMoeFewPairs ? (int64_t)experts * 8 : 0) + ((int64_t)pairs + 1) * 14 + 64;
 }
 
 // A job: an expert's pairs order[at .. at + n).
 __device__ __forceinline__ uint32_t moe_job(int expert, int at, int n) { return (uint32_t)expert << 17 | (uint32_t)at << 6 | (uint32_t)n; }
 static_assert(kMaxExperts <= 1024 && kMoeSlicePairs <= 2048, "a job's fields");
-// A tile's cost: its weights' way, and less for each further n-tile of pairs.
-__device__ __forceinline__ int moe_tile_cost(int pairs) { return 8 + (pairs - 1) / 8; }
+// A tile's cost: its weights' way, and three eighths of that for each further n-tile of
+// pairs (61 tokens 2048 x 768, 8 of 128: a tile of 9 .. 16 pairs took 1.44 times one of
+// up to 8; 256 tokens 2064 x 1424, 6 of 60: 1.2, and 1.4 with a third n-tile).
+__device__ __forceinline__ int moe_tile_cost(int pairs) { return 8 + 3 * ((pairs - 1) / 8); }
+// And a job's besides its tiles: mostly its vectors' way into shared memory.
+__device__ __forceinline__ int moe_begin_cost(const MoeLaunch &p, int pairs) { return p.job_cost * (4 + pairs) / 8; }
+__device__ __forceinline__ int moe_job_cost(const MoeLaunch &p, int pairs) { return moe_begin_cost(p, pairs) + p.tiles * moe_tile_cost(pairs); }
 
 // The plan: the pairs that have an expert by expert, ascending, so that every
 // CTA cuts an expert's into the same jobs; the jobs, and the cost of those
@@ -113,7 +120,7 @@ __device__ void moe_plan_few(const MoeLaunch &p, const MoePlan &o, int lane) {
   const uint32_t same = __match_any_sync(~0u, e), before = same & ((1u << lane) - 1u);
   const int pos = __popc(before), n = min(N, __popc(same) - pos);  // pairs from here to the job's end, at a job's first
   const bool first = there && pos % N == 0;
-  const int cost = first ? p.tiles * moe_tile_cost(n) : 0;
+  const int cost = first ? moe_job_cost(p, n) : 0;
   int rank = 0, job = 0, start = 0;
 #pragma unroll
   for (int l = 0; l < 32; ++l) {
@@ -144,7 +151,7 @@ __device__ void moe_plan(const MoeLaunch &p, const MoePlan &o, int tid, int thre
   int total = 0, named = 0, cost = 0;  // jobs; pairs that have an expert; the jobs' cost
   for (int e0 = 0; e0 < E; e0 += threads) {
     const int e = e0 + tid, n = e < E ? o.count[e] : 0, j = (n + N - 1) / N;
-    const int c = j > 0 ? p.tiles * ((j - 1) * moe_tile_cost(N) + moe_tile_cost(n - (j - 1) * N)) : 0;
+    const int full = moe_job_cost(p, N), c = j > 0 ? (j - 1) * full + moe_job_cost(p, n - (j - 1) * N) : 0;
     int sn = n, sj = j, sc = c;  // inclusive sums over the warp, then over the warps
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -163,7 +170,7 @@ __device__ void moe_plan(const MoeLaunch &p, const MoePlan &o, int tid, int thre
       o.end[e] = bn;  // (its first pair, until they are found)
       for (int i = 0; i < j; ++i) {
         o.jobs[bj + i] = moe_job(e, bn + i * N, min(N, n - i * N));
-        o.start[bj + i] = bc + i * p.tiles * moe_tile_cost(N);
+        o.start[bj + i] = bc + i * full;
       }
     }
     __syncthreads();
@@ -191,7 +198,9 @@ __device__ void moe_plan(const MoeLaunch &p, const MoePlan &o, int tid, int thre
 // n-tiles that the group's pairs fill at most.
 template <int NT, bool DOWN, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_constant__ MoeLaunch p) {
-  extern __shared__ uint4 dsm[];
+  // Rows of codes lie in whole 128-byte lines of shared memory: where they lay across
+  // two, each copy took four times the requests to L2 and 2.5 times the sectors.
+  extern __shared__ __align__(128) uint4 dsm[];
   __shared__ int scan[3][kMoeMaxWarps], jobs_there;
   const MoeArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
@@ -200,8 +209,8 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   constexpr int kSlot = moe_slot(WIDE);
   uint4 *xs = dsm;                                                        // [nk][8][N][4] 16-byte units of f16
   uint4 *slots = dsm + (size_t)nk * 32 * N;                               // [warps][depth][kSlot / 16]: units in flight
-  float4 *own = reinterpret_cast<float4 *>(slots + warps * kMoeDepth * (kSlot / 16));  // [warps][NB][32]
-  slots += warp * kMoeDepth * (kSlot / 16);
+  float4 *own = reinterpret_cast<float4 *>(slots + warps * p.depth * (kSlot / 16));  // [warps][NB][32]
+  slots += warp * p.depth * (kSlot / 16);
   int8_t *ups = reinterpret_cast<int8_t *>(own + warps * NB * 32);        // [N][up_pitch]
   float *xdown = reinterpret_cast<float *>(ups + (DOWN ? N * p.up_pitch : 0));  // [2][32]: the vectors' scales, undone
   int *xtop = reinterpret_cast<int *>(xdown + 64);                        // [2][32]: their largest entries' bits, or their scales' exponents
@@ -232,7 +241,9 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
 
   // ---- this CTA's tiles: the job and the tile at two places of the total cost
   const int total = jobs_there, cost = o.start[total];
-  auto place = [&](int64_t at, int *job, int *tile) {
+  auto place = [&](uint32_t share, int *job, int *tile) {
+    const uint32_t whole = (uint32_t)cost / gridDim.x, rest = (uint32_t)cost - whole * gridDim.x;
+    const int at = (int)(share * whole + share * rest / gridDim.x);  // (both factors below 2^16)
     int lo = 0, hi = total;
     while (lo < hi) {  // the last job that starts at `at` or before, or `total`
       const int mid = (lo + hi + 1) / 2;
@@ -240,11 +251,12 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       else hi = mid - 1;
     }
     *job = lo;
-    *tile = lo < total ? (int)(at - o.start[lo]) / moe_tile_cost(o.jobs[lo] & 63u) : 0;
+    const int n = lo < total ? (int)(o.jobs[lo] & 63u) : 1;
+    *tile = lo < total ? max(at - o.start[lo] - moe_begin_cost(p, n), 0) / moe_tile_cost(n) : 0;
   };
   int j0, t0, j1, t1;
-  place((int64_t)blockIdx.x * cost / gridDim.x, &j0, &t0);
-  place((int64_t)(blockIdx.x + 1) * cost / gridDim.x, &j1, &t1);
+  place(blockIdx.x, &j0, &t0);
+  place(blockIdx.x + 1, &j1, &t1);
   if (j0 == j1 && t0 == t1) {
     if constexpr (DOWN) {
       pdl_wait();
@@ -335,29 +347,17 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       next.k = last ? 0 : next.k + 1;
       next.at += last ? wrap : 16;
     }
-    fill = fill == (kMoeDepth - 1) * kSlot ? 0 : fill + kSlot;
+    fill = fill == (p.depth - 1) * kSlot ? 0 : fill + kSlot;
     asm volatile("cp.async.commit_group;" ::: "memory");  // (one per unit, empty after the last, for the waits to count)
   };
-#pragma unroll
-  for (int i = 0; i < kMoeDepth; ++i) fetch();
-  if constexpr (DOWN) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
-
-  // ---- the jobs.  xtop and xdown alternate between two places: a warp may
-  // still finish a job's sums while others take in the next one's vectors.
-  int par = 0, take = 0;  // take: the ring's place of the next unit
-  for (int j = j0; j <= j1; ++j, par ^= 1) {
-    const int e = (int)(o.jobs[j] >> 17), np = (int)(o.jobs[j] & 63u);
-    const uint16_t *pair = o.order + (o.jobs[j] >> 6 & 2047u);
-
-    // Vectors into shared memory, 8 columns (a unit) at a time: copies of what
-    // lies in memory, bf16 or f16 of eighths, to their places; the scale of each
-    // vector; and, in place, f16 of that scale.
-    const int wide = (int)(p.cols / 8);  // units of a vector (nk * 32 with those past the end)
-    // unit u: step u / 32, lane quarter (u / 8) % 4, pair of k-steps u % 8
-    auto unit_at = [&](int n, int u) { return xs + (((u >> 5) * 8 + (u & 7)) * N + n) * 4 + ((u >> 3) & 3); };
+  // A job's vectors into shared memory, 8 columns (a unit) at a time: copies of
+  // what lies in memory, bf16 or f16 of eighths, to their places.
+  const int wide = (int)(p.cols / 8);  // units of a vector (nk * 32 with those past the end)
+  // unit u: step u / 32, lane quarter (u / 8) % 4, pair of k-steps u % 8
+  auto unit_at = [&](int n, int u) { return xs + (((u >> 5) * 8 + (u & 7)) * N + n) * 4 + ((u >> 3) & 3); };
+  auto take_in = [&](uint32_t job) {
+    const int np = (int)(job & 63u);
+    const uint16_t *pair = o.order + (job >> 6 & 2047u);
     if constexpr (DOWN) {
       const int pieces = p.up_pitch / 16;
       for (int i = tid; i < np * pieces; i += threads) {
@@ -375,7 +375,32 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
                    ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(unit_at(n, u)))),
                    "l"(static_cast<const uint4 *>(v) + (u < wide ? u : 0)), "r"(u < wide ? 16 : 0) : "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // (x before the weights, which take longer; h is not there yet)
+  if constexpr (!DOWN) take_in(o.jobs[j0]);
+#pragma unroll 1
+  for (int i = 0; i < p.depth; ++i) fetch();
+  if constexpr (DOWN) {
+    pdl_wait();
+    pdl_launch_dependents();
+  }
+
+  // ---- the jobs.  xtop and xdown alternate between two places: a warp may
+  // still finish a job's sums while others take in the next one's vectors.
+  int par = 0, take = 0;  // take: the ring's place of the next unit
+  for (int j = j0; j <= j1; ++j, par ^= 1) {
+    const int e = (int)(o.jobs[j] >> 17), np = (int)(o.jobs[j] & 63u);
+    const uint16_t *pair = o.order + (o.jobs[j] >> 6 & 2047u);
+
+    // the vectors; the scale of each; and, in place, f16 of that scale
+    if (DOWN || j > j0) {
+      take_in(o.jobs[j]);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      if (p.depth == kMoeDepth) asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth) : "memory");
+      else asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDeep) : "memory");
+    }
     if constexpr (DOWN) {
       __syncthreads();
       for (int n = warp; n < np; n += warps) {
@@ -492,10 +517,11 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       }
       const int chunk0 = g * 8 + ((2 * cq) ^ g), chunk1 = g * 8 + ((2 * cq + 1) ^ g);
       for (int left = r.u1 - r.u0; left > 0; --left) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth - 1) : "memory");
+        if (p.depth == kMoeDepth) asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth - 1) : "memory");
+        else asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDeep - 1) : "memory");
         __syncwarp();
         const uint4 *here = slots + take;
-        take = take == (kMoeDepth - 1) * (kSlot / 16) ? 0 : take + kSlot / 16;
+        take = take == (p.depth - 1) * (kSlot / 16) ? 0 : take + kSlot / 16;
         uint32_t sc[2][2][2];  // [half][row][block]: f16 pairs {Delta, Delta}
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -589,13 +615,22 @@ __global__ void __launch_bounds__(256) k_moe_join(const __grid_constant__ MoeLau
   if (i >= quads * a.tokens) return;
   const int64_t t = i / quads, c = (i - t * quads) * 4;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < a.top_k; ++s) {
-    const int64_t at = t * a.top_k + s;
-    const int e = a.ids[at];
-    if (e < 0 || e >= a.experts) continue;
-    const float w = a.weights[at];
-    const float4 o = *reinterpret_cast<const float4 *>(p.part + at * a.hidden + c);
-    v[0] = fmaf(w, o.x, v[0]), v[1] = fmaf(w, o.y, v[1]), v[2] = fmaf(w, o.z, v[2]), v[3] = fmaf(w, o.w, v[3]);
+  for (int s0 = 0; s0 < a.top_k; s0 += 8) {  // eight slots' loads at a time
+    float w[8];
+    float4 o[8];
+    bool there[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = t * a.top_k + min(s0 + i, a.top_k - 1);
+      const int e = a.ids[at];
+      there[i] = s0 + i < a.top_k && e >= 0 && e < a.experts;
+      w[i] = a.weights[at];
+      o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (there[i]) o[i] = *reinterpret_cast<const float4 *>(p.part + at * a.hidden + c);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (there[i]) v[0] = fmaf(w[i], o[i].x, v[0]), v[1] = fmaf(w[i], o[i].y, v[1]), v[2] = fmaf(w[i], o[i].z, v[2]), v[3] = fmaf(w[i], o[i].w, v[3]);
   }
   const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(a.residual);
   if (res) {
@@ -613,9 +648,9 @@ __global__ void __launch_bounds__(256) k_moe_join(const __grid_constant__ MoeLau
 namespace {
 
 // Pairs of a job at most, of those wanted, for the vectors' room in shared memory.
-int moe_group(int wanted, int64_t cols, bool down, int warps, bool wide, int experts, int pairs, int64_t room) {
+int moe_group(int wanted, int64_t cols, bool down, int warps, int depth, bool wide, int experts, int pairs, int64_t room) {
   for (int n = wanted; n > 0; --n)
-    if (moe_smem(n, cols, down, warps, wide, experts, pairs) <= room) return n;
+    if (moe_smem(n, cols, down, warps, depth, wide, experts, pairs) <= room) return n;
   return 0;
 }
 
@@ -658,17 +693,26 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
   const bool wide = p.cols % 64 == 0 && (down ? wide_matrix(a.down) : wide_matrix(a.up) && (!a.gated || wide_matrix(a.gate)));
   // Pairs that a job should take: few experts have more than three times the mean and four.
   const int wanted = std::min({p.pairs, 32, 4 + 3 * p.pairs / a.experts});
-  int warps = 8, ctas = 2 * sms;
-  p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, kMoeHalfSmem);
+  // Little work: one small CTA per SM, so that the next launch's CTAs find room beside it.
+  p.job_cost = std::min(576 / p.steps, p.tiles);
+  const bool little = (int64_t)std::min(p.pairs, a.experts) * p.tiles * p.steps <= (int64_t)64 * sms;
+  int warps = 8, ctas = little ? sms : 2 * sms;
+  auto fit = [&](int64_t room) { p.group = moe_group(wanted, p.cols, down, warps, p.depth, wide, a.experts, p.pairs, room); };
+  p.depth = kMoeDeep;
+  if (little) fit(kMoeHalfSmem);
+  if (!little || p.group < wanted) {
+    p.depth = kMoeDepth;
+    fit(kMoeHalfSmem);
+  }
   if (p.group < wanted) {
     warps = kMoeMaxWarps, ctas = sms;
-    p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, kMoeSmem);
+    fit(kMoeSmem);
   }
   if (p.group == 0) {  // vectors too long for that many units in flight
     warps = 8;
-    p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, kMoeSmem);
+    fit(kMoeSmem);
   }
-  const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, wide, a.experts, p.pairs);
+  const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, p.depth, wide, a.experts, p.pairs);
   return with_kernel(p.group <= 8 ? 1 : 4, down, a.gated, wide,
                      [&](auto *k) { return launch_dependent(k, ctas, warps * 32, smem, p, st); });
 }
@@ -679,8 +723,8 @@ size_t moe_up_bytes(int64_t inner, int pairs) { return ((size_t)pairs * moe_up_p
 }  // namespace
 
 bool moe_fits(int64_t hidden, int64_t inner, int experts, int pairs) {
-  return moe_group(1, hidden, false, 8, false, experts, pairs, kMoeSmem) > 0 &&
-         moe_group(1, inner, true, 8, false, experts, pairs, kMoeSmem) > 0;
+  return moe_group(1, hidden, false, 8, kMoeDepth, false, experts, pairs, kMoeSmem) > 0 &&
+         moe_group(1, inner, true, 8, kMoeDepth, false, experts, pairs, kMoeSmem) > 0;
 }
 
 size_t moe_workspace_bytes(int64_t hidden, int64_t inner, int pairs) {
