@@ -384,12 +384,12 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
  *   the score.  Weights are fp32.  Results repeat bit for bit.
  * Arguments:
  *   x       device, bf16, 16-byte aligned, [tokens][hidden], rows x_stride
- *           elements apart (>= hidden, a multiple of 8).
- *   tokens  >= 0.  hidden >= 8, a multiple of 8, below 2^31.
+ *           elements apart (>= hidden, a multiple of 8).  x and router finite.
+ *   tokens  0 .. 2^31 - 1.  hidden >= 8, a multiple of 8, below 2^31.
  *   router  device, 16-byte aligned, bf16 or fp32 (router_dtype), [experts]
  *           [hidden], rows router_stride elements apart (a multiple of 8, or 4 for fp32).
  *   experts 1 .. 1024.  top_k 1 .. min(32, experts).
- *   bias    device, fp32, [experts], or NULL for 0 (sigmoid only).
+ *   bias    device, fp32, [experts], or NULL for 0.  NULL with softmax.
  *   renormalize  0 or 1.  scale finite.
  *   ids     device, int32, [tokens][top_k] (written).
  *   weights device, fp32, [tokens][top_k] (written).

@@ -27,6 +27,8 @@ ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
                "silu": ACT_SILU}
 DTYPE_BF16, DTYPE_FP32, DTYPE_E4M3 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORINGS = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 _lib = None
 _raw_stream = None
@@ -107,6 +109,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_paged_attention.argtypes = [ctypes.POINTER(nvfp4_kv_cache), vp, i64, i64, ci, vp, vp, i64, i64,
                                         ctypes.c_float, i64, vp, vp, vp, i64, vp]
     L.nvfp4_paged_attention.restype = ci
+    L.nvfp4_moe_route.argtypes = [vp, i64, i64, vp, ci, i64, i64, ci, vp, ci, ci, ctypes.c_float, ci, vp, vp, vp]
+    L.nvfp4_moe_route.restype = ci
     L.nvfp4_moe_workspace_bytes.argtypes = [ctypes.POINTER(nvfp4_experts), i64, ci]
     L.nvfp4_moe_workspace_bytes.restype = i64
     L.nvfp4_moe.argtypes = [ctypes.POINTER(nvfp4_experts), vp, i64, i64, ci, vp, vp, ci, vp, i64, vp, i64, vp, i64, vp]
@@ -210,6 +214,12 @@ def nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table
                           window, out, lse, workspace, workspace_bytes, stream) -> int:
     return load().nvfp4_paged_attention(cache, q, q_stride, sequences, q_heads, lengths, table, table_width,
                                         table_stride, scale, window, out, lse, workspace, workspace_bytes, stream)
+
+
+def nvfp4_moe_route(x, x_stride, tokens, router, router_dtype, router_stride, hidden, experts, bias, scoring, renormalize,
+                    scale, top_k, ids, weights, stream) -> int:
+    return load().nvfp4_moe_route(x, x_stride, tokens, router, router_dtype, router_stride, hidden, experts, bias, scoring,
+                                  renormalize, scale, top_k, ids, weights, stream)
 
 
 def nvfp4_moe_workspace_bytes(experts, tokens, top_k) -> int:
@@ -681,6 +691,43 @@ def paged_attention(cache: KVCache, q, table, lengths, scale=None, window: int =
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wb,
         _on(cache.device, stream)), "nvfp4_paged_attention")
     return (out, lse) if return_lse else out
+
+
+def moe_route(x, router, top_k: int, scoring: str = "softmax", renormalize: bool = True, bias=None, scale: float = 1.0,
+              stream=None):
+    """The router of a mixture-of-experts layer: (ids int32, weights fp32), both
+    [tokens, top_k], of each token's top_k experts in descending order of their
+    scores, for bf16 x [tokens, hidden] and a bf16 or fp32 router [experts,
+    hidden] (rows may lie further apart than their width).  scoring "softmax":
+    chosen by the logits, weighted by their softmax over all experts;
+    "sigmoid": chosen by sigmoid(logit) + bias (fp32 [experts] or None), weighted
+    by the sigmoid.  renormalize: a token's weights sum to 1; scale multiplies
+    them.  See nvfp4_moe_route in include/nvfp4.h."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be a bf16 CUDA tensor [tokens, hidden]")
+    tokens, hidden = x.shape
+    xp, xs = _rows_of(x, tokens, hidden, "x")
+    kind = router.dtype
+    if (kind is not torch.bfloat16 and kind is not torch.float32) or router.device != x.device or router.dim() != 2 or \
+            router.shape[1] != hidden or (hidden > 1 and router.stride(1) != 1):
+        raise ValueError(f"router must be a bf16 or fp32 tensor [experts, {hidden}] with contiguous rows on x's device")
+    experts = router.shape[0]
+    if scoring not in SCORINGS:
+        raise ValueError(f"scoring must be one of {sorted(SCORINGS)}")
+    bp = None
+    if bias is not None:
+        if scoring != "sigmoid" or bias.dtype is not torch.float32 or bias.device != x.device or \
+                bias.shape != (experts,) or not bias.is_contiguous():
+            raise ValueError("bias goes with sigmoid: a contiguous fp32 tensor [experts] on x's device")
+        bp = bias.data_ptr()
+    ids = _empty((tokens, top_k), torch.int32, x.device, stream)
+    weights = _empty((tokens, top_k), torch.float32, x.device, stream)
+    _check((_lib or load()).nvfp4_moe_route(
+        xp, xs, tokens, router.data_ptr(), DTYPE_FP32 if kind is torch.float32 else DTYPE_BF16,
+        router.stride(0) if experts > 1 else (hidden + 7) // 8 * 8, hidden, experts, bp, SCORINGS[scoring], bool(renormalize),
+        scale, top_k, ids.data_ptr(), weights.data_ptr(), _on(x.device, stream)), "nvfp4_moe_route")
+    return ids, weights
 
 
 class Experts:

@@ -277,8 +277,8 @@ int take_workspace(void **ws, void **own, int64_t given, size_t need, const DevI
 
 enum { kTrAmax = 0, kTrQuantMax, kTrQuantFos, kTrCjsoInit, kTrCjsoIter, kTrDecoupled, kTrDequant, kTrEncode,
        kTrGroupAmax, kTrGroupQuantMax, kTrGroupQuantFos, kTrGemv, kTrSwizzle, kTrAmaxLdg, kTrGemmTc,
-       kTrGemmTcReduce, kTrLinear, kTrLinearTcF16, kTrLinearTcBf16, kTrKvAppend, kTrAttend, kTrMoe,
-       kTrKinds };
+       kTrGemmTcReduce, kTrLinear, kTrLinearTcF16, kTrLinearTcBf16, kTrKvAppend, kTrAttend, kTrMoeRoute,
+       kTrMoe, kTrKinds };
 const char *const kTraceNames[kTrKinds] = {"k_amax_bulk",        "k_quant_max_fos<max>", "k_quant_max_fos<fos>",
                                            "k_cjso_sweep<init>",  "k_cjso_sweep<iter>",   "k_decoupled",
                                            "k_dequant",           "k_encode",             "k_group_amax",
@@ -286,7 +286,7 @@ const char *const kTraceNames[kTrKinds] = {"k_amax_bulk",        "k_quant_max_fo
                                            "k_swizzle_scales",   "k_amax_partials",      "k_gemm_tc",
                                            "k_gemm_tc_reduce",   "k_linear",             "k_linear_tc<f16>",
                                            "k_linear_tc<bf16>",  "k_kv_append",          "k_attend",
-                                           "k_moe"};
+                                           "k_moe_route",         "k_moe"};
 
 struct TraceRec {
   int kind;
@@ -764,6 +764,33 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
   }
   const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);
+}
+
+int nvfp4_moe_route(const void *x, int64_t x_stride, int64_t tokens, const void *router, int router_dtype,
+                    int64_t router_stride, int64_t hidden, int experts, const float *bias, int scoring, int renormalize,
+                    float scale, int top_k, int32_t *ids, float *weights, cudaStream_t stream) {
+  if (tokens < 0 || tokens > INT32_MAX || hidden < 8 || hidden > INT32_MAX || hidden % 8 != 0 || experts < 1 ||
+      experts > kMaxExperts || top_k < 1 || top_k > std::min(kMaxTopK, experts))
+    return NVFP4_ERR_INVALID_ARG;
+  if ((router_dtype != NVFP4_DTYPE_BF16 && router_dtype != NVFP4_DTYPE_FP32) ||
+      (scoring != NVFP4_SCORE_SOFTMAX && scoring != NVFP4_SCORE_SIGMOID) || (renormalize != 0 && renormalize != 1) ||
+      !(scale - scale == 0.0f) || (bias && scoring != NVFP4_SCORE_SIGMOID))
+    return NVFP4_ERR_INVALID_ARG;
+  auto bad_stride = [&](int64_t s, int64_t n) { return s < hidden || s >= kMaxElems || (n > 0 && s > INT64_MAX / 8 / n); };
+  if (bad_stride(x_stride, tokens) || bad_stride(router_stride, experts)) return NVFP4_ERR_INVALID_ARG;
+  if (tokens > 0 && (!x || !router || !ids || !weights)) return NVFP4_ERR_INVALID_ARG;
+  const bool fp32 = router_dtype == NVFP4_DTYPE_FP32;
+  if (!aligned(x, 16) || x_stride % 8 != 0 || !aligned(router, 16) || router_stride % (fp32 ? 4 : 8) != 0 ||
+      !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return NVFP4_ERR_MISALIGNED;
+  DevInfo *d = nullptr;
+  const int st = device_info(&d);
+  if (st != NVFP4_OK) return st;
+  if (tokens == 0) return NVFP4_OK;
+  const RouteArgs a = {x, x_stride, tokens, router, fp32, router_stride, hidden, experts, top_k, bias,
+                       scoring == NVFP4_SCORE_SIGMOID, renormalize != 0, scale, ids, weights};
+  TraceScope tr(kTrMoeRoute, stream);
+  return map_cuda(launch_route(a, d->sms, stream));
 }
 
 int64_t nvfp4_moe_workspace_bytes(const nvfp4_experts *experts, int64_t tokens, int top_k) {

@@ -44,7 +44,8 @@
 
 namespace nvfp4 {
 
-constexpr int kMoeDepth = 2, kMoeDeep = 5;  // units of 256 columns in flight per warp
+constexpr int kMoeDepth = 2;            // units of 256 columns in flight per warp (3: 650 -> 764 us on the
+                                        // largest case, the rows' lines come less often from an open DRAM page)
 constexpr int kMoeMaxWarps = 16;        // of a CTA
 constexpr int kMoeSmem = 226 * 1024;    // dynamic shared memory of a CTA that has an SM to itself
 constexpr int kMoeHalfSmem = 112 * 1024;  // of one of two
@@ -59,9 +60,9 @@ struct MoeLaunch {
   int pairs;          // tokens * top_k
   int group;          // pairs of a job at most
   int steps;          // of 256 columns
-  int depth;          // units in flight per warp: kMoeDepth or kMoeDeep
   int tiles;          // of a job
-  int job_cost;       // of a job of four besides its tiles
+  int job_cost;       // of a job besides its tiles: its vectors' way, mostly (3.5 us of 32 at 61 tokens)
+  int more_cost;      // of a tile for each further n-tile, in eighths of a tile's
   int64_t cols;       // of this launch's matrices
 };
 
@@ -81,22 +82,21 @@ __host__ __device__ constexpr int moe_slot(bool wide) { return wide ? 2304 : 256
 __host__ __device__ constexpr int moe_up_pitch(int64_t cols) { return (int)((cols / 8 + 15) / 16 * 16); }
 // Shared memory: the vectors (with h's exponents), the warps' units in flight
 // and partial sums, the vectors' scales, the plan.
-__host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, int depth, bool wide, int experts, int pairs) {
+__host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, bool wide, int experts, int pairs) {
   return (cols + 255) / 256 * 512 * group + (down ? (int64_t)group * moe_up_pitch(cols) : 0) +
-         (int64_t)warps * (depth * moe_slot(wide) + (group + 7) / 8 * 512) + 512 +
+         (int64_t)warps * (kMoeDepth * moe_slot(wide) + (group + 7) / 8 * 512) + 512 +
          (pairs > kMoeFewPairs ? (int64_t)experts * 8 : 0) + ((int64_t)pairs + 1) * 14 + 64;
 }
 
 // A job: an expert's pairs order[at .. at + n).
 __device__ __forceinline__ uint32_t moe_job(int expert, int at, int n) { return (uint32_t)expert << 17 | (uint32_t)at << 6 | (uint32_t)n; }
 static_assert(kMaxExperts <= 1024 && kMoeSlicePairs <= 2048, "a job's fields");
-// A tile's cost: its weights' way, and three eighths of that for each further n-tile of
-// pairs (61 tokens 2048 x 768, 8 of 128: a tile of 9 .. 16 pairs took 1.44 times one of
-// up to 8; 256 tokens 2064 x 1424, 6 of 60: 1.2, and 1.4 with a third n-tile).
-__device__ __forceinline__ int moe_tile_cost(int pairs) { return 8 + 3 * ((pairs - 1) / 8); }
-// And a job's besides its tiles: mostly its vectors' way into shared memory.
-__device__ __forceinline__ int moe_begin_cost(const MoeLaunch &p, int pairs) { return p.job_cost * (4 + pairs) / 8; }
-__device__ __forceinline__ int moe_job_cost(const MoeLaunch &p, int pairs) { return moe_begin_cost(p, pairs) + p.tiles * moe_tile_cost(pairs); }
+// A tile's cost: its weights' way, and a part of that for each further n-tile of pairs.
+// Measured: 61 tokens 2048 x 768, 8 of 128 (wide copies): a tile of 9 .. 16 pairs took
+// 1.44 times one of up to 8; 256 tokens 2064 x 1424, 6 of 60 (narrow ones): 1.2, and
+// 1.4 with a third n-tile.
+__device__ __forceinline__ int moe_tile_cost(const MoeLaunch &p, int pairs) { return 8 + p.more_cost * ((pairs - 1) / 8); }
+__device__ __forceinline__ int moe_job_cost(const MoeLaunch &p, int pairs) { return p.job_cost + p.tiles * moe_tile_cost(p, pairs); }
 
 // The plan: the pairs that have an expert by expert, ascending, so that every
 // CTA cuts an expert's into the same jobs; the jobs, and the cost of those
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   constexpr int kSlot = moe_slot(WIDE);
   uint4 *xs = dsm;                                                        // [nk][8][N][4] 16-byte units of f16
   uint4 *slots = dsm + (size_t)nk * 32 * N;                               // [warps][depth][kSlot / 16]: units in flight
-  float4 *own = reinterpret_cast<float4 *>(slots + warps * p.depth * (kSlot / 16));  // [warps][NB][32]
-  slots += warp * p.depth * (kSlot / 16);
+  float4 *own = reinterpret_cast<float4 *>(slots + warps * kMoeDepth * (kSlot / 16));  // [warps][NB][32]
+  slots += warp * kMoeDepth * (kSlot / 16);
   int8_t *ups = reinterpret_cast<int8_t *>(own + warps * NB * 32);        // [N][up_pitch]
   float *xdown = reinterpret_cast<float *>(ups + (DOWN ? N * p.up_pitch : 0));  // [2][32]: the vectors' scales, undone
   int *xtop = reinterpret_cast<int *>(xdown + 64);                        // [2][32]: their largest entries' bits, or their scales' exponents
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
     }
     *job = lo;
     const int n = lo < total ? (int)(o.jobs[lo] & 63u) : 1;
-    *tile = lo < total ? max(at - o.start[lo] - moe_begin_cost(p, n), 0) / moe_tile_cost(n) : 0;
+    *tile = lo < total ? max(at - o.start[lo] - p.job_cost, 0) / moe_tile_cost(p, n) : 0;
   };
   int j0, t0, j1, t1;
   place(blockIdx.x, &j0, &t0);
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       next.k = last ? 0 : next.k + 1;
       next.at += last ? wrap : 16;
     }
-    fill = fill == (p.depth - 1) * kSlot ? 0 : fill + kSlot;
+    fill = fill == (kMoeDepth - 1) * kSlot ? 0 : fill + kSlot;
     asm volatile("cp.async.commit_group;" ::: "memory");  // (one per unit, empty after the last, for the waits to count)
   };
   // A job's vectors into shared memory, 8 columns (a unit) at a time: copies of
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   // (x before the weights, which take longer; h is not there yet)
   if constexpr (!DOWN) take_in(o.jobs[j0]);
 #pragma unroll 1
-  for (int i = 0; i < p.depth; ++i) fetch();
+  for (int i = 0; i < kMoeDepth; ++i) fetch();
   if constexpr (DOWN) {
     pdl_wait();
     pdl_launch_dependents();
@@ -398,8 +398,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       take_in(o.jobs[j]);
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-      if (p.depth == kMoeDepth) asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth) : "memory");
-      else asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDeep) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth) : "memory");
     }
     if constexpr (DOWN) {
       __syncthreads();
@@ -517,11 +516,10 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       }
       const int chunk0 = g * 8 + ((2 * cq) ^ g), chunk1 = g * 8 + ((2 * cq + 1) ^ g);
       for (int left = r.u1 - r.u0; left > 0; --left) {
-        if (p.depth == kMoeDepth) asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth - 1) : "memory");
-        else asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDeep - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth - 1) : "memory");
         __syncwarp();
         const uint4 *here = slots + take;
-        take = take == (p.depth - 1) * (kSlot / 16) ? 0 : take + kSlot / 16;
+        take = take == (kMoeDepth - 1) * (kSlot / 16) ? 0 : take + kSlot / 16;
         uint32_t sc[2][2][2];  // [half][row][block]: f16 pairs {Delta, Delta}
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -648,9 +646,9 @@ __global__ void __launch_bounds__(256) k_moe_join(const __grid_constant__ MoeLau
 namespace {
 
 // Pairs of a job at most, of those wanted, for the vectors' room in shared memory.
-int moe_group(int wanted, int64_t cols, bool down, int warps, int depth, bool wide, int experts, int pairs, int64_t room) {
+int moe_group(int wanted, int64_t cols, bool down, int warps, bool wide, int experts, int pairs, int64_t room) {
   for (int n = wanted; n > 0; --n)
-    if (moe_smem(n, cols, down, warps, depth, wide, experts, pairs) <= room) return n;
+    if (moe_smem(n, cols, down, warps, wide, experts, pairs) <= room) return n;
   return 0;
 }
 
@@ -693,17 +691,14 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
   const bool wide = p.cols % 64 == 0 && (down ? wide_matrix(a.down) : wide_matrix(a.up) && (!a.gated || wide_matrix(a.gate)));
   // Pairs that a job should take: few experts have more than three times the mean and four.
   const int wanted = std::min({p.pairs, 32, 4 + 3 * p.pairs / a.experts});
-  // Little work: one small CTA per SM, so that the next launch's CTAs find room beside it.
   p.job_cost = std::min(576 / p.steps, p.tiles);
+  p.more_cost = wide ? 3 : 2;
+  // Little work: one small CTA per SM, so that the next launch's CTAs find room beside
+  // it (1 token 2048 x 768, 8 of 128: 22.1 -> 20.6 us).
   const bool little = (int64_t)std::min(p.pairs, a.experts) * p.tiles * p.steps <= (int64_t)64 * sms;
   int warps = 8, ctas = little ? sms : 2 * sms;
-  auto fit = [&](int64_t room) { p.group = moe_group(wanted, p.cols, down, warps, p.depth, wide, a.experts, p.pairs, room); };
-  p.depth = kMoeDeep;
-  if (little) fit(kMoeHalfSmem);
-  if (!little || p.group < wanted) {
-    p.depth = kMoeDepth;
-    fit(kMoeHalfSmem);
-  }
+  auto fit = [&](int64_t room) { p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, room); };
+  fit(kMoeHalfSmem);
   if (p.group < wanted) {
     warps = kMoeMaxWarps, ctas = sms;
     fit(kMoeSmem);
@@ -712,7 +707,7 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
     warps = 8;
     fit(kMoeSmem);
   }
-  const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, p.depth, wide, a.experts, p.pairs);
+  const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, wide, a.experts, p.pairs);
   return with_kernel(p.group <= 8 ? 1 : 4, down, a.gated, wide,
                      [&](auto *k) { return launch_dependent(k, ctas, warps * 32, smem, p, st); });
 }
@@ -723,8 +718,8 @@ size_t moe_up_bytes(int64_t inner, int pairs) { return ((size_t)pairs * moe_up_p
 }  // namespace
 
 bool moe_fits(int64_t hidden, int64_t inner, int experts, int pairs) {
-  return moe_group(1, hidden, false, 8, kMoeDepth, false, experts, pairs, kMoeSmem) > 0 &&
-         moe_group(1, inner, true, 8, kMoeDepth, false, experts, pairs, kMoeSmem) > 0;
+  return moe_group(1, hidden, false, 8, false, experts, pairs, kMoeSmem) > 0 &&
+         moe_group(1, inner, true, 8, false, experts, pairs, kMoeSmem) > 0;
 }
 
 size_t moe_workspace_bytes(int64_t hidden, int64_t inner, int pairs) {

@@ -1,0 +1,98 @@
+"""The router against its formulas in 64 bits: the experts and their order have
+to be equal, the weights within fp32's roundings."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scale_gb300 as nv
+
+pytestmark = pytest.mark.gpu
+
+
+def _want(x, router, k, scoring, renormalize, bias, scale):
+    logit = x.double().numpy() @ router.double().numpy().T
+    if scoring == "sigmoid":
+        p = 1.0 / (1.0 + np.exp(-logit))
+        score = p + (0.0 if bias is None else bias.double().numpy())
+    else:
+        e = np.exp(logit - logit.max(1, keepdims=True))
+        p, score = e / e.sum(1, keepdims=True), logit
+    ids = np.argsort(-score, axis=1, kind="stable")[:, :k]
+    w = np.take_along_axis(p, ids, 1)
+    if renormalize:
+        w = w / w.sum(1, keepdims=True)
+    return ids, w * scale
+
+
+def _check(x, router, k, scoring="softmax", renormalize=True, bias=None, scale=1.0):
+    ids, w = nv.moe_route(x.cuda(), router.cuda(), k, scoring, renormalize, None if bias is None else bias.cuda(), scale)
+    torch.cuda.synchronize()
+    wi, ww = _want(x, router, k, scoring, renormalize, bias, scale)
+    assert np.array_equal(ids.cpu().numpy(), wi)
+    # an exponential good to 2 ulp of an argument off by 2^-24 of up to 40, a sum of up to 1024 of them in any order
+    # (each lane's at most 64 roundings deep), a quotient and a product
+    err = np.abs(w.double().cpu().numpy() - ww)
+    assert np.all(err <= (2 * (2 ** -22 + 40 * 2.0 ** -24) + 64 * 2.0 ** -24 + 2 ** -23) * np.abs(ww) + 1e-44)
+    return ids, w
+
+
+# tokens, hidden, experts, k: one of everything; fewer experts than CTAs of a cluster; tokens that no cluster divides;
+# more experts than threads; every expert chosen; columns that no lane divides
+SHAPES = [(1, 8, 1, 1), (1, 2048, 128, 8), (3, 264, 5, 5), (61, 512, 8, 2), (130, 72, 60, 6), (700, 40, 33, 3),
+          (2, 136, 1024, 32), (9, 7168, 256, 8), (1, 1000, 3, 1)]
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scoring,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_choice_and_weights(shape, scoring, renormalize, kind):
+    tokens, hidden, experts, k = shape
+    g = torch.Generator().manual_seed(sum(shape))
+    x = torch.randn((tokens, hidden), generator=g).to(torch.bfloat16)
+    r = (1.5 * hidden ** -0.5 * torch.randn((experts, hidden), generator=g)).to(kind)
+    bias = 0.2 * torch.randn(experts, generator=g) if scoring == "sigmoid" else None
+    _check(x, r, k, scoring, renormalize, bias, 2.5 if scoring == "sigmoid" else 1.0)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_scores_closer_than_fp32_tells_apart(kind):
+    """Every logit is 2^14 (eleven 1024s and so on, large and cancelling ones
+    among them) plus a multiple of 2^-12, which fp32 would drop."""
+    g = torch.Generator().manual_seed(3)
+    experts, hidden = 64, 512
+    small = torch.randperm(experts, generator=g).double()
+    r = torch.zeros((experts, hidden), dtype=torch.float64)
+    r[:, 0::2] = 64.0 * torch.randint(1, 200, (experts, hidden // 2), generator=g)
+    r[:, 1::2] = -r[:, 0::2]
+    r = r[:, torch.randperm(hidden, generator=g)]
+    x = torch.ones((5, hidden))
+    r[:, 7], r[:, 300], r[:, 5] = 16384.0, small * 2.0 ** -12, 0.0
+    r[:, 5] = 16384.0 - r.sum(1) + small * 2.0 ** -12  # what the pairs that were overwritten left over
+    r = r.to(kind)
+    exact = r.double().sum(1)
+    ids, _ = nv.moe_route(x.to(torch.bfloat16).cuda(), r.cuda(), 32, "softmax", True)
+    order = sorted(range(experts), key=lambda e: (-exact[e].item(), e))[:32]
+    assert exact.unique().numel() > 32 and ids.cpu().tolist() == [order] * 5
+
+
+def test_equal_scores_go_to_the_lower_expert():
+    x = torch.randn((4, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    row = torch.randn((1, 64), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    ids, w = _check(x, row.expand(300, 64).contiguous(), 7)
+    assert ids.cpu().tolist() == [list(range(7))] * 4 and torch.allclose(w, torch.full_like(w, 1 / 7))
+    _check(x, torch.zeros((9, 64)), 9, "sigmoid", False, torch.tensor([0.0, -0.0, 1, 1, 0, -1, 2, 2, 0]))
+
+
+def test_strides_streams_and_repeats():
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn((20, 304), generator=g).to(torch.bfloat16).cuda()[:, :160]
+    r = torch.randn((16, 168), generator=g).cuda()[:, :160]
+    a = nv.moe_route(x, r, 4)
+    b = nv.moe_route(x.contiguous(), r.contiguous(), 4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c = nv.moe_route(x, r, 4, stream=s)
+    torch.cuda.synchronize()
+    for p, q in zip(a + a, b + c):
+        assert torch.equal(p, q)
+    assert nv.moe_route(x[:0], r, 4)[0].shape == (0, 4)
