@@ -207,7 +207,7 @@ def fp32_peak_derived(sms: int, mhz: float) -> float:
 
 # sources that take no part in any recorded call: the decode-step operators
 OTHER_SOURCES = {"nvfp4_attention.cu", "nvfp4_epilogue.cuh", "nvfp4_kv.cu", "nvfp4_linear.cu", "nvfp4_linear_tc.cu",
-                 "nvfp4_moe.cu", "nvfp4_route.cu"}
+                 "nvfp4_moe.cu", "nvfp4_route.cu", "nvfp4_sample.cu"}
 
 
 def source_digest() -> str:

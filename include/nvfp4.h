@@ -464,6 +464,50 @@ int nvfp4_moe(const nvfp4_experts *experts, const void *x, int64_t x_stride, int
               int64_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * nvfp4_sample -- the next token of each row of logits, by a given random number.
+ *   With m = max l and w_i = exp((l_i - m) / temperature), and the row's unmasked
+ *   tokens in descending order of l (equal ones: the lower index first):
+ *     top-k   the first top_k of them stay (top_k <= 0: all);
+ *     top-p   of those a token stays while the w before it sum to less than top_p
+ *             times the sum of all of those (top_p >= 1 or NaN: all; the first
+ *             stays whatever top_p);
+ *     min-p   a token stays if w_i >= min_p (min_p <= 0 or NaN: all; the largest
+ *             stay whatever min_p).
+ *   token is the least i whose w, with those of the tokens that stay below it,
+ *   sums to more than uniform times the sum of all that stay; logprob is
+ *   ln(w_token / that sum).  temperature <= 0 or NaN: token is the largest (the
+ *   lowest index of equal ones), logprob 0.  Logits of -inf and NaN are masked:
+ *   they are never chosen; a row without others gives token -1, logprob -inf.
+ *   Infinite logits share their row evenly.
+ *   Weights are whole numbers of 2^-42, off by at most 2^-30 of themselves or one
+ *   unit, their sums and every comparison of sums exact, so results repeat bit for bit.
+ * Arguments:
+ *   logits  device, bf16 or fp32 (dtype), aligned to its type, [rows][vocabulary],
+ *           rows stride elements apart (>= vocabulary).
+ *   rows    0 .. 2^27.  vocabulary 0 .. 2^20.
+ *   sampling  host struct (read during the call only): for each parameter a
+ *           device array [rows], or NULL and one value for all rows.  NULL:
+ *           temperature 1, everything stays.
+ *   uniform device, fp32, [rows], in [0, 1) (below, or NaN: 0; above: 1 - 2^-24).
+ *   token   device, int32, [rows] (written).
+ *   logprob device, fp32, [rows] (written), or NULL.
+ * Returns an nvfp4_status.
+ */
+typedef struct nvfp4_sampling {
+  const float *temperature;
+  const int32_t *top_k;
+  const float *top_p;
+  const float *min_p;
+  float temperature_all;
+  int top_k_all;
+  float top_p_all;
+  float min_p_all;
+} nvfp4_sampling;
+int nvfp4_sample(const void *logits, int dtype, int64_t stride, int64_t rows, int64_t vocabulary,
+                 const nvfp4_sampling *sampling, const float *uniform, int32_t *token, float *logprob,
+                 cudaStream_t stream);
+
+/*
  * nvfp4_swizzle_scales -- the E4M3 block scales of a quantized [rows, cols]
  *   tensor, from the linear [rows, cols/16] layout that nvfp4_quantize
  *   writes to the layout block-scaled tensor-core matrix multiplies read

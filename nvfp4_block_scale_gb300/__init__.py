@@ -60,6 +60,13 @@ class nvfp4_experts(ctypes.Structure):
                 ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64), ("experts", ctypes.c_int)]
 
 
+class nvfp4_sampling(ctypes.Structure):
+    """The parameters of nvfp4_sample (include/nvfp4.h)."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
+
+
 class nvfp4_tensor(ctypes.Structure):
     """One descriptor of nvfp4_quantize_grouped (include/nvfp4.h)."""
     _fields_ = [("W", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
@@ -115,6 +122,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_moe_workspace_bytes.restype = i64
     L.nvfp4_moe.argtypes = [ctypes.POINTER(nvfp4_experts), vp, i64, i64, ci, vp, vp, ci, vp, i64, vp, i64, vp, i64, vp]
     L.nvfp4_moe.restype = ci
+    L.nvfp4_sample.argtypes = [vp, ci, i64, i64, i64, ctypes.POINTER(nvfp4_sampling), vp, vp, vp, vp]
+    L.nvfp4_sample.restype = ci
     L.nvfp4_swizzled_scales_bytes.argtypes = [i64, i64]
     L.nvfp4_swizzled_scales_bytes.restype = i64
     L.nvfp4_swizzle_scales.argtypes = [vp, i64, i64, vp, vp]
@@ -231,6 +240,11 @@ def nvfp4_moe(experts, x, x_stride, tokens, top_k, ids, weights, activation, res
               workspace, workspace_bytes, stream) -> int:
     return load().nvfp4_moe(experts, x, x_stride, tokens, top_k, ids, weights, activation, residual, residual_stride, y,
                             y_stride, workspace, workspace_bytes, stream)
+
+
+def nvfp4_sample(logits, dtype, stride, rows, vocabulary, sampling, uniform, token, logprob, stream) -> int:
+    """`sampling`: an nvfp4_sampling (passed by reference) or None."""
+    return load().nvfp4_sample(logits, dtype, stride, rows, vocabulary, sampling, uniform, token, logprob, stream)
 
 
 def nvfp4_swizzled_scales_bytes(rows, cols) -> int:
@@ -817,6 +831,49 @@ def moe(experts: Experts, x, ids, weights, activation="silu", residual=None, out
                                       ACTIVATIONS[activation], rp, rs, yp, ys, wp, wb, _on(experts.device, stream)),
            "nvfp4_moe")
     return out
+
+
+def _setting(v, off, rows: int, kind, device, what: str):
+    """A sampling parameter: the address of a tensor [rows], or nothing and one value."""
+    import torch
+    if isinstance(v, torch.Tensor):
+        if v.dtype is not kind or v.shape != (rows,) or v.device != device or not v.is_contiguous():
+            raise ValueError(f"{what} must be a number or a contiguous {kind} tensor [{rows}] on the logits' device")
+        return v.data_ptr(), off
+    return None, off if v is None else v
+
+
+def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, return_logprob: bool = False,
+           stream=None):
+    """The next token of each row of logits (bf16 or fp32 [rows, vocabulary], rows
+    may lie further apart than their width): int32 [rows], with return_logprob
+    also the fp32 logarithm of its probability among the tokens that stay.
+    uniform: fp32 [rows] random numbers in [0, 1).  temperature (1), top_k (all),
+    top_p (1), min_p (0): a number, a tensor [rows] (fp32; top_k int32) or None.
+    temperature 0 takes the largest; logits of -inf are masked, and a row of
+    them gives -1.  See nvfp4_sample in include/nvfp4.h."""
+    import torch
+    kind = logits.dtype
+    if (kind is not torch.bfloat16 and kind is not torch.float32) or not logits.is_cuda or logits.dim() != 2 or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a bf16 or fp32 CUDA tensor [rows, vocabulary] with contiguous rows")
+    rows, vocabulary = logits.shape
+    device = logits.device
+    if uniform.dtype is not torch.float32 or uniform.shape != (rows,) or uniform.device != device or \
+            not uniform.is_contiguous():
+        raise ValueError(f"uniform must be a contiguous fp32 tensor [{rows}] on the logits' device")
+    tp, t = _setting(temperature, 1.0, rows, torch.float32, device, "temperature")
+    kp, k = _setting(top_k, 0, rows, torch.int32, device, "top_k")
+    pp, p = _setting(top_p, 1.0, rows, torch.float32, device, "top_p")
+    mp, m = _setting(min_p, 0.0, rows, torch.float32, device, "min_p")
+    token = _empty((rows,), torch.int32, device, stream)
+    logprob = _empty((rows,), torch.float32, device, stream) if return_logprob else None
+    _check((_lib or load()).nvfp4_sample(
+        logits.data_ptr(), DTYPE_FP32 if kind is torch.float32 else DTYPE_BF16,
+        logits.stride(0) if rows > 1 else vocabulary, rows, vocabulary, nvfp4_sampling(tp, kp, pp, mp, t, k, p, m),
+        uniform.data_ptr(), token.data_ptr(), None if logprob is None else logprob.data_ptr(), _on(device, stream)),
+        "nvfp4_sample")
+    return (token, logprob) if return_logprob else token
 
 
 def swizzle_scales(scales, rows: int, cols: int, stream=None):

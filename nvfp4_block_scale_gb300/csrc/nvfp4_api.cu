@@ -119,6 +119,7 @@ int device_info(DevInfo **out) {
       if (e == cudaSuccess) e = prepare_linear_tc_kernels();
       if (e == cudaSuccess) e = prepare_attention_kernels();
       if (e == cudaSuccess) e = prepare_moe_kernels();
+      if (e == cudaSuccess) e = prepare_sample_kernels();
       if (e != cudaSuccess) return map_cuda(e);
       cudaMemPoolProps props = {};
       props.allocType = cudaMemAllocationTypePinned;
@@ -278,7 +279,7 @@ int take_workspace(void **ws, void **own, int64_t given, size_t need, const DevI
 enum { kTrAmax = 0, kTrQuantMax, kTrQuantFos, kTrCjsoInit, kTrCjsoIter, kTrDecoupled, kTrDequant, kTrEncode,
        kTrGroupAmax, kTrGroupQuantMax, kTrGroupQuantFos, kTrGemv, kTrSwizzle, kTrAmaxLdg, kTrGemmTc,
        kTrGemmTcReduce, kTrLinear, kTrLinearTcF16, kTrLinearTcBf16, kTrKvAppend, kTrAttend, kTrMoeRoute,
-       kTrMoe, kTrKinds };
+       kTrMoe, kTrSample, kTrKinds };
 const char *const kTraceNames[kTrKinds] = {"k_amax_bulk",        "k_quant_max_fos<max>", "k_quant_max_fos<fos>",
                                            "k_cjso_sweep<init>",  "k_cjso_sweep<iter>",   "k_decoupled",
                                            "k_dequant",           "k_encode",             "k_group_amax",
@@ -286,7 +287,7 @@ const char *const kTraceNames[kTrKinds] = {"k_amax_bulk",        "k_quant_max_fo
                                            "k_swizzle_scales",   "k_amax_partials",      "k_gemm_tc",
                                            "k_gemm_tc_reduce",   "k_linear",             "k_linear_tc<f16>",
                                            "k_linear_tc<bf16>",  "k_kv_append",          "k_attend",
-                                           "k_moe_route",         "k_moe"};
+                                           "k_moe_route",         "k_moe",                "k_sample"};
 
 struct TraceRec {
   int kind;
@@ -841,6 +842,30 @@ int nvfp4_moe(const nvfp4_experts *experts, const void *x, int64_t x_stride, int
   }
   const cudaError_t ef = own ? cudaFreeAsync(own, stream) : cudaSuccess;
   return map_cuda(e != cudaSuccess ? e : ef);
+}
+
+int nvfp4_sample(const void *logits, int dtype, int64_t stride, int64_t rows, int64_t vocabulary,
+                 const nvfp4_sampling *sampling, const float *uniform, int32_t *token, float *logprob, cudaStream_t stream) {
+  if ((dtype != NVFP4_DTYPE_BF16 && dtype != NVFP4_DTYPE_FP32) || rows < 0 || rows > (int64_t(1) << 27) ||
+      vocabulary < 0 || vocabulary > kMaxVocabulary || stride < vocabulary || stride >= kMaxElems)
+    return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0 && ((vocabulary > 0 && !logits) || !uniform || !token)) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_sampling s = {};
+  s.temperature_all = s.top_p_all = 1.0f;
+  if (sampling) s = *sampling;
+  if (!aligned(logits, dtype == NVFP4_DTYPE_FP32 ? 4 : 2) || !aligned(uniform, 4) || !aligned(token, 4) ||
+      !aligned(logprob, 4) || !aligned(s.temperature, 4) || !aligned(s.top_k, 4) || !aligned(s.top_p, 4) ||
+      !aligned(s.min_p, 4))
+    return NVFP4_ERR_MISALIGNED;
+  DevInfo *d = nullptr;
+  const int st = device_info(&d);
+  if (st != NVFP4_OK) return st;
+  if (rows == 0) return NVFP4_OK;
+  const SampleArgs a = {logits, dtype == NVFP4_DTYPE_FP32, stride, (int)rows, (int)vocabulary, s.temperature, s.top_p,
+                        s.min_p, s.top_k, s.temperature_all, s.top_p_all, s.min_p_all, s.top_k_all, uniform, token,
+                        logprob};
+  TraceScope tr(kTrSample, stream);
+  return map_cuda(launch_sample(a, d->sms, stream));
 }
 
 int64_t nvfp4_swizzled_scales_bytes(int64_t rows, int64_t cols) {

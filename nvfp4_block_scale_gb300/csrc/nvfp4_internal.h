@@ -138,6 +138,7 @@ struct MoeMatrix {
 };
 constexpr int kMoeSlicePairs = 2048, kMoeSliceTokens = 256;  // (token, slot) pairs and tokens of one launch at most
 constexpr int kMaxExperts = 1024, kMaxTopK = 32;
+constexpr int kMaxVocabulary = 1 << 20;
 struct MoeArgs {
   MoeMatrix gate, up, down;
   bool gated;
