@@ -38,9 +38,10 @@ namespace nvfp4 {
 namespace cg = cooperative_groups;
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
-constexpr int kSampleMaxCtas = 8;
+constexpr int kSampleMaxCtas = 16;  // of a cluster (8 where a device cannot place more)
 constexpr int kBins = 2048;
-constexpr int kList = 512;        // tokens that one CTA ranks
+constexpr int kList = kSampleThreads;  // tokens that one CTA ranks, one per thread
+constexpr int kShortK = 256;           // top-k up to which one CTA finishes the row
 constexpr int kOneBits = 42;      // a weight of 1
 constexpr int kSampleSmem = 226 * 1024;
 static_assert(kMaxVocabulary <= 1 << 20, "a sum of weights stays below 2^63, a bin's high words below 2^32");
@@ -103,6 +104,10 @@ struct alignas(16) SampleShared {
   uint64_t total_mass[2][kSampleMaxCtas];  // of the slices of a histogram, by CTA
   uint32_t total_count[2][kSampleMaxCtas];
   uint32_t listed;
+  // of the row, by one thread (fp64 is slow): log2(e) / temperature in two parts, the
+  // least weight that stays, and how far below the largest logit it lies at most
+  float unit_hi, unit_lo, reach;
+  uint64_t least;
 };
 struct SampleList {  // over the histogram
   uint64_t key[kList], mass[kList];
@@ -113,7 +118,9 @@ __host__ __device__ constexpr int64_t sample_slices(int ctas) { return 2 * (int6
 
 constexpr uint64_t kNoCut = 0;  // keeps every token
 
-template <typename T>
+// CUTS: some row may have a top_k or top_p.  Without (known from the values for
+// all rows) the kernel is a third as long and needs no histogram.
+template <typename T, bool CUTS>
 __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_constant__ SampleLaunch p) {
   constexpr int kVec = 16 / sizeof(T);
   extern __shared__ __align__(16) uint8_t dsm[];
@@ -141,14 +148,27 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   };
   auto alive = [](float v) { return v > -INFINITY; };  // (not NaN either)
 
+  const float temperature = a.temperature ? a.temperature[row] : a.temperature_all;
+  if (tid == kSampleThreads - 1 && temperature > 0.0f) {
+    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all;
+    uint64_t least = 1;
+    if (min_p > 0.0f) least = min_p < 1.0f ? max(uint64_t{1}, share_of(uint64_t{1} << kOneBits, min_p, true)) : uint64_t{1} << kOneBits;
+    const double unit = fmin(1.4426950408889634 / (double)temperature, 1e38);
+    sh.unit_hi = (float)unit;
+    sh.unit_lo = (float)(unit - (double)(float)unit);
+    sh.least = least;
+    sh.reach = (float)((log2((double)least) - kOneBits - 0.01) / unit);  // (0.01: more than fp32 rounds)
+  }
+
   // ---- the row into shared memory; its largest
   for (int i = tid; i < 256; i += kSampleThreads) sh.pow2[i] = make_uint2(kPow2.q[i], __float_as_uint(kPow2.f[i]));
-  uint64_t top = 0;
-  auto put = [&](float v, int i) {
-    if (i < kept) vals[shift + i] = v;
-    if (alive(v)) top = max(top, key_of(v, i));
-  };
-  if (tid < head && tid < n) put(as_float(logits[tid]), tid);
+  float most = -INFINITY;  // of this thread, first seen at `where` or in the kVec from there
+  int where = -1;
+  if (tid < head && tid < n) {
+    const float v = as_float(logits[tid]);
+    if (tid < kept) vals[shift + tid] = v;
+    if (v > most) most = v, where = tid;
+  }
   const int whole = max(0, n - head) / kVec;
 #pragma unroll 4
   for (int v = tid; v < whole; v += kSampleThreads) {
@@ -169,14 +189,21 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       for (int i = 0; i < kVec; ++i)
         if (at + i < kept) vals[shift + at + i] = x[i];
     }
-    float best = x[0];
-    int where = 0;
+    float here = x[0];
 #pragma unroll
-    for (int i = 1; i < kVec; ++i)
-      if (x[i] > best || !(best == best)) best = x[i], where = i;  // (the first of equal ones; NaN gives way)
-    if (alive(best)) top = max(top, key_of(best, at + where));
+    for (int i = 1; i < kVec; ++i) here = fmaxf(here, x[i]);  // (NaN gives way)
+    if (here > most) most = here, where = at;
   }
-  for (int i = head + whole * kVec + tid; i < n; i += kSampleThreads) put(as_float(logits[i]), i);
+  for (int i = head + whole * kVec + tid; i < n; i += kSampleThreads) {
+    const float v = as_float(logits[i]);
+    if (i < kept) vals[shift + i] = v;
+    if (v > most) most = v, where = i;
+  }
+  uint64_t top = 0;
+  if (where >= 0) {
+    while (as_float(logits[where]) != most) ++where;
+    top = key_of(most, where);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
   if (lane == 0) sh.warp_sum[warp] = top;
@@ -198,7 +225,6 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   for (int r = 0; r < ctas; ++r) top = max(top, sh.box[turn][r][0]);
   const bool writes = rank == 0 && tid == 0;
   const int best = (int)~(uint32_t)top;
-  const float temperature = a.temperature ? a.temperature[row] : a.temperature_all;
   if (top == 0 || !(temperature > 0.0f)) {  // nothing unmasked; or the largest is asked for
     if (writes) {
       a.token[row] = top == 0 ? -1 : best;
@@ -210,8 +236,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   // ---- weights
   const uint32_t tb = (uint32_t)(top >> 32);
   const float m = __uint_as_float(tb >> 31 ? tb & 0x7FFFFFFFu : ~tb);
-  const double unit = fmin(1.4426950408889634 / (double)temperature, 1e38);  // log2(e) / T
-  const float ch = (float)unit, cl = (float)(unit - (double)ch);
+  const float ch = sh.unit_hi, cl = sh.unit_lo;
   const bool endless = m == INFINITY;  // then the infinite ones share the row
   // log2 of a weight, its larger part (in the order of the values: each operation keeps it)
   auto power = [&](float v) { return endless ? v == m ? 0.0f : -INFINITY : (v - m) * ch; };
@@ -237,24 +262,34 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   const int t0 = min(tid * p.run, n), t1 = min(t0 + p.run, n);  // this thread's tokens
 
   // ---- cuts
-  int top_k = a.top_k ? a.top_k[row] : a.top_k_all;
+  int top_k = CUTS ? a.top_k ? a.top_k[row] : a.top_k_all : 0;
   if (top_k < 0 || top_k >= a.vocabulary) top_k = 0;
-  const float top_p = a.top_p ? a.top_p[row] : a.top_p_all, min_p = a.min_p ? a.min_p[row] : a.min_p_all;
+  const float top_p = CUTS ? a.top_p ? a.top_p[row] : a.top_p_all : 1.0f;
   const bool by_mass = top_p < 1.0f;
   uint64_t cut = kNoCut;
 
   // A histogram's totals in this CTA's slice of it, and those of every slice.
-  auto add_slices = [&](int set) {
+  auto add_slices = [&](int set, bool masses) {
     cluster.sync();
     uint64_t ms = 0;
     uint32_t cs = 0;
     for (int i = tid; i < bins; i += kSampleThreads) {
       uint64_t mass = 0;
       uint32_t count = 0;
-      for (int r = 0; r < ctas; ++r) {
-        const uint32_t *h = cluster.map_shared_rank(&sh.hist[0][0], r) + rank * bins + i;
-        count += h[0];
-        mass += (uint64_t)h[kBins] + ((uint64_t)h[2 * kBins] << 32);
+#pragma unroll
+      for (int r0 = 0; r0 < kSampleMaxCtas; r0 += 8) {  // (eight CTAs' words on their way at once)
+        uint32_t w[8][3];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          w[r][0] = w[r][1] = w[r][2] = 0u;
+          if (r0 + r < ctas) {
+            const uint32_t *h = cluster.map_shared_rank(&sh.hist[0][0], r0 + r) + rank * bins + i;
+            w[r][0] = h[0];
+            if (masses) w[r][1] = h[kBins], w[r][2] = h[2 * kBins];
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) count += w[r][0], mass += (uint64_t)w[r][1] + ((uint64_t)w[r][2] << 32);
       }
       slice_mass[set * bins + i] = mass;
       slice_count[set * bins + i] = count;
@@ -341,8 +376,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     uint32_t inside;
     Totals b = find_bin(0, Totals{0, 0}, mass, goal, &bin, &inside);
     uint64_t high = ~0ull, low = 0;  // the range's keys, once it is one of keys
-    auto in_range = [&](float v, int i, uint64_t w) {
-      if (w == 0) return false;
+    auto in_range = [&](float v, int i) {  // (the last bin's weights are 0: no cut lies there)
+      if (!alive(v)) return false;
       if (low == 0) return bin_of(v) == bin;
       const uint64_t k = key_of(v, i);
       return k <= high && k >= low;
@@ -351,7 +386,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       uint64_t hk = 0, lk = ~0ull;  // the largest and smallest key inside
       for (int i = t0; i < t1; ++i) {
         const float v = get(i);
-        if (alive(v) && in_range(v, i, weight(v))) hk = max(hk, key_of(v, i)), lk = min(lk, key_of(v, i));
+        if (in_range(v, i)) hk = max(hk, key_of(v, i)), lk = min(lk, key_of(v, i));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) hk = max(hk, __shfl_xor_sync(~0u, hk, o)), lk = min(lk, __shfl_xor_sync(~0u, lk, o));
@@ -364,11 +399,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       const int width = 64 - __clzll((hk - lk) | 1), down = max(0, width - 11);  // (hk - lk) >> down < 2048
       for (int i = t0; i < t1; ++i) {
         const float v = get(i);
-        if (!alive(v)) continue;
-        const uint64_t w = weight(v);
-        if (in_range(v, i, w)) add((int)((hk - key_of(v, i)) >> down), w);
+        if (in_range(v, i)) add((int)((hk - key_of(v, i)) >> down), by_mass ? weight(v) : 0);
       }
-      add_slices(1);
+      add_slices(1, by_mass);
       int at;
       b = find_bin(1, b, mass, goal, &at, &inside);
       high = hk - ((uint64_t)at << down);  // (keys of finite values are above 2^54, a bin's width is at most 2^53)
@@ -381,11 +414,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     uint32_t *listed = cluster.map_shared_rank(&sh.listed, 0);
     for (int i = t0; i < t1; ++i) {
       const float v = get(i);
-      if (!alive(v)) continue;
-      const uint64_t w = weight(v);
-      if (!in_range(v, i, w)) continue;
+      if (!in_range(v, i)) continue;
       const uint32_t at = atomicAdd(listed, 1u);
-      if (at < kList) list->key[at] = key_of(v, i), list->mass[at] = w;  // (there are `inside` of them)
+      if (at < kList) list->key[at] = key_of(v, i), list->mass[at] = weight(v);  // (there are `inside` of them)
     }
     cluster.sync();
     if (rank == 0) {
@@ -407,14 +438,96 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     return Totals{sh.box[turn][0][1], (uint32_t)sh.box[turn][0][2]};
   };
 
-  if (by_mass || top_k > 0) {
+  const uint64_t least = sh.least;
+  float u = a.uniform[row];
+  u = u > 0.0f ? u < 1.0f ? u : 0.99999994f : 0.0f;  // (NaN: 0)
+  auto write = [&](int i, float v, uint64_t total) {
+    a.token[row] = i;
+    if (!a.logprob) return;
+    const double l = endless ? 0.0 : ((double)v - (double)m) / (double)temperature;
+    a.logprob[row] = (float)(l - log((double)total * (1.0 / (1ull << kOneBits))));
+  };
+
+  // ---- few tokens to choose from: a histogram of counts alone, and CTA 0 does the rest
+  if (CUTS && top_k > 0 && top_k <= kShortK) {
+    for (int i = tid; i < kBins; i += kSampleThreads) sh.hist[0][i] = 0u;
+    __syncthreads();
+    for (int i = t0; i < t1; ++i) {
+      const float v = get(i);
+      if (!alive(v)) continue;
+      const int bin = bin_of(v);
+      if (bin < kBins - 1) atomicAdd(&sh.hist[0][bin], 1u);  // (the last bin's weights are 0)
+    }
+    add_slices(0, false);
+    uint32_t count = 0;
+    for (int r = 0; r < ctas; ++r) count += sh.total_count[0][r];
+    int last = kBins - 2;
+    if (count > (uint32_t)top_k) {
+      uint32_t inside;
+      count = find_bin(0, Totals{0, 0}, false, (uint64_t)top_k, &last, &inside).count + inside;
+    }
+    if (count <= kList) {
+      if (rank == 0 && tid == 0) sh.listed = 0;
+      cluster.sync();
+      SampleList *list = reinterpret_cast<SampleList *>(cluster.map_shared_rank(&sh.hist[0][0], 0));
+      uint32_t *listed = cluster.map_shared_rank(&sh.listed, 0);
+      for (int i = t0; i < t1; ++i) {
+        const float v = get(i);
+        if (!alive(v) || bin_of(v) > last) continue;
+        const uint32_t at = atomicAdd(listed, 1u);
+        if (at < kList) list->key[at] = key_of(v, i), list->mass[at] = weight(v);  // (there are `count` of them)
+      }
+      cluster.sync();
+      if (rank > 0) return;
+      SampleList &l = *reinterpret_cast<SampleList *>(&sh.hist[0][0]);
+      auto block_sum = [&](uint64_t v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        __syncthreads();
+        if (lane == 0) sh.warp_sum[warp] = v;
+        __syncthreads();
+        v = 0;
+        for (int w = 0; w < kSampleWarps; ++w) v += sh.warp_sum[w];
+        return v;
+      };
+      const bool there = tid < (int)count;
+      const uint64_t key = there ? l.key[tid] : 0, mass = there ? l.mass[tid] : 0;
+      Totals ahead = {0, 0};
+      if (there)
+        for (int j = 0; j < (int)count; ++j)
+          if (l.key[j] > key) ahead.mass += l.mass[j], ++ahead.count;
+      uint64_t w = there && ahead.count < (uint32_t)top_k ? mass : 0;
+      if (by_mass) {  // (the largest token stays whatever top_p)
+        const uint64_t goal = max(uint64_t{1}, share_of(block_sum(w), top_p > 0.0f ? top_p : 0.0f, true));
+        if (ahead.mass >= goal) w = 0;
+      }
+      if (w < least) w = 0;
+      const uint64_t total = block_sum(w), goal = share_of(total, u, false);  // (its barriers: every key and mass has been read)
+      if (there) l.mass[tid] = w;
+      __syncthreads();
+      if (w) {
+        const uint32_t mine = (uint32_t)key;  // smaller indices have larger ones
+        uint64_t before = 0;
+        for (int j = 0; j < (int)count; ++j)
+          if ((uint32_t)l.key[j] > mine) before += l.mass[j];
+        if (before <= goal && before + w > goal) {
+          const uint32_t vb = (uint32_t)(key >> 32);
+          write((int)~mine, __uint_as_float(vb >> 31 ? vb & 0x7FFFFFFFu : ~vb), total);
+        }
+      }
+      return;
+    }
+  }
+
+  if (CUTS && (by_mass || top_k > 0)) {
     clear();
     for (int i = t0; i < t1; ++i) {
       const float v = get(i);
-      const uint64_t w = weight(v);
-      if (w) add(bin_of(v), w);
+      if (!alive(v)) continue;
+      const int bin = bin_of(v);
+      if (bin < kBins - 1) add(bin, by_mass ? weight(v) : 0);
     }
-    add_slices(0);
+    add_slices(0, by_mass);
     Totals whole_row = {0, 0};
     for (int r = 0; r < ctas; ++r) whole_row.mass += sh.total_mass[0][r], whole_row.count += sh.total_count[0][r];
     if (top_k > 0 && whole_row.count > (uint32_t)top_k) whole_row = find(false, (uint64_t)top_k, &cut);
@@ -425,14 +538,21 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   }
 
   // ---- the kept weights' sum, and the token
-  uint64_t least = 1;  // weight that stays
-  if (min_p > 0.0f) least = min_p < 1.0f ? max(uint64_t{1}, share_of(uint64_t{1} << kOneBits, min_p, true)) : uint64_t{1} << kOneBits;
+  // a value below which nothing stays: most tokens need no weight
+  const float floor_v = endless ? m : __fadd_rd(m, sh.reach);
+  const uint32_t cb = (uint32_t)(cut >> 32);
+  const float cut_v = cut == kNoCut ? -INFINITY : __uint_as_float(cb >> 31 ? cb & 0x7FFFFFFFu : ~cb);
+  const float low_v = fmaxf(floor_v, cut_v);
   auto stays = [&](float v, int i) -> uint64_t {
     const uint64_t w = weight(v);
     return w >= least && (cut == kNoCut || key_of(v, i) >= cut) ? w : 0;
   };
   uint64_t own = 0;
-  for (int i = t0; i < t1; ++i) own += stays(get(i), i);
+#pragma unroll 4
+  for (int i = t0; i < t1; ++i) {
+    const float v = get(i);
+    if (v >= low_v) own += stays(v, i);
+  }
   uint64_t upto = own;  // of this warp's threads, this one's included
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -453,20 +573,15 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     if (r < rank) before += sh.box[turn][r][0];
     total += sh.box[turn][r][0];
   }
-  float u = a.uniform[row];
-  u = u > 0.0f ? u < 1.0f ? u : 0.99999994f : 0.0f;  // (NaN: 0)
   const uint64_t goal = share_of(total, u, false);  // a whole sum is above u * total where it is above this
   before += upto - own;
   if (before <= goal && before + own > goal) {  // one thread of the cluster
     for (int i = t0; i < t1; ++i) {
       const float v = get(i);
+      if (!(v >= low_v)) continue;
       before += stays(v, i);
       if (before > goal) {
-        a.token[row] = first + i;
-        if (a.logprob) {
-          const double l = endless ? 0.0 : ((double)v - (double)m) / (double)temperature;
-          a.logprob[row] = (float)(l - log((double)total * (1.0 / (1ull << kOneBits))));
-        }
+        write(first + i, v, total);
         break;
       }
     }
@@ -475,6 +590,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
 
 namespace {
 
+int g_sample_ctas = 8;  // of a cluster at most
+
 template <typename T>
 cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
   // As few CTAs per row as keep it in half an SM's shared memory each; more, down
@@ -482,7 +599,7 @@ cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
   int ctas = 1;
   auto seg = [&](int c) { return (a.vocabulary + c - 1) / c; };
   auto room = [&](int c) { return (int)((112 * 1024 - (int64_t)sizeof(SampleShared) - sample_slices(c)) / 4) - 8; };
-  while (ctas < kSampleMaxCtas && (seg(ctas) > room(ctas) || ((int64_t)a.rows * ctas < sms && seg(ctas) > 2048))) ctas *= 2;
+  while (ctas < g_sample_ctas && (seg(ctas) > room(ctas) || ((int64_t)a.rows * ctas < sms && seg(ctas) > 2048))) ctas *= 2;
   SampleLaunch p = {a, seg(ctas), 0, 0};
   p.run = (p.seg + kSampleThreads - 1) / kSampleThreads | 1;
   const int64_t most = (kSampleSmem - (int64_t)sizeof(SampleShared) - sample_slices(ctas)) / 4 - 8;
@@ -498,7 +615,8 @@ cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sample<T>, p);
+  const bool cuts = a.top_k || a.top_p || (a.top_k_all > 0 && a.top_k_all < a.vocabulary) || a.top_p_all < 1.0f;
+  return cuts ? cudaLaunchKernelEx(&cfg, k_sample<T, true>, p) : cudaLaunchKernelEx(&cfg, k_sample<T, false>, p);
 }
 
 }  // namespace
@@ -508,8 +626,30 @@ cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t st) {
 }
 
 cudaError_t prepare_sample_kernels() {
-  const cudaError_t e = cudaFuncSetAttribute(k_sample<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_sample<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem);
+  auto prepare = [](auto *k) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+  };
+  cudaError_t e = prepare(k_sample<float, true>);
+  if (e == cudaSuccess) e = prepare(k_sample<float, false>);
+  if (e == cudaSuccess) e = prepare(k_sample<__nv_bfloat16, true>);
+  if (e == cudaSuccess) e = prepare(k_sample<__nv_bfloat16, false>);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kSampleMaxCtas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSampleMaxCtas);
+  cfg.blockDim = dim3(kSampleThreads);
+  cfg.dynamicSmemBytes = kSampleSmem;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, k_sample<float, true>, &cfg) != cudaSuccess) cudaGetLastError();  // (8 then)
+  g_sample_ctas = clusters > 0 ? kSampleMaxCtas : 8;
+  return cudaSuccess;
 }
 
 }  // namespace nvfp4
