@@ -119,6 +119,7 @@ int device_info(DevInfo **out) {
       if (e == cudaSuccess) e = prepare_linear_tc_kernels();
       if (e == cudaSuccess) e = prepare_attention_kernels();
       if (e == cudaSuccess) e = prepare_moe_kernels();
+      if (e == cudaSuccess) e = prepare_route_kernels();
       if (e == cudaSuccess) e = prepare_sample_kernels();
       if (e != cudaSuccess) return map_cuda(e);
       cudaMemPoolProps props = {};

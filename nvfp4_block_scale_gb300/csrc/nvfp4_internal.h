@@ -197,6 +197,7 @@ bool moe_fits(int64_t hidden, int64_t inner, int experts, int pairs);
 size_t moe_workspace_bytes(int64_t hidden, int64_t inner, int pairs);
 cudaError_t prepare_moe_kernels();
 cudaError_t launch_moe(const MoeArgs &a, int sms, void *ws, cudaStream_t st);
+cudaError_t prepare_route_kernels();
 cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st);
 cudaError_t prepare_sample_kernels();
 cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t st);

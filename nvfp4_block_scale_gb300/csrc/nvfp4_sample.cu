@@ -94,8 +94,9 @@ __device__ __forceinline__ uint64_t share_of(uint64_t m, float f, bool ceiling) 
 }
 
 // Shared memory of a CTA before its tokens' values.
+template <bool CUTS>
 struct alignas(16) SampleShared {
-  uint32_t hist[3][kBins];  // counts; masses' low and high words.  CTA 0: also the list.
+  uint32_t hist[3][CUTS ? kBins : 4];  // counts; masses' low and high words.  CTA 0: also the list.
   uint2 pow2[256];
   uint64_t box[2][kSampleMaxCtas][4];  // what the cluster's CTAs tell each other, in turn
   uint64_t warp_sum[kSampleWarps];
@@ -112,9 +113,9 @@ struct alignas(16) SampleShared {
 struct SampleList {  // over the histogram
   uint64_t key[kList], mass[kList];
 };
-static_assert(sizeof(SampleList) <= sizeof(uint32_t) * 3 * kBins, "the list lies over the histogram");
+static_assert(sizeof(SampleList) <= sizeof(SampleShared<true>::hist), "the list lies over the histogram");
 // The slices' totals (for the first histogram and for a finer one), then the values.
-__host__ __device__ constexpr int64_t sample_slices(int ctas) { return 2 * (int64_t)(kBins / ctas) * 12; }
+__host__ __device__ constexpr int64_t sample_slices(bool cuts, int ctas) { return cuts ? 2 * (int64_t)(kBins / ctas) * 12 : 0; }
 
 constexpr uint64_t kNoCut = 0;  // keeps every token
 
@@ -124,14 +125,14 @@ template <typename T, bool CUTS>
 __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_constant__ SampleLaunch p) {
   constexpr int kVec = 16 / sizeof(T);
   extern __shared__ __align__(16) uint8_t dsm[];
-  SampleShared &sh = *reinterpret_cast<SampleShared *>(dsm);
+  SampleShared<CUTS> &sh = *reinterpret_cast<SampleShared<CUTS> *>(dsm);
   const auto cluster = cg::this_cluster();
   const SampleArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), bins = kBins / ctas;
-  uint64_t *slice_mass = reinterpret_cast<uint64_t *>(dsm + sizeof(SampleShared));     // [2][bins]
+  uint64_t *slice_mass = reinterpret_cast<uint64_t *>(dsm + sizeof(sh));     // [2][bins]
   uint32_t *slice_count = reinterpret_cast<uint32_t *>(slice_mass + 2 * bins);         // [2][bins]
-  float *vals = reinterpret_cast<float *>(slice_count + 2 * bins);
+  float *vals = reinterpret_cast<float *>(CUTS ? (void *)(slice_count + 2 * bins) : (void *)slice_mass);
   const int row = blockIdx.x / ctas;
   const int first = rank * p.seg, n = max(0, min(p.seg, a.vocabulary - first));
   const T *logits = static_cast<const T *>(a.logits) + (int64_t)row * a.stride + first;
@@ -592,18 +593,20 @@ namespace {
 
 int g_sample_ctas = 8;  // of a cluster at most
 
-template <typename T>
+template <typename T, bool CUTS>
 cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
-  // As few CTAs per row as keep it in half an SM's shared memory each; more, down
-  // to 2048 tokens each, while that leaves SMs idle.
+  // As few CTAs per row as let two of them share an SM (three, of twice as many, took 133
+  // us instead of 124 on 256 x 151003); more, down to 2048 tokens each, while that
+  // leaves SMs idle.
   int ctas = 1;
+  const int64_t share = 112 * 1024;
+  auto fixed = [&](int c) { return (int64_t)sizeof(SampleShared<CUTS>) + sample_slices(CUTS, c); };
   auto seg = [&](int c) { return (a.vocabulary + c - 1) / c; };
-  auto room = [&](int c) { return (int)((112 * 1024 - (int64_t)sizeof(SampleShared) - sample_slices(c)) / 4) - 8; };
-  while (ctas < g_sample_ctas && (seg(ctas) > room(ctas) || ((int64_t)a.rows * ctas < sms && seg(ctas) > 2048))) ctas *= 2;
+  while (ctas < g_sample_ctas && (seg(ctas) > (share - fixed(ctas)) / 4 - 8 || ((int64_t)a.rows * ctas < sms && seg(ctas) > 2048)))
+    ctas *= 2;
   SampleLaunch p = {a, seg(ctas), 0, 0};
   p.run = (p.seg + kSampleThreads - 1) / kSampleThreads | 1;
-  const int64_t most = (kSampleSmem - (int64_t)sizeof(SampleShared) - sample_slices(ctas)) / 4 - 8;
-  p.cap = (int)std::min<int64_t>(p.seg, most);
+  p.cap = (int)std::min<int64_t>(p.seg, (kSampleSmem - fixed(ctas)) / 4 - 8);
   cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = (unsigned)ctas;
@@ -611,18 +614,19 @@ cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * ctas));
   cfg.blockDim = dim3(kSampleThreads);
-  cfg.dynamicSmemBytes = sizeof(SampleShared) + (size_t)sample_slices(ctas) + 4 * ((size_t)p.cap + 8);
+  cfg.dynamicSmemBytes = (size_t)fixed(ctas) + 4 * ((size_t)p.cap + 8);
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const bool cuts = a.top_k || a.top_p || (a.top_k_all > 0 && a.top_k_all < a.vocabulary) || a.top_p_all < 1.0f;
-  return cuts ? cudaLaunchKernelEx(&cfg, k_sample<T, true>, p) : cudaLaunchKernelEx(&cfg, k_sample<T, false>, p);
+  return cudaLaunchKernelEx(&cfg, k_sample<T, CUTS>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t st) {
-  return a.fp32 ? sample_launch<float>(a, sms, st) : sample_launch<__nv_bfloat16>(a, sms, st);
+  const bool cuts = a.top_k || a.top_p || (a.top_k_all > 0 && a.top_k_all < a.vocabulary) || a.top_p_all < 1.0f;
+  if (a.fp32) return cuts ? sample_launch<float, true>(a, sms, st) : sample_launch<float, false>(a, sms, st);
+  return cuts ? sample_launch<__nv_bfloat16, true>(a, sms, st) : sample_launch<__nv_bfloat16, false>(a, sms, st);
 }
 
 cudaError_t prepare_sample_kernels() {

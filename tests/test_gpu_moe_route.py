@@ -29,17 +29,25 @@ def _check(x, router, k, scoring="softmax", renormalize=True, bias=None, scale=1
     torch.cuda.synchronize()
     wi, ww = _want(x, router, k, scoring, renormalize, bias, scale)
     assert np.array_equal(ids.cpu().numpy(), wi)
+    # many tokens and experts: chosen as if exactly, weighted by logits off by 2^-18 (2^-16.4 with an fp32 router) of
+    # their vectors' norms at most, which move a weight by twice that of itself at most
+    off = 0.0
+    if x.shape[0] >= 32 and router.shape[0] >= 64:
+        off = 2 ** (-18 if router.dtype == torch.bfloat16 else -16.4) * \
+            x.double().norm(dim=1).numpy()[:, None] * float(router.double().norm(dim=1).max())
     # an exponential good to 2 ulp of an argument off by 2^-24 of up to 40, a sum of up to 1024 of them in any order
     # (each lane's at most 64 roundings deep), a quotient and a product
     err = np.abs(w.double().cpu().numpy() - ww)
-    assert np.all(err <= (2 * (2 ** -22 + 40 * 2.0 ** -24) + 64 * 2.0 ** -24 + 2 ** -23) * np.abs(ww) + 1e-44)
+    assert np.all(err <= (2 * off + 2 * (2 ** -22 + 40 * 2.0 ** -24) + 64 * 2.0 ** -24 + 2 ** -23) * np.abs(ww) + 1e-44)
     return ids, w
 
 
 # tokens, hidden, experts, k: one of everything; fewer experts than CTAs of a cluster; tokens that no cluster divides;
-# more experts than threads; every expert chosen; columns that no lane divides
+# more experts than threads; every expert chosen; columns that no lane divides; many tokens and experts (the tensor
+# cores): fewer columns than warps, tokens that no tile divides, all of an expert's warps
 SHAPES = [(1, 8, 1, 1), (1, 2048, 128, 8), (3, 264, 5, 5), (61, 512, 8, 2), (130, 72, 60, 6), (700, 40, 33, 3),
-          (2, 136, 1024, 32), (9, 7168, 256, 8), (1, 1000, 3, 1)]
+          (2, 136, 1024, 32), (9, 7168, 256, 8), (1, 1000, 3, 1),
+          (32, 8, 64, 6), (33, 72, 64, 8), (200, 520, 256, 8), (47, 4096, 1000, 32), (300, 1032, 129, 1)]
 
 
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
@@ -54,8 +62,9 @@ def test_choice_and_weights(shape, scoring, renormalize, kind):
     _check(x, r, k, scoring, renormalize, bias, 2.5 if scoring == "sigmoid" else 1.0)
 
 
+@pytest.mark.parametrize("tokens", [5, 40])
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
-def test_scores_closer_than_fp32_tells_apart(kind):
+def test_scores_closer_than_fp32_tells_apart(kind, tokens):
     """Every logit is 2^14 (eleven 1024s and so on, large and cancelling ones
     among them) plus a multiple of 2^-12, which fp32 would drop."""
     g = torch.Generator().manual_seed(3)
@@ -65,14 +74,37 @@ def test_scores_closer_than_fp32_tells_apart(kind):
     r[:, 0::2] = 64.0 * torch.randint(1, 200, (experts, hidden // 2), generator=g)
     r[:, 1::2] = -r[:, 0::2]
     r = r[:, torch.randperm(hidden, generator=g)]
-    x = torch.ones((5, hidden))
+    x = torch.ones((tokens, hidden))
     r[:, 7], r[:, 300], r[:, 5] = 16384.0, small * 2.0 ** -12, 0.0
     r[:, 5] = 16384.0 - r.sum(1) + small * 2.0 ** -12  # what the pairs that were overwritten left over
     r = r.to(kind)
     exact = r.double().sum(1)
     ids, _ = nv.moe_route(x.to(torch.bfloat16).cuda(), r.cuda(), 32, "softmax", True)
     order = sorted(range(experts), key=lambda e: (-exact[e].item(), e))[:32]
-    assert exact.unique().numel() > 32 and ids.cpu().tolist() == [order] * 5
+    assert exact.unique().numel() > 32 and ids.cpu().tolist() == [order] * tokens
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_neighbours_in_every_token(kind):
+    """Experts in pairs whose logits differ by 2^-20 of their terms' sizes: the tensor cores leave each pair open."""
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn((50, 512), generator=g).to(torch.bfloat16)
+    r = torch.randn((64, 512), generator=g).to(torch.bfloat16)
+    r = torch.cat((r, r))
+    r[64:, 3] = 0.0
+    r[:64, 3] = 2.0 ** -12 * torch.randn(64, generator=g).to(torch.bfloat16)
+    _check(x, r.to(kind), 16)
+    _check(x, r.to(kind), 16, "sigmoid", True, 0.01 * torch.randn(64, generator=g).repeat(2))
+
+
+def test_tokens_of_zeros_and_tiny_ones():
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn((40, 256), generator=g)
+    x[::7] = 0.0
+    x[3] *= 2.0 ** -90
+    r = torch.randn((128, 256), generator=g).to(torch.bfloat16)
+    _check(x.to(torch.bfloat16), r, 5)
+    _check(x.to(torch.bfloat16), torch.cat((r[:64], r[:64])), 5, "sigmoid", False, torch.zeros(128))
 
 
 def test_equal_scores_go_to_the_lower_expert():
