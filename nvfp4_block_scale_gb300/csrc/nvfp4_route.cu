@@ -19,6 +19,7 @@
 // expert's rank is the number of those before it.  No global memory, no second
 // launch.
 #include <algorithm>
+#include <climits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -31,8 +32,8 @@ namespace nvfp4 {
 
 namespace cg = cooperative_groups;
 
-constexpr int kRouteCtas = 8;
 constexpr int kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
+constexpr int kTcCtas = 8, kTcThreads = 256, kTcWarps = kTcThreads / 32;  // of the kernel for many tokens
 
 // Adds a * b to the sum hi + lo.
 __device__ __forceinline__ void add_product(float a, float b, float &hi, float &lo, bool exact) {
@@ -73,9 +74,9 @@ struct RouterLoad<float> {
   }
 };
 
-// A number's place in the order of scores: NaN below everything.
+// A number's place in the order of scores, above 0: NaN below everything.
 __device__ __forceinline__ uint64_t score_key(double v) {
-  if (v != v) return 0;
+  if (v != v) return 1;
   if (v == 0.0) v = 0.0;  // (-0 and 0 are equal)
   const uint64_t b = (uint64_t)__double_as_longlong(v);
   return b >> 63 ? ~b : b | 1ull << 63;
@@ -85,13 +86,22 @@ __device__ __forceinline__ uint64_t score_key(double v) {
 template <typename R>
 __device__ __forceinline__ double exact_dot(const __nv_bfloat16 *x, const R *w, int u0, int u1, int lane) {
   float hi = 0.0f, lo = 0.0f;
-  for (int u = u0 + lane; u < u1; u += 32) {
-    RouterLoad<R> r;
-    RouterLoad<__nv_bfloat16> v;
-    r.get(w + 8 * u);
-    v.get(x + 8 * u);
+  constexpr int kAhead = 4;
+  for (int u = u0 + lane; u < u1; u += 32 * kAhead) {
+    RouterLoad<R> r[kAhead];
+    RouterLoad<__nv_bfloat16> v[kAhead];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) add_product(r.at(c), v.at(c), hi, lo, sizeof(R) == 2);
+    for (int i = 0; i < kAhead; ++i) {
+      const int at = min(u + 32 * i, u1 - 1);
+      r[i].get(w + 8 * at);
+      v[i].get(x + 8 * at);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (u + 32 * i >= u1) break;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) add_product(r[i].at(c), v[i].at(c), hi, lo, sizeof(R) == 2);
+    }
   }
   double d = (double)hi + (double)lo;
 #pragma unroll
@@ -103,47 +113,51 @@ __device__ __forceinline__ double route_score(const RouteArgs &a, double logit, 
   return a.sigmoid ? 1.0 / (1.0 + exp(-logit)) + (a.bias ? (double)a.bias[e] : 0.0) : logit;
 }
 
-// A token's experts and weights from its logits, by the whole CTA.
-__device__ void choose(const RouteArgs &a, int64_t t, const double *l, uint64_t *keys, int *best, float *partial) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e < a.experts; e += kRouteThreads) keys[e] = score_key(route_score(a, l[e], e));
-  if (tid < kMaxTopK) best[tid] = 0;
-  __syncthreads();
-  for (int e = tid; e < a.experts; e += kRouteThreads) {
-    const uint64_t k = keys[e];
-    int before = 0;
-    for (int o = 0; o < a.experts; ++o) before += keys[o] > k || (keys[o] == k && o < e);
-    if (before < a.top_k) best[before] = e;
+// A token's top_k experts in order, by one warp: in each of top_k rounds every lane
+// offers the first of its own (e = lane, lane + 32, ..) that is left.  Lane i has
+// the i-th in the end.
+__device__ __forceinline__ int choose(const RouteArgs &a, uint64_t *keys, int lane) {
+  uint64_t best = 0;
+  int at = INT_MAX, chosen = 0;
+  auto look = [&] {
+    best = 0, at = INT_MAX;
+    for (int e = lane; e < a.experts; e += 32)
+      if (keys[e] > best) best = keys[e], at = e;
+  };
+  look();
+  for (int i = 0; i < a.top_k; ++i) {
+    const uint32_t hi = __reduce_max_sync(~0u, (uint32_t)(best >> 32));
+    const uint32_t lo = __reduce_max_sync(~0u, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+    const bool first = (uint32_t)(best >> 32) == hi && (uint32_t)best == lo;
+    const int e = (int)__reduce_min_sync(~0u, first ? (unsigned)at : ~0u);
+    if (lane == i) chosen = e;
+    if (e == at) {
+      keys[e] = 0;
+      look();
+    }
   }
-  __syncthreads();
-  // softmax: its maximum is the first choice's logit; its sum in a fixed order
-  const double m = l[best[0]];
-  if (!a.sigmoid && !a.renormalize) {
-    float z = 0.0f;
-    for (int e = tid; e < a.experts; e += kRouteThreads) z += expf((float)(l[e] - m));
+  return chosen;
+}
+
+// Its weights, by the same warp; lane i's expert is the i-th.
+__device__ __forceinline__ void weigh(const RouteArgs &a, int64_t t, const double *l, int e, int lane) {
+  const double m = l[__shfl_sync(~0u, e, 0)];  // softmax: the first choice has the largest logit
+  float w = 0.0f, z = 1.0f;
+  if (lane < a.top_k) w = a.sigmoid ? (float)(1.0 / (1.0 + exp(-l[e]))) : expf((float)(l[e] - m));
+  if (a.renormalize) {
+    z = w;
+  } else if (!a.sigmoid) {
+    z = 0.0f;
+    for (int o = lane; o < a.experts; o += 32) z += expf((float)(l[o] - m));
+  }
+  if (a.renormalize || !a.sigmoid) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
-    if (lane == 0) partial[warp] = z;
   }
-  __syncthreads();
-  if (warp == 0) {
-    const int e = best[min(lane, a.top_k - 1)];
-    float w = lane < a.top_k ? a.sigmoid ? (float)(1.0 / (1.0 + exp(-l[e]))) : expf((float)(l[e] - m)) : 0.0f;
-    float z = 1.0f;
-    if (a.renormalize) {
-      z = w;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
-    } else if (!a.sigmoid) {
-      z = 0.0f;
-      for (int i = 0; i < kRouteWarps; ++i) z += partial[i];
-    }
-    if (lane < a.top_k) {
-      a.ids[t * a.top_k + lane] = e;
-      a.weights[t * a.top_k + lane] = __fdiv_rn(w, z) * a.scale;
-    }
+  if (lane < a.top_k) {
+    a.ids[t * a.top_k + lane] = e;
+    a.weights[t * a.top_k + lane] = __fdiv_rn(w, z) * a.scale;
   }
-  __syncthreads();
 }
 
 struct RouteLaunch {
@@ -154,14 +168,13 @@ struct RouteLaunch {
 
 template <typename R, int G>
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __grid_constant__ RouteLaunch p) {
-  // [splits][per][G] sums, later [experts] keys; then the logits of this CTA's tokens [ceil(G / kRouteCtas)][experts]
+  // [splits][per][G] sums, later [experts] keys; then the logits of this CTA's token [experts]
   extern __shared__ double sums[];
-  __shared__ int best[kMaxTopK];
-  __shared__ float partial[kRouteWarps];
   const RouteArgs &a = p.a;
   const auto cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = (int)cluster.block_rank();
-  const int64_t t0 = (int64_t)(blockIdx.x / kRouteCtas) * G;
+  static_assert(G <= 8, "a token per CTA of the cluster at most");
+  const int64_t t0 = (int64_t)(blockIdx.x / cluster.num_blocks()) * G;
   const int tokens = (int)min((int64_t)G, a.tokens - t0);
   const int e0 = rank * p.per, mine = max(0, min(p.per, a.experts - e0));
   double *const logits = sums + max(p.splits * p.per * G, a.experts);
@@ -178,7 +191,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __grid_consta
     float hi[G], lo[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) hi[g] = lo[g] = 0.0f;
-    constexpr int kAhead = G <= 2 ? 4 : 2;
+    constexpr int kAhead = G == 1 ? 8 : G == 2 ? 4 : 2;
     for (int u = u0 + lane; u < u1; u += 32 * kAhead) {
       RouterLoad<R> r[kAhead];
       RouterLoad<__nv_bfloat16> v[kAhead][G];
@@ -223,13 +236,18 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __grid_consta
     const int e = i / tokens, g = i - e * tokens;
     double v = 0.0;
     for (int s = 0; s < p.splits; ++s) v += sums[((size_t)s * p.per + e) * G + g];
-    cluster.map_shared_rank(logits, g % kRouteCtas)[(g / kRouteCtas) * a.experts + e0 + e] = v;
+    cluster.map_shared_rank(logits, g)[e0 + e] = v;
   }
   cluster.sync();
 
   // ---- the choice
-  for (int g = rank, r = 0; g < tokens; g += kRouteCtas, ++r)
-    choose(a, t0 + g, logits + (size_t)r * a.experts, reinterpret_cast<uint64_t *>(sums), best, partial);  // (the sums are spent)
+  if (rank >= tokens) return;
+  uint64_t *keys = reinterpret_cast<uint64_t *>(sums);  // (the sums are spent)
+  for (int e = tid; e < a.experts; e += kRouteThreads) keys[e] = score_key(route_score(a, logits[e], e));
+  __syncthreads();
+  if (warp > 0) return;
+  const int e = choose(a, keys, lane);
+  weigh(a, t0 + rank, logits, e, lane);
 }
 
 // Many tokens: the products on the tensor cores (mma.sync m16n8k16, 16 experts by 8
@@ -268,17 +286,16 @@ __device__ __forceinline__ float squares(const uint4 &v) {
 }
 
 template <typename R>
-__global__ void __launch_bounds__(kRouteThreads) k_moe_route_tc(const __grid_constant__ RouteLaunch p) {
-  // [splits][tiles * 16][kTcTokens] sums, later [experts] keys and [experts] fp32 scores; the logits of this CTA's
-  // tokens [2][experts]; norms of the router's rows [experts], of this CTA's by split, of the tokens by split, and
-  // whether a token has an entry other than 0
+__global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_constant__ RouteLaunch p) {
+  // [splits][tiles * 16][kTcTokens] sums, later [2][experts] keys; the logits of this CTA's two tokens [2][experts];
+  // norms of the router's rows [experts], of this CTA's by split, of the tokens by split, whether a token has an
+  // entry other than 0, and the scores of the two tokens [2][experts]
   extern __shared__ double sums[];
-  __shared__ int best[kMaxTopK], doubtful, list[kMaxExperts];
-  __shared__ float partial[kRouteWarps];
+  __shared__ int doubtful, list[2 * kMaxExperts];
   const RouteArgs &a = p.a;
   const auto cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3, rank = (int)cluster.block_rank();
-  const int64_t t0 = (int64_t)(blockIdx.x / kRouteCtas) * kTcTokens;
+  const int64_t t0 = (int64_t)(blockIdx.x / kTcCtas) * kTcTokens;
   const int tokens = (int)min((int64_t)kTcTokens, a.tokens - t0);
   const int e0 = rank * p.per, mine = max(0, min(p.per, a.experts - e0));
   const int tiles = (p.per + 15) / 16, rows = tiles * 16;
@@ -287,13 +304,15 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_tc(const __grid_con
   float *const row_part = row_norm + a.experts;                               // [splits][rows]
   float *const token_part = row_part + p.splits * rows;                       // [splits][kTcTokens]
   uint32_t *const token_any = reinterpret_cast<uint32_t *>(token_part + p.splits * kTcTokens);  // [splits][kTcTokens]
+  float *const scores = reinterpret_cast<float *>(token_any + p.splits * kTcTokens);            // [2][experts]
+  if (tid == 0) doubtful = 0;
   pdl_wait();
   pdl_launch_dependents();
 
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x) + t0 * a.x_stride;
   const int eighths = (int)(a.hidden / 8), steps = (eighths + 3) / 4;
-  if (warp < tiles * p.splits) {
-    const int tile = warp / p.splits, s = warp - tile * p.splits;
+  for (int task = warp; task < tiles * p.splits; task += kTcWarps) {
+    const int tile = task / p.splits, s = task - tile * p.splits;
     const int k0 = (int)((int64_t)s * steps / p.splits), k1 = (int)((int64_t)(s + 1) * steps / p.splits);
     const R *w[2];
     const __nv_bfloat16 *v[2];
@@ -308,7 +327,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_tc(const __grid_con
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) hi[i][c] = lo[i][c] = 0.0f;
-    constexpr int kAhead = 2;
+    constexpr int kAhead = sizeof(R) == 2 ? 4 : 2;
     struct Step {
       RouterLoad<R> r[2];
       RouterLoad<__nv_bfloat16> t[2];
@@ -396,55 +415,81 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route_tc(const __grid_con
   }
   __syncthreads();
   // ---- every logit to the CTA of its token, every row's norm to all
-  for (int i = tid; i < mine * kTcTokens; i += kRouteThreads) {
+  for (int i = tid; i < mine * kTcTokens; i += kTcThreads) {
     const int e = i / kTcTokens, t = i - e * kTcTokens;
     double v = 0.0;
     for (int s = 0; s < p.splits; ++s) v += sums[((size_t)s * rows + e) * kTcTokens + t];
-    cluster.map_shared_rank(logits, t % kRouteCtas)[(t / kRouteCtas) * a.experts + e0 + e] = v;
+    cluster.map_shared_rank(logits, t % kTcCtas)[(t / kTcCtas) * a.experts + e0 + e] = v;
   }
-  for (int i = tid; i < mine * kRouteCtas; i += kRouteThreads) {
-    const int e = i / kRouteCtas, r = i - e * kRouteCtas;
+  for (int i = tid; i < mine * kTcCtas; i += kTcThreads) {
+    const int e = i / kTcCtas, r = i - e * kTcCtas;
     float n = 0.0f;
     for (int s = 0; s < p.splits; ++s) n += row_part[s * rows + e];
     cluster.map_shared_rank(row_norm, r)[e0 + e] = sqrtf(n);
   }
   cluster.sync();
 
-  // ---- experts in doubt, exactly; the choice
-  float *const scores = reinterpret_cast<float *>(sums + a.experts);  // (the sums are spent)
-  for (int t = rank, r = 0; t < tokens; t += kRouteCtas, ++r) {
-    double *l = logits + (size_t)r * a.experts;
+  // ---- the choice of each of this CTA's tokens, by a warp
+  uint64_t *const keys = reinterpret_cast<uint64_t *>(sums);  // (the sums are spent)
+  auto make_keys = [&] {
+    for (int i = tid; i < 2 * a.experts; i += kTcThreads) {
+      const int r = i >= a.experts, e = i - r * a.experts;
+      if (rank + r * kTcCtas >= tokens) continue;
+      const double s = route_score(a, logits[i], e);
+      keys[i] = score_key(s);
+      scores[i] = (float)s;
+    }
+    __syncthreads();
+  };
+  make_keys();
+  const int t = rank + warp * kTcCtas;  // this warp's token
+  const bool has = warp < 2 && t < tokens;
+  int e = 0;
+  if (has) {
+    const float *score = scores + (size_t)warp * a.experts;
+    e = choose(a, keys + (size_t)warp * a.experts, lane);
     float norm = 0.0f;
     uint32_t any = 0u;
     for (int s = 0; s < p.splits; ++s) norm += token_part[s * kTcTokens + t], any |= token_any[s * kTcTokens + t];
     // (squares that may have underflowed bound nothing; a token of zeros has exact logits)
     norm = norm > 0x1p-100f ? sqrtf(norm) * kBand<R> : INFINITY;
-    if (tid == 0) doubtful = 0;
-    for (int e = tid; e < a.experts; e += kRouteThreads) scores[e] = (float)route_score(a, l[e], e);
-    __syncthreads();
-    for (int e = any ? tid : a.experts; e < a.experts; e += kRouteThreads) {
-      const float s = scores[e], own = norm * row_norm[e];
-      int before = 0;
-      bool near = false;
-      for (int o = 0; o < a.experts; ++o) {
-        // scores' distance that arithmetic explains (a sigmoid's slope is at most 1/4; 2^-22 for the scores' own roundings)
-        const float band = (own + norm * row_norm[o]) * (a.sigmoid ? 0.25f : 1.0f) + 0x1p-22f * (fabsf(s) + fabsf(scores[o]));
-        const float d = scores[o] - s;
-        before += d > band;
-        near |= o != e && !(fabsf(d) > band);
+    // how far arithmetic may have moved an expert's score (a sigmoid's slope is at most 1/4; 2^-22 for roundings)
+    auto off = [&](int o, float s) { return norm * row_norm[o] * (a.sigmoid ? 0.25f : 1.0f) + 0x1p-22f * fabsf(s); };
+    // those that may be among the chosen reach up to where the last of these may have come from
+    const float s0 = lane < a.top_k ? score[e] : INFINITY, low = lane < a.top_k ? s0 - off(e, s0) : INFINITY;
+    float least = low;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
+    for (int o0 = 0; any && o0 < a.experts; o0 += 32) {
+      const int o = o0 + lane;
+      const float so = o < a.experts ? score[o] : 0.0f, bo = o < a.experts ? off(o, so) : 0.0f;
+      for (uint32_t todo = __ballot_sync(~0u, o < a.experts && !(so + bo < least)); todo; todo &= todo - 1) {
+        // one of them: does another's range meet its own?
+        const int src = __ffs(todo) - 1, c = o0 + src;
+        const float sc = __shfl_sync(~0u, so, src), bc = __shfl_sync(~0u, bo, src);
+        bool near = false;
+        for (int q = lane; q < a.experts; q += 32) {
+          const float sq = score[q];
+          near |= q != c && !(fabsf(sq - sc) > bc + off(q, sq));
+        }
+        if (__any_sync(~0u, near) && lane == 0) list[atomicAdd(&doubtful, 1)] = warp * a.experts + c;
       }
-      if (near && before < a.top_k) list[atomicAdd(&doubtful, 1)] = e;
     }
-    __syncthreads();
-    const int count = doubtful;
-    for (int i = warp; i < count; i += kRouteWarps) {
-      const int e = list[i];
-      const double v = exact_dot(x + (int64_t)t * a.x_stride, static_cast<const R *>(a.router) + (int64_t)e * a.router_stride, 0, eighths, lane);
-      if (lane == 0) l[e] = v;
-    }
-    __syncthreads();
-    choose(a, t0 + t, l, reinterpret_cast<uint64_t *>(sums), best, partial);
   }
+  __syncthreads();
+  const int count = doubtful;
+  if (count > 0) {  // those once more, exactly
+    for (int i = warp; i < count; i += kTcWarps) {
+      const int r = list[i] >= a.experts, c = list[i] - r * a.experts;
+      const double v = exact_dot(x + (int64_t)(rank + r * kTcCtas) * a.x_stride,
+                                 static_cast<const R *>(a.router) + (int64_t)c * a.router_stride, 0, eighths, lane);
+      if (lane == 0) logits[list[i]] = v;
+    }
+    __syncthreads();
+    make_keys();
+    if (has) e = choose(a, keys + (size_t)warp * a.experts, lane);
+  }
+  if (has) weigh(a, t0 + t, logits + (size_t)warp * a.experts, e, lane);
 }
 
 namespace {
@@ -459,47 +504,50 @@ auto with_route(bool fp32, int g, F f) {
 }
 
 size_t route_smem(const RouteLaunch &p, int g) {
-  return ((size_t)std::max(p.splits * p.per * g, p.a.experts) + (size_t)((g + kRouteCtas - 1) / kRouteCtas) * p.a.experts) * sizeof(double);
+  return ((size_t)std::max(p.splits * p.per * g, p.a.experts) + (size_t)p.a.experts) * sizeof(double);
 }
 
 size_t route_tc_smem(const RouteLaunch &p) {
   const int rows = (p.per + 15) / 16 * 16, e = p.a.experts;
   return ((size_t)std::max(p.splits * rows * kTcTokens, 2 * e) + 2 * (size_t)e) * sizeof(double) +
-         ((size_t)e + (size_t)p.splits * (rows + 2 * kTcTokens)) * sizeof(float);
+         (3 * (size_t)e + (size_t)p.splits * (rows + 2 * kTcTokens)) * sizeof(float);
 }
 
 }  // namespace
 
 cudaError_t prepare_route_kernels() {
-  // splits * rows <= 256 rows of 16 tokens, and 1024 experts
-  const int most = (256 * kTcTokens + 2 * kMaxExperts) * 8 + (kMaxExperts + 256 + kRouteWarps * 2 * kTcTokens) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(k_moe_route_tc<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_moe_route_tc<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  // splits * rows <= 128 rows of 16 tokens, and 1024 experts
+  const int most = (128 * kTcTokens + 4 * kMaxExperts) * 8 + (3 * kMaxExperts + 128 + kTcWarps * 2 * kTcTokens) * 4;
+  cudaError_t e = cudaFuncSetAttribute(k_moe_route_tc<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_moe_route_tc<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  return e;
 }
 
 cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st) {
-  RouteLaunch p = {a, (a.experts + kRouteCtas - 1) / kRouteCtas, 1};
-  p.splits = std::max(1, std::min<int>(kRouteWarps / p.per, (int)(a.hidden / 256)));
+  RouteLaunch p = {a, 0, 1};
   // The tensor cores where they fill their tiles.  Measured (us): XXX
   const bool tc = a.tokens >= 32 && a.experts >= 64;
+  int g = kTcTokens, ctas = kTcCtas, threads = kTcThreads;
+  p.per = (a.experts + ctas - 1) / ctas;
   if (tc) {
-    const int tiles = (p.per + 15) / 16;
-    p.splits = std::min(kRouteWarps / tiles, (int)((a.hidden + 31) / 32));
+    p.splits = std::max(1, std::min(kTcWarps / ((p.per + 15) / 16), (int)((a.hidden + 31) / 32)));
+  } else {
+    // as few tokens per cluster as one wave of CTAs allows: a router row's way
+    // through L2 is shared by a cluster's tokens, but a lane's work is theirs together
+    g = 1, threads = kRouteThreads;
+    p.splits = std::max(1, std::min<int>(kRouteWarps / p.per, (int)(a.hidden / 256)));
+    while (g < 8 && (a.tokens + g - 1) / g * ctas > 2 * sms) g *= 2;
   }
-  // as few tokens per cluster as one wave of CTAs allows: a router row's way
-  // through L2 is shared by a cluster's tokens, but a lane's work is theirs together
-  int g = tc ? kTcTokens : 1;
-  while (!tc && g < 8 && (a.tokens + g - 1) / g * kRouteCtas > 2 * sms) g *= 2;
   const int64_t groups = (a.tokens + g - 1) / g;
   cudaLaunchAttribute at[2] = {};
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kRouteCtas;
+  at[0].val.clusterDim.x = (unsigned)ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * kRouteCtas));
-  cfg.blockDim = dim3(kRouteThreads);
+  cfg.gridDim = dim3((unsigned)(groups * ctas));
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = tc ? route_tc_smem(p) : route_smem(p, g);
   cfg.stream = st;
   cfg.attrs = at;
