@@ -381,9 +381,9 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
  *   errors kept in a second fp32 sum) and fp64 scores, so experts whose scores
  *   agree in fp32 are still told apart; equal scores go to the lower expert,
  *   and a NaN is below every number.  ids are in descending order of the score.
- *   Weights are fp32; from 32 tokens and 64 experts on they follow logits of fp32
- *   accuracy (off by 2^-18 of ||x|| ||router[e]|| at most, 2^-16 with an fp32
- *   router).  Results repeat bit for bit.
+ *   Weights are fp32; those of many tokens (128 or more, or 16 with 8192 scores
+ *   among them) follow logits of fp32 accuracy (off by 2^-18 of ||x|| ||router[e]||
+ *   at most, 2^-16 with an fp32 router).  Results repeat bit for bit.
  * Arguments:
  *   x       device, bf16, 16-byte aligned, [tokens][hidden], rows x_stride
  *           elements apart (>= hidden, a multiple of 8).  x and router finite.

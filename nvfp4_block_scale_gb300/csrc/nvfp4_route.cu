@@ -33,6 +33,7 @@ namespace nvfp4 {
 namespace cg = cooperative_groups;
 
 constexpr int kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteMaxCtas = 16;  // of a cluster (8 where a device cannot place more)
 constexpr int kTcCtas = 8, kTcThreads = 256, kTcWarps = kTcThreads / 32;  // of the kernel for many tokens
 
 // Adds a * b to the sum hi + lo.
@@ -87,7 +88,7 @@ template <typename R>
 __device__ __forceinline__ double exact_dot(const __nv_bfloat16 *x, const R *w, int u0, int u1, int lane) {
   float hi = 0.0f, lo = 0.0f;
   constexpr int kAhead = 4;
-  for (int u = u0 + lane; u < u1; u += 32 * kAhead) {
+  for (int u = u0 + lane; u < u1; u += 32 * kAhead) {  // (u1 > u0 wherever this loads)
     RouterLoad<R> r[kAhead];
     RouterLoad<__nv_bfloat16> v[kAhead];
 #pragma unroll
@@ -109,8 +110,14 @@ __device__ __forceinline__ double exact_dot(const __nv_bfloat16 *x, const R *w, 
   return d;
 }
 
+__device__ __forceinline__ float sigmoid(float v) { return __fdiv_rn(1.0f, 1.0f + expf(-v)); }
 __device__ __forceinline__ double route_score(const RouteArgs &a, double logit, int e) {
   return a.sigmoid ? 1.0 / (1.0 + exp(-logit)) + (a.bias ? (double)a.bias[e] : 0.0) : logit;
+}
+// The same in fp32, off by at most 2^-21 of itself and (a sigmoid's) of 1: fp64's
+// exponentials take longer than everything else about a choice.
+__device__ __forceinline__ float route_score_fp32(const RouteArgs &a, double logit, int e) {
+  return a.sigmoid ? sigmoid((float)logit) + (a.bias ? a.bias[e] : 0.0f) : (float)logit;
 }
 
 // A token's top_k experts in order, by one warp: in each of top_k rounds every lane
@@ -121,8 +128,11 @@ __device__ __forceinline__ int choose(const RouteArgs &a, uint64_t *keys, int la
   int at = INT_MAX, chosen = 0;
   auto look = [&] {
     best = 0, at = INT_MAX;
-    for (int e = lane; e < a.experts; e += 32)
-      if (keys[e] > best) best = keys[e], at = e;
+#pragma unroll 4
+    for (int e = lane; e < a.experts; e += 32) {
+      const uint64_t k = keys[e];
+      if (k > best) best = k, at = e;
+    }
   };
   look();
   for (int i = 0; i < a.top_k; ++i) {
@@ -143,7 +153,7 @@ __device__ __forceinline__ int choose(const RouteArgs &a, uint64_t *keys, int la
 __device__ __forceinline__ void weigh(const RouteArgs &a, int64_t t, const double *l, int e, int lane) {
   const double m = l[__shfl_sync(~0u, e, 0)];  // softmax: the first choice has the largest logit
   float w = 0.0f, z = 1.0f;
-  if (lane < a.top_k) w = a.sigmoid ? (float)(1.0 / (1.0 + exp(-l[e]))) : expf((float)(l[e] - m));
+  if (lane < a.top_k) w = a.sigmoid ? sigmoid((float)l[e]) : expf((float)(l[e] - m));
   if (a.renormalize) {
     z = w;
   } else if (!a.sigmoid) {
@@ -292,6 +302,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
   // entry other than 0, and the scores of the two tokens [2][experts]
   extern __shared__ double sums[];
   __shared__ int doubtful, list[2 * kMaxExperts];
+  __shared__ uint16_t candidates[2][kMaxExperts];
+  __shared__ double parts[kTcWarps][kTcWarps];
   const RouteArgs &a = p.a;
   const auto cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3, rank = (int)cluster.block_rank();
@@ -431,17 +443,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
 
   // ---- the choice of each of this CTA's tokens, by a warp
   uint64_t *const keys = reinterpret_cast<uint64_t *>(sums);  // (the sums are spent)
-  auto make_keys = [&] {
+  auto make_keys = [&](bool fp64) {
     for (int i = tid; i < 2 * a.experts; i += kTcThreads) {
       const int r = i >= a.experts, e = i - r * a.experts;
       if (rank + r * kTcCtas >= tokens) continue;
-      const double s = route_score(a, logits[i], e);
-      keys[i] = score_key(s);
-      scores[i] = (float)s;
+      const float s = route_score_fp32(a, logits[i], e);
+      keys[i] = score_key(fp64 ? route_score(a, logits[i], e) : (double)s);
+      scores[i] = s;
     }
     __syncthreads();
   };
-  make_keys();
+  make_keys(false);
   const int t = rank + warp * kTcCtas;  // this warp's token
   const bool has = warp < 2 && t < tokens;
   int e = 0;
@@ -453,40 +465,66 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
     for (int s = 0; s < p.splits; ++s) norm += token_part[s * kTcTokens + t], any |= token_any[s * kTcTokens + t];
     // (squares that may have underflowed bound nothing; a token of zeros has exact logits)
     norm = norm > 0x1p-100f ? sqrtf(norm) * kBand<R> : INFINITY;
-    // how far arithmetic may have moved an expert's score (a sigmoid's slope is at most 1/4; 2^-22 for roundings)
-    auto off = [&](int o, float s) { return norm * row_norm[o] * (a.sigmoid ? 0.25f : 1.0f) + 0x1p-22f * fabsf(s); };
+    // how far arithmetic may have moved an expert's score (a sigmoid's slope is at most 1/4)
+    auto off = [&](int o, float s) {
+      return norm * row_norm[o] * (a.sigmoid ? 0.25f : 1.0f) + 0x1p-21f * (fabsf(s) + (a.sigmoid ? 1.0f : 0.0f));
+    };
     // those that may be among the chosen reach up to where the last of these may have come from
     const float s0 = lane < a.top_k ? score[e] : INFINITY, low = lane < a.top_k ? s0 - off(e, s0) : INFINITY;
     float least = low;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(~0u, least, o));
+    // Candidates: an expert that is none lies below all of the chosen whatever
+    // arithmetic did, and so does a candidate that is near no other.
+    int n = 0;
     for (int o0 = 0; any && o0 < a.experts; o0 += 32) {
       const int o = o0 + lane;
-      const float so = o < a.experts ? score[o] : 0.0f, bo = o < a.experts ? off(o, so) : 0.0f;
-      for (uint32_t todo = __ballot_sync(~0u, o < a.experts && !(so + bo < least)); todo; todo &= todo - 1) {
-        // one of them: does another's range meet its own?
-        const int src = __ffs(todo) - 1, c = o0 + src;
-        const float sc = __shfl_sync(~0u, so, src), bc = __shfl_sync(~0u, bo, src);
-        bool near = false;
-        for (int q = lane; q < a.experts; q += 32) {
-          const float sq = score[q];
-          near |= q != c && !(fabsf(sq - sc) > bc + off(q, sq));
-        }
-        if (__any_sync(~0u, near) && lane == 0) list[atomicAdd(&doubtful, 1)] = warp * a.experts + c;
+      const float so = o < a.experts ? score[o] : 0.0f;
+      const bool is = o < a.experts && !(so + off(o, so) < least);
+      const uint32_t all = __ballot_sync(~0u, is);
+      if (is) candidates[warp][n + __popc(all & ((1u << lane) - 1u))] = (uint16_t)o;
+      n += __popc(all);
+    }
+    __syncwarp();
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int c = candidates[warp][min(i0 + lane, n - 1)];
+      const float sc = score[c], bc = off(c, sc);
+      bool near = n > 128;  // (too many to compare: all of them)
+      for (int q = 0; q < n && n <= 128; ++q) {
+        const int o = candidates[warp][q];
+        const float so = score[o];
+        near |= o != c && !(fabsf(so - sc) > bc + off(o, so));
       }
+      if (near && i0 + lane < n) list[atomicAdd(&doubtful, 1)] = warp * a.experts + c;
     }
   }
   __syncthreads();
   const int count = doubtful;
   if (count > 0) {  // those once more, exactly
-    for (int i = warp; i < count; i += kTcWarps) {
+    auto dot = [&](int i, int u0, int u1) {
       const int r = list[i] >= a.experts, c = list[i] - r * a.experts;
-      const double v = exact_dot(x + (int64_t)(rank + r * kTcCtas) * a.x_stride,
-                                 static_cast<const R *>(a.router) + (int64_t)c * a.router_stride, 0, eighths, lane);
-      if (lane == 0) logits[list[i]] = v;
+      return exact_dot(x + (int64_t)(rank + r * kTcCtas) * a.x_stride,
+                       static_cast<const R *>(a.router) + (int64_t)c * a.router_stride, u0, u1, lane);
+    };
+    if (count <= kTcWarps) {  // all warps on each
+      for (int i = 0; i < count; ++i) {
+        const double v = dot(i, warp * eighths / kTcWarps, (warp + 1) * eighths / kTcWarps);
+        if (lane == 0) parts[i][warp] = v;
+      }
+      __syncthreads();
+      if (tid < count) {
+        double v = 0.0;
+        for (int w = 0; w < kTcWarps; ++w) v += parts[tid][w];
+        logits[list[tid]] = v;
+      }
+    } else {
+      for (int i = warp; i < count; i += kTcWarps) {
+        const double v = dot(i, 0, eighths);
+        if (lane == 0) logits[list[i]] = v;
+      }
     }
     __syncthreads();
-    make_keys();
+    make_keys(true);
     if (has) e = choose(a, keys + (size_t)warp * a.experts, lane);
   }
   if (has) weigh(a, t0 + t, logits + (size_t)warp * a.experts, e, lane);
@@ -502,6 +540,8 @@ auto with_route(bool fp32, int g, F f) {
   };
   return fp32 ? pick(0.0f) : pick(__nv_bfloat16());
 }
+
+int g_route_ctas = 8;  // of a cluster for few tokens
 
 size_t route_smem(const RouteLaunch &p, int g) {
   return ((size_t)std::max(p.splits * p.per * g, p.a.experts) + (size_t)p.a.experts) * sizeof(double);
@@ -520,13 +560,33 @@ cudaError_t prepare_route_kernels() {
   const int most = (128 * kTcTokens + 4 * kMaxExperts) * 8 + (3 * kMaxExperts + 128 + kTcWarps * 2 * kTcTokens) * 4;
   cudaError_t e = cudaFuncSetAttribute(k_moe_route_tc<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_moe_route_tc<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  return e;
+  for (const bool fp32 : {false, true})
+    if (e == cudaSuccess)
+      e = with_route(fp32, 1, [](auto *k) { return cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kRouteMaxCtas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kRouteMaxCtas);
+  cfg.blockDim = dim3(kRouteThreads);
+  cfg.dynamicSmemBytes = 48 * 1024;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, k_moe_route<float, 1>, &cfg) != cudaSuccess) cudaGetLastError();  // (8 then)
+  g_route_ctas = clusters > 0 ? kRouteMaxCtas : 8;
+  return cudaSuccess;
 }
 
 cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st) {
   RouteLaunch p = {a, 0, 1};
-  // The tensor cores where they fill their tiles.  Measured (us): XXX
-  const bool tc = a.tokens >= 32 && a.experts >= 64;
+  // The tensor cores where they fill their tiles.  Measured (us, then the other kernel's):
+  // 7168, 256 experts: 16 tokens 30 and 33, 64 33 and 53, 256 39 and 266; 2048, 128
+  // experts: 31 tokens 15 and 11, 64 17 and 15, 128 15 and 20; 4096, 60 experts: 64 tokens
+  // 16 and 15, 128 12 and 20; 4096, 8 experts: 64 tokens 11 and 10, 128 11 and 11, 256 14 and 28.
+  const bool tc = a.tokens >= 128 || (a.tokens >= 16 && a.tokens * a.experts >= 8192);
   int g = kTcTokens, ctas = kTcCtas, threads = kTcThreads;
   p.per = (a.experts + ctas - 1) / ctas;
   if (tc) {
@@ -535,6 +595,9 @@ cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st) {
     // as few tokens per cluster as one wave of CTAs allows: a router row's way
     // through L2 is shared by a cluster's tokens, but a lane's work is theirs together
     g = 1, threads = kRouteThreads;
+    // (1 token 7168, 256 experts: 23 us with clusters of 8, 14 with 16; 2048, 128 experts: 7.9 and 6.6)
+    if (a.experts >= 32 && a.tokens * kRouteMaxCtas <= sms) ctas = g_route_ctas;
+    p.per = (a.experts + ctas - 1) / ctas;
     p.splits = std::max(1, std::min<int>(kRouteWarps / p.per, (int)(a.hidden / 256)));
     while (g < 8 && (a.tokens + g - 1) / g * ctas > 2 * sms) g *= 2;
   }
