@@ -107,7 +107,7 @@ struct MoePlan {
   uint16_t *order;  // [pairs]
   int *count, *end; // [experts]: pairs of an expert, and where they end (unused with few pairs)
   uint16_t *named;  // [pairs]: their experts
-  uint16_t *found;  // [pairs]: by expert, as they came
+  uint16_t *found;  // [pairs]: by expert, as they came (where that is not yet the order)
   int *total;       // jobs
 };
 
@@ -149,8 +149,10 @@ __device__ void moe_plan(const MoeLaunch &p, const MoePlan &o, int tid, int thre
   }
   __syncthreads();
   int total = 0, named = 0, cost = 0;  // jobs; pairs that have an expert; the jobs' cost
+  bool many = false;                   // an expert of this thread has several jobs
   for (int e0 = 0; e0 < E; e0 += threads) {
     const int e = e0 + tid, n = e < E ? o.count[e] : 0, j = (n + N - 1) / N;
+    many |= j > 1;
     const int full = moe_job_cost(p, N), c = j > 0 ? (j - 1) * full + moe_job_cost(p, n - (j - 1) * N) : 0;
     int sn = n, sj = j, sc = c;  // inclusive sums over the warp, then over the warps
 #pragma unroll
@@ -176,19 +178,23 @@ __device__ void moe_plan(const MoeLaunch &p, const MoePlan &o, int tid, int thre
     __syncthreads();
   }
   if (tid == 0) o.start[total] = cost, *o.total = total;
+  // (in an expert's only job a pair's place just decides which column of an MMA it takes)
+  const bool several = __syncthreads_or(many);
+  uint16_t *to = several ? o.found : o.order;
   for (int i = tid; i < p.pairs; i += threads) {
     const int e = o.named[i];
-    if (e != 0xFFFF) o.found[atomicAdd(&o.end[e], 1)] = (uint16_t)i;
+    if (e != 0xFFFF) to[atomicAdd(&o.end[e], 1)] = (uint16_t)i;
   }
+  if (!several) return;
   __syncthreads();
   for (int q = tid; q < named; q += threads) {
     const int i = o.found[q], e = o.named[i], n = o.count[e], b = o.end[e] - n;
-    int to = q;
-    if (n > N) {  // (in one job a pair's place only decides which column of an MMA it takes)
-      to = b;
-      for (int f = b; f < b + n; ++f) to += o.found[f] < i;
+    int at = q;
+    if (n > N) {
+      at = b;
+      for (int f = b; f < b + n; ++f) at += o.found[f] < i;
     }
-    o.order[to] = (uint16_t)i;
+    o.order[at] = (uint16_t)i;
   }
 }
 
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   // Rows of codes lie in whole 128-byte lines of shared memory: where they lay across
   // two, each copy took four times the requests to L2 and 2.5 times the sectors.
   extern __shared__ __align__(128) uint4 dsm[];
-  __shared__ int scan[3][kMoeMaxWarps], jobs_there;
+  __shared__ int scan[3][kMoeMaxWarps], jobs_there, bound[2][2];
   const MoeArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
   const int threads = blockDim.x, warps = threads >> 5;
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
     pdl_wait();
     pdl_launch_dependents();
   }
-  if (tid < 64) xtop[tid] = INT_MIN;
+  if (tid < 64) xtop[tid] = DOWN ? INT_MAX : INT_MIN;
   if (p.pairs <= kMoeFewPairs) {
     if (warp == 0) moe_plan_few(p, o, lane);
   } else {
@@ -241,22 +247,22 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
 
   // ---- this CTA's tiles: the job and the tile at two places of the total cost
   const int total = jobs_there, cost = o.start[total];
-  auto place = [&](uint32_t share, int *job, int *tile) {
+  {
     const uint32_t whole = (uint32_t)cost / gridDim.x, rest = (uint32_t)cost - whole * gridDim.x;
-    const int at = (int)(share * whole + share * rest / gridDim.x);  // (both factors below 2^16)
-    int lo = 0, hi = total;
-    while (lo < hi) {  // the last job that starts at `at` or before, or `total`
-      const int mid = (lo + hi + 1) / 2;
-      if (o.start[mid] <= at) lo = mid;
-      else hi = mid - 1;
+    const uint32_t at0 = blockIdx.x * whole + blockIdx.x * rest / gridDim.x,  // (both factors below 2^16)
+                   at1 = (blockIdx.x + 1) * whole + (blockIdx.x + 1) * rest / gridDim.x;
+    for (int j = tid; j <= total; j += threads) {  // one j holds each place
+      const uint32_t from = (uint32_t)o.start[j], to = j < total ? (uint32_t)o.start[j + 1] : ~0u;
+      const int c = j < total ? moe_tile_cost(p, (int)(o.jobs[j] & 63u)) : 1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t at = i ? at1 : at0;
+        if (from <= at && at < to) bound[i][0] = j, bound[i][1] = j < total ? max((int)(at - from) - p.job_cost, 0) / c : 0;
+      }
     }
-    *job = lo;
-    const int n = lo < total ? (int)(o.jobs[lo] & 63u) : 1;
-    *tile = lo < total ? max(at - o.start[lo] - p.job_cost, 0) / moe_tile_cost(p, n) : 0;
-  };
-  int j0, t0, j1, t1;
-  place(blockIdx.x, &j0, &t0);
-  place(blockIdx.x + 1, &j1, &t1);
+    __syncthreads();
+  }
+  int j0 = bound[0][0], t0 = bound[0][1], j1 = bound[1][0], t1 = bound[1][1];
   if (j0 == j1 && t0 == t1) {
     if constexpr (DOWN) {
       pdl_wait();
@@ -400,16 +406,25 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
     } else {
       asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth) : "memory");
     }
-    if constexpr (DOWN) {
-      __syncthreads();
-      for (int n = warp; n < np; n += warps) {
-        int low = INT8_MAX;
-        for (int u = lane; u < wide; u += 32) low = min(low, (int)ups[n * p.up_pitch + u]);
-        low = __reduce_min_sync(~0u, low);
-        if (lane == 0) xtop[par * 32 + n] = low;
+    if constexpr (DOWN) {  // (a thread reads what it copied itself, here and below)
+      const int pieces = p.up_pitch / 16;
+      for (int i = tid; i < np * pieces; i += threads) {
+        const int n = i / pieces, q = i - n * pieces;
+        const uint4 r = *reinterpret_cast<const uint4 *>(ups + n * p.up_pitch + 16 * q);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        uint32_t low = 0x7F7F7F7Fu;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int valid = wide - 16 * q - 4 * b;  // bytes of this word
+          const uint32_t mask = valid >= 4 ? 0u : valid <= 0 ? ~0u : ~0u << 8 * valid;
+          low = __vmins4(low, (w[b] & ~mask) | (0x7F7F7F7Fu & mask));
+        }
+        low = __vmins4(low, low >> 16 | 0x7F7F0000u);
+        low = __vmins4(low, low >> 8 | 0x7F7F7F00u);
+        atomicMin(&xtop[par * 32 + n], (int)(int8_t)(low & 0xFFu));
       }
     } else {
-      for (int i = warp; i < np * nk; i += warps) {  // (a thread reads the units that it copied)
+      for (int i = warp; i < np * nk; i += warps) {
         const int n = i / nk, u = (i - n * nk) * 32 + lane;
         const uint4 r = *unit_at(n, u);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -440,7 +455,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       }
       *to = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (tid < 32) xtop[(par ^ 1) * 32 + tid] = INT_MIN;
+    if (tid < 32) xtop[(par ^ 1) * 32 + tid] = DOWN ? INT_MAX : INT_MIN;
     __syncthreads();
 
     // ---- the run, with as many n-tiles as the job's pairs fill
