@@ -78,13 +78,22 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 // into [2^14, 2^15); for an infinity or a NaN one that leaves it what it is.
 __device__ __forceinline__ int f16_up(unsigned top) { return min(14 + 127 - (int)(top >> 23), 126); }
 
-__host__ __device__ constexpr int moe_slot(bool wide) { return wide ? 2304 : 2560; }  // a unit's codes and scales
+// How a unit's codes and scales reach shared memory, by what their rows' addresses allow:
+//   kWide   rows of codes are whole multiples of 16 bytes and of scales of 4, and so
+//           aligned: 16 bytes and a word at a time;
+//   kOdd    a tile's codes begin on 16 bytes, but its odd rows perhaps 8 behind: each
+//           row's 16-byte pieces from the last such boundary before it, nine instead
+//           of eight; scales on any byte, in the two words that hold a lane's four;
+//   kAny    codes on any 8 bytes: 8 at a time, which takes 1.7 times as long as kOdd.
+enum MoeLoads { kWide = 0, kOdd = 1, kAny = 2 };
+__host__ __device__ constexpr int moe_code_slot(int loads) { return loads == kOdd ? 16 * 144 : 16 * 128; }
+__host__ __device__ constexpr int moe_slot(int loads) { return moe_code_slot(loads) + (loads == kWide ? 256 : 512); }
 __host__ __device__ constexpr int moe_up_pitch(int64_t cols) { return (int)((cols / 8 + 15) / 16 * 16); }
 // Shared memory: the vectors (with h's exponents), the warps' units in flight
 // and partial sums, the vectors' scales, the plan.
-__host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, bool wide, int experts, int pairs) {
+__host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, int loads, int experts, int pairs) {
   return (cols + 255) / 256 * 512 * group + (down ? (int64_t)group * moe_up_pitch(cols) : 0) +
-         (int64_t)warps * (kMoeDepth * moe_slot(wide) + (group + 7) / 8 * 512) + 512 +
+         (int64_t)warps * (kMoeDepth * moe_slot(loads) + (group + 7) / 8 * 512) + 512 +
          (pairs > kMoeFewPairs ? (int64_t)experts * 8 : 0) + ((int64_t)pairs + 1) * 14 + 64;
 }
 
@@ -92,8 +101,8 @@ __host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool dow
 __device__ __forceinline__ uint32_t moe_job(int expert, int at, int n) { return (uint32_t)expert << 17 | (uint32_t)at << 6 | (uint32_t)n; }
 static_assert(kMaxExperts <= 1024 && kMoeSlicePairs <= 2048, "a job's fields");
 // A tile's cost: its weights' way, and a part of that for each further n-tile of pairs.
-// Measured: 61 tokens 2048 x 768, 8 of 128 (wide copies): a tile of 9 .. 16 pairs took
-// 1.44 times one of up to 8; 256 tokens 2064 x 1424, 6 of 60 (narrow ones): 1.2, and
+// Measured: 61 tokens 2048 x 768, 8 of 128 (kWide): a tile of 9 .. 16 pairs took
+// 1.44 times one of up to 8; 256 tokens 2064 x 1424, 6 of 60 (kAny): 1.2, and
 // 1.4 with a third n-tile.
 __device__ __forceinline__ int moe_tile_cost(const MoeLaunch &p, int pairs) { return 8 + p.more_cost * ((pairs - 1) / 8); }
 __device__ __forceinline__ int moe_job_cost(const MoeLaunch &p, int pairs) { return p.job_cost + p.tiles * moe_tile_cost(p, pairs); }
@@ -199,10 +208,9 @@ __device__ void moe_plan(const MoeLaunch &p, const MoePlan &o, int tid, int thre
 }
 
 // DOWN: the second product (h -> part), else the first (x -> h).  GATED: the
-// first product's tiles hold 8 rows of gate and 8 of up.  WIDE: rows of codes
-// are whole multiples of 16 bytes and of scales of 4, and so aligned.  NT:
+// first product's tiles hold 8 rows of gate and 8 of up.  LOADS: MoeLoads.  NT:
 // n-tiles that the group's pairs fill at most.
-template <int NT, bool DOWN, bool GATED, bool WIDE>
+template <int NT, bool DOWN, bool GATED, int LOADS>
 __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_constant__ MoeLaunch p) {
   // Rows of codes lie in whole 128-byte lines of shared memory: where they lay across
   // two, each copy took four times the requests to L2 and 2.5 times the sectors.
@@ -212,7 +220,8 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
   const int threads = blockDim.x, warps = threads >> 5;
   const int nk = p.steps, N = p.group, NB = (N + 7) / 8;
-  constexpr int kSlot = moe_slot(WIDE);
+  constexpr bool WIDE = LOADS == kWide;
+  constexpr int kSlot = moe_slot(LOADS), kScales = moe_code_slot(LOADS);  // of a slot: its bytes, where its scales begin
   uint4 *xs = dsm;                                                        // [nk][8][N][4] 16-byte units of f16
   uint4 *slots = dsm + (size_t)nk * 32 * N;                               // [warps][depth][kSlot / 16]: units in flight
   float4 *own = reinterpret_cast<float4 *>(slots + warps * kMoeDepth * (kSlot / 16));  // [warps][NB][32]
@@ -288,15 +297,20 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   // words that hold them.
   const int64_t nblk = p.cols / 16, pitch = 8 * nblk;     // blocks and code bytes of a row
   constexpr int kTileRows = GATED && !DOWN ? 8 : 16;      // rows between tiles
-  constexpr int kPiece = WIDE ? 16 : 8, kRows = 4 * kPiece / 16, kCopies = 16 / kRows;  // of a copy by the warp
+  constexpr int kPiece = LOADS == kAny ? 8 : 16, kRows = 4 * kPiece / 16, kCopies = 16 / kRows;  // of a copy by the warp
   const int row0 = lane / (32 / kRows), byte0 = lane % (32 / kRows) * kPiece;
   // bytes of the last step's piece and scales (past the end come zeros, from no address)
   const int code_tail = max(0, min(kPiece, (int)(pitch - (int64_t)(nk - 1) * 128) - byte0));
   const int scale_tail = max(0, min(4, (int)(nblk - (int64_t)(nk - 1) * 16) - 4 * cq));
-  const uint32_t slot_at = static_cast<uint32_t>(__cvta_generic_to_shared(slots)), scale_to = slot_at + 2048 + lane * 4;
+  const uint32_t slot_at = static_cast<uint32_t>(__cvta_generic_to_shared(slots)), scale_to = slot_at + kScales + lane * 4;
   // the lane's place in rows 0 .. 7: copies 0 and 1 of the wide form's two
   const uint32_t code_to0 = slot_at + row0 * 128 + (((byte0 >> 4) ^ row0) << 4) + (byte0 & 15),
                  code_to1 = slot_at + (row0 + 4) * 128 + (((byte0 >> 4) ^ (row0 + 4)) << 4);
+  // kOdd: piece i of the lane is 16 bytes of row odd_row(i) from `odd_from`, of which
+  // 8 may belong to the row before; `back`: how far behind a boundary odd rows begin
+  const int back = LOADS == kOdd && (pitch & 8) ? 8 : 0;
+  auto odd_row = [&](int i) { return (i * 32 + lane) / 9; };
+  auto odd_chunk = [&](int i) { return (i * 32 + lane) % 9; };
   struct {
     int j, k, left;     // the next unit's job and step; units left of the run
     uint32_t at;        // its scales' offset in the matrix (and an eighth of its codes')
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
       for (int h = 0; h < 2; ++h) {
         const MoeMatrix &m = DOWN ? a.down : GATED && h == 0 ? a.gate : a.up;
         const int64_t row = GATED && !DOWN ? 0 : 8 * h;
-        next.code[h] = m.codes + e * m.code_stride + (row + row0) * pitch + byte0;
+        next.code[h] = m.codes + e * m.code_stride + (LOADS == kOdd ? row * pitch : (row + row0) * pitch + byte0);
         next.scale[h] = m.scales + e * m.scale_stride + (row + g) * nblk + 4 * cq;
       }
     }
@@ -324,17 +338,34 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
     if (next.left == 0) open_run();
     if (next.left > 0) {
       const bool last = next.k == nk - 1;
-      const int cb = last ? code_tail : kPiece, sb = last ? scale_tail : 4;
+      const int sb = last ? scale_tail : 4;
+      if constexpr (LOADS == kOdd) {
+        const int row_left = last ? (int)(pitch - (int64_t)(nk - 1) * 128) : 128;  // bytes of a row from here
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const uint8_t *from = next.code[i / (kCopies / 2)] + (uint64_t)next.at * 8 + (i % (kCopies / 2)) * rows4;
-        if (WIDE) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                       ::"r"((i & 1 ? code_to1 : code_to0) + (i >> 1) * 1024 + fill), "l"(from), "r"(cb) : "memory");
-        } else {
-          const int r = i * kRows + row0;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
-                       ::"r"(slot_at + r * 128 + (((byte0 >> 4) ^ (r & 7)) << 4) + (byte0 & 15) + fill), "l"(from), "r"(cb) : "memory");
+        for (int i = 0; i < 5; ++i) {
+          const int r = odd_row(i), from = odd_chunk(i) * 16 - (r & 1 ? back : 0);  // counted from the row's place here
+          if (i < 4 || r < 16) {
+            // (pieces that begin past the row's end are zeros; one that reaches past it takes in the next row's
+            // bytes, which there are: such a row is an even one)
+            const int bytes = from < row_left ? 16 : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"(slot_at + r * 144 + odd_chunk(i) * 16 + fill),
+                           "l"((r >= 8 ? next.code[1] : next.code[0]) + (int64_t)next.at * 8 + (r & 7) * (int)pitch + from), "r"(bytes) : "memory");
+          }
+        }
+      } else {
+        const int cb = last ? code_tail : kPiece;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const uint8_t *from = next.code[i / (kCopies / 2)] + (uint64_t)next.at * 8 + (i % (kCopies / 2)) * rows4;
+          if (WIDE) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"((i & 1 ? code_to1 : code_to0) + (i >> 1) * 1024 + fill), "l"(from), "r"(cb) : "memory");
+          } else {
+            const int r = i * kRows + row0;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                         ::"r"(slot_at + r * 128 + (((byte0 >> 4) ^ (r & 7)) << 4) + (byte0 & 15) + fill), "l"(from), "r"(cb) : "memory");
+          }
         }
       }
 #pragma unroll
@@ -529,7 +560,8 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
         xl[nt] = xs + min(8 * nt + g, np - 1) * 4 + cq;
         xk[nt] = xl[nt] + ck * 32 * N;
       }
-      const int chunk0 = g * 8 + ((2 * cq) ^ g), chunk1 = g * 8 + ((2 * cq + 1) ^ g);
+      [[maybe_unused]] const int chunk0 = g * 8 + ((2 * cq) ^ g), chunk1 = g * 8 + ((2 * cq + 1) ^ g);
+      [[maybe_unused]] const int odd_at = g * 144 + (g & 1 ? back : 0) + 32 * cq;
       for (int left = r.u1 - r.u0; left > 0; --left) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kMoeDepth - 1) : "memory");
         __syncwarp();
@@ -538,7 +570,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
         uint32_t sc[2][2][2];  // [half][row][block]: f16 pairs {Delta, Delta}
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t *words = reinterpret_cast<const uint32_t *>(here + 128) + lane;
+          const uint32_t *words = reinterpret_cast<const uint32_t *>(here + kScales / 16) + lane;
           uint32_t word;
           if constexpr (WIDE) {
             word = words[h * 32];
@@ -559,7 +591,14 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint4 c0 = here[half ? chunk1 : chunk0], c1 = here[64 + (half ? chunk1 : chunk0)];
+          uint4 c0, c1;
+          if constexpr (LOADS == kOdd) {
+            const uint2 *from = reinterpret_cast<const uint2 *>(reinterpret_cast<const uint8_t *>(here) + odd_at) + 2 * half;
+            const uint2 l0 = from[0], h0 = from[1], l1 = from[8 * 18], h1 = from[8 * 18 + 1];
+            c0 = make_uint4(l0.x, l0.y, h0.x, h0.y), c1 = make_uint4(l1.x, l1.y, h1.x, h1.y);
+          } else {
+            c0 = here[half ? chunk1 : chunk0], c1 = here[64 + (half ? chunk1 : chunk0)];
+          }
           const uint32_t cw[2][4] = {{c0.x, c0.y, c0.z, c0.w}, {c1.x, c1.y, c1.z, c1.w}};
 #pragma unroll
           for (int jj = 0; jj < 4; ++jj) {  // a word of codes: 8 columns, two k-steps
@@ -661,23 +700,23 @@ __global__ void __launch_bounds__(256) k_moe_join(const __grid_constant__ MoeLau
 namespace {
 
 // Pairs of a job at most, of those wanted, for the vectors' room in shared memory.
-int moe_group(int wanted, int64_t cols, bool down, int warps, bool wide, int experts, int pairs, int64_t room) {
+int moe_group(int wanted, int64_t cols, bool down, int warps, int loads, int experts, int pairs, int64_t room) {
   for (int n = wanted; n > 0; --n)
-    if (moe_smem(n, cols, down, warps, wide, experts, pairs) <= room) return n;
+    if (moe_smem(n, cols, down, warps, loads, experts, pairs) <= room) return n;
   return 0;
 }
 
 template <typename F>
-auto with_kernel(int nt, bool down, bool gated, bool wide, F f) {
-  auto pick_wide = [&](auto w, auto n) {
-    constexpr bool W = decltype(w)::value;
-    constexpr int N = decltype(n)::value;
-    return down ? f(k_moe<N, true, false, W>) : gated ? f(k_moe<N, false, true, W>) : f(k_moe<N, false, false, W>);
+auto with_kernel(int nt, bool down, bool gated, int loads, F f) {
+  auto pick = [&](auto l, auto n) {
+    constexpr int L = decltype(l)::value, N = decltype(n)::value;
+    return down ? f(k_moe<N, true, false, L>) : gated ? f(k_moe<N, false, true, L>) : f(k_moe<N, false, false, L>);
   };
-  auto pick_nt = [&](auto w) {
-    return nt == 1 ? pick_wide(w, std::integral_constant<int, 1>()) : pick_wide(w, std::integral_constant<int, 4>());
+  auto pick_nt = [&](auto l) {
+    return nt == 1 ? pick(l, std::integral_constant<int, 1>()) : pick(l, std::integral_constant<int, 4>());
   };
-  return wide ? pick_nt(std::true_type()) : pick_nt(std::false_type());
+  return loads == kWide ? pick_nt(std::integral_constant<int, kWide>())
+         : loads == kOdd ? pick_nt(std::integral_constant<int, kOdd>()) : pick_nt(std::integral_constant<int, kAny>());
 }
 
 template <typename K>
@@ -700,19 +739,20 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
   p.cols = down ? a.inner : a.hidden;
   p.steps = (int)((p.cols + 255) / 256);
   p.tiles = (int)(down ? a.hidden / 16 : a.gated ? a.inner / 8 : a.inner / 16);
-  auto wide_matrix = [&](const MoeMatrix &m) {
-    return ((reinterpret_cast<uintptr_t>(m.codes) | m.code_stride) % 16 | (reinterpret_cast<uintptr_t>(m.scales) | m.scale_stride) % 4) == 0;
+  auto loads_of = [&](const MoeMatrix &m) -> int {
+    if ((reinterpret_cast<uintptr_t>(m.codes) | m.code_stride) % 16) return kAny;
+    return p.cols % 64 || (reinterpret_cast<uintptr_t>(m.scales) | m.scale_stride) % 4 ? kOdd : kWide;
   };
-  const bool wide = p.cols % 64 == 0 && (down ? wide_matrix(a.down) : wide_matrix(a.up) && (!a.gated || wide_matrix(a.gate)));
+  const int loads = down ? loads_of(a.down) : std::max(loads_of(a.up), a.gated ? loads_of(a.gate) : (int)kWide);
   // Pairs that a job should take: few experts have more than three times the mean and four.
   const int wanted = std::min({p.pairs, 32, 4 + 3 * p.pairs / a.experts});
   p.job_cost = std::min(576 / p.steps, p.tiles);
-  p.more_cost = wide ? 3 : 2;
+  p.more_cost = loads == kWide ? 3 : 2;
   // Little work: one small CTA per SM, so that the next launch's CTAs find room beside
   // it (1 token 2048 x 768, 8 of 128: 22.1 -> 20.6 us).
   const bool little = (int64_t)std::min(p.pairs, a.experts) * p.tiles * p.steps <= (int64_t)64 * sms;
   int warps = 8, ctas = little ? sms : 2 * sms;
-  auto fit = [&](int64_t room) { p.group = moe_group(wanted, p.cols, down, warps, wide, a.experts, p.pairs, room); };
+  auto fit = [&](int64_t room) { p.group = moe_group(wanted, p.cols, down, warps, loads, a.experts, p.pairs, room); };
   fit(kMoeHalfSmem);
   if (p.group < wanted) {
     warps = kMoeMaxWarps, ctas = sms;
@@ -722,8 +762,8 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
     warps = 8;
     fit(kMoeSmem);
   }
-  const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, wide, a.experts, p.pairs);
-  return with_kernel(p.group <= 8 ? 1 : 4, down, a.gated, wide,
+  const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, loads, a.experts, p.pairs);
+  return with_kernel(p.group <= 8 ? 1 : 4, down, a.gated, loads,
                      [&](auto *k) { return launch_dependent(k, ctas, warps * 32, smem, p, st); });
 }
 
@@ -733,8 +773,8 @@ size_t moe_up_bytes(int64_t inner, int pairs) { return ((size_t)pairs * moe_up_p
 }  // namespace
 
 bool moe_fits(int64_t hidden, int64_t inner, int experts, int pairs) {
-  return moe_group(1, hidden, false, 8, false, experts, pairs, kMoeSmem) > 0 &&
-         moe_group(1, inner, true, 8, false, experts, pairs, kMoeSmem) > 0;
+  return moe_group(1, hidden, false, 8, kOdd, experts, pairs, kMoeSmem) > 0 &&
+         moe_group(1, inner, true, 8, kOdd, experts, pairs, kMoeSmem) > 0;
 }
 
 size_t moe_workspace_bytes(int64_t hidden, int64_t inner, int pairs) {
@@ -760,9 +800,9 @@ cudaError_t prepare_moe_kernels() {
   cudaError_t e = cudaSuccess;
   for (int nt : {1, 4})
     for (int form : {0, 1, 2})
-      for (bool wide : {false, true})
+      for (int loads : {kWide, kOdd, kAny})
         if (e == cudaSuccess)
-          e = with_kernel(nt, form == 2, form == 1, wide,
+          e = with_kernel(nt, form == 2, form == 1, loads,
                           [](auto *k) { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem); });
   return e;
 }
