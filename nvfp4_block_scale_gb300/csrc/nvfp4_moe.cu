@@ -131,8 +131,8 @@ __device__ void moe_plan_few(const MoeLaunch &p, const MoePlan &o, int lane) {
   const bool first = there && pos % N == 0;
   const int cost = first ? moe_job_cost(p, n) : 0;
   int rank = 0, job = 0, start = 0;
-#pragma unroll
-  for (int l = 0; l < 32; ++l) {
+#pragma unroll 4
+  for (int l = 0; l < p.pairs; ++l) {
     const int el = __shfl_sync(~0u, e, l), cl = __shfl_sync(~0u, cost, l);
     if (el < e || (el == e && l < lane)) ++rank, job += cl > 0, start += cl;
   }
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   __shared__ int scan[3][kMoeMaxWarps], jobs_there, bound[2][2];
   const MoeArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
-  const int threads = blockDim.x, warps = threads >> 5;
+  const int threads = blockDim.x, warps = threads >> 5, warps_bits = 31 - __clz(warps);  // (8 or 16)
   const int nk = p.steps, N = p.group, NB = (N + 7) / 8;
   constexpr bool WIDE = LOADS == kWide;
   constexpr int kSlot = moe_slot(LOADS), kScales = moe_code_slot(LOADS);  // of a slot: its bytes, where its scales begin
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   };
   auto run_of = [&](int j, int w) {
     const int from = j == j0 ? t0 : 0, units = ((j == j1 ? t1 : p.tiles) - from) * nk;
-    return Run{from, w * units / warps, (w + 1) * units / warps};
+    return Run{from, w * units >> warps_bits, (w + 1) * units >> warps_bits};
   };
   // Units go to the ring kMoeDepth ahead.  Codes: 16 rows of 128 bytes, the 16-byte
   // chunk c of row r at place c ^ (r % 8), so that both the copies (full rows) and
@@ -659,42 +659,50 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
 }
 
 // y = residual + the sum of a token's slots, in slot order; four columns a thread.
+// What was there before the products is read before they end.
 __global__ void __launch_bounds__(256) k_moe_join(const __grid_constant__ MoeLaunch p) {
   const MoeArgs &a = p.a;
-  pdl_launch_dependents();
-  pdl_wait();
   const int64_t quads = a.hidden / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= quads * a.tokens) return;
+  const bool mine = i < quads * a.tokens;
   const int64_t t = i / quads, c = (i - t * quads) * 4;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s0 = 0; s0 < a.top_k; s0 += 8) {  // eight slots' loads at a time
-    float w[8];
-    float4 o[8];
-    bool there[8];
+  constexpr int kSlots = 8;  // slots read at a time
+  float w[kSlots];
+  bool there[kSlots];
+  auto slots = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t at = t * a.top_k + min(s0 + i, a.top_k - 1);
-      const int e = a.ids[at];
-      there[i] = s0 + i < a.top_k && e >= 0 && e < a.experts;
-      w[i] = a.weights[at];
-      o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (there[i]) o[i] = *reinterpret_cast<const float4 *>(p.part + at * a.hidden + c);
+    for (int s = 0; s < kSlots; ++s) {
+      const int64_t at = t * a.top_k + min(s0 + s, a.top_k - 1);
+      const int e = mine ? a.ids[at] : -1;
+      there[s] = s0 + s < a.top_k && e >= 0 && e < a.experts;
+      w[s] = mine ? a.weights[at] : 0.0f;
+    }
+  };
+  slots(0);
+  float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(a.residual);
+  if (res && mine) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) r[b] = __bfloat162float(res[t * a.residual_stride + c + b]);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!mine) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < a.top_k; s0 += kSlots) {
+    if (s0 > 0) slots(s0);
+    float4 o[kSlots];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      o[s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (there[s]) o[s] = *reinterpret_cast<const float4 *>(p.part + (t * a.top_k + s0 + s) * a.hidden + c);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (there[i]) v[0] = fmaf(w[i], o[i].x, v[0]), v[1] = fmaf(w[i], o[i].y, v[1]), v[2] = fmaf(w[i], o[i].z, v[2]), v[3] = fmaf(w[i], o[i].w, v[3]);
-  }
-  const __nv_bfloat16 *res = static_cast<const __nv_bfloat16 *>(a.residual);
-  if (res) {
-    __nv_bfloat16 rv[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) rv[b] = res[t * a.residual_stride + c + b];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) v[b] += __bfloat162float(rv[b]);
+    for (int s = 0; s < kSlots; ++s)
+      if (there[s]) v[0] = fmaf(w[s], o[s].x, v[0]), v[1] = fmaf(w[s], o[s].y, v[1]), v[2] = fmaf(w[s], o[s].z, v[2]), v[3] = fmaf(w[s], o[s].w, v[3]);
   }
   __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + t * a.y_stride + c;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) y[b] = __float2bfloat16(v[b]);
+  for (int b = 0; b < 4; ++b) y[b] = __float2bfloat16(v[b] + r[b]);
 }
 
 namespace {
