@@ -63,6 +63,7 @@ struct MoeLaunch {
   int tiles;          // of a job
   int job_cost;       // of a job besides its tiles: its vectors' way, mostly (3.5 us of 32 at 61 tokens)
   int more_cost;      // of a tile for each further n-tile, in eighths of a tile's
+  uint32_t share;     // of the cost, of a CTA: 2^32 / CTAs
   int64_t cols;       // of this launch's matrices
 };
 
@@ -257,9 +258,9 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   // ---- this CTA's tiles: the job and the tile at two places of the total cost
   const int total = jobs_there, cost = o.start[total];
   {
-    const uint32_t whole = (uint32_t)cost / gridDim.x, rest = (uint32_t)cost - whole * gridDim.x;
-    const uint32_t at0 = blockIdx.x * whole + blockIdx.x * rest / gridDim.x,  // (both factors below 2^16)
-                   at1 = (blockIdx.x + 1) * whole + (blockIdx.x + 1) * rest / gridDim.x;
+    // (p.share: 2^32 / CTAs)
+    const uint32_t at0 = __umulhi(blockIdx.x * p.share, (uint32_t)cost),
+                   at1 = blockIdx.x + 1 == gridDim.x ? (uint32_t)cost : __umulhi((blockIdx.x + 1) * p.share, (uint32_t)cost);
     for (int j = tid; j <= total; j += threads) {  // one j holds each place
       const uint32_t from = (uint32_t)o.start[j], to = j < total ? (uint32_t)o.start[j + 1] : ~0u;
       const int c = j < total ? moe_tile_cost(p, (int)(o.jobs[j] & 63u)) : 1;
@@ -392,6 +393,15 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   const int wide = (int)(p.cols / 8);  // units of a vector (nk * 32 with those past the end)
   // unit u: step u / 32, lane quarter (u / 8) % 4, pair of k-steps u % 8
   auto unit_at = [&](int n, int u) { return xs + (((u >> 5) * 8 + (u & 7)) * N + n) * 4 + ((u >> 3) & 3); };
+  // this warp's chunks of 32 units of n vectors: (vector, chunk)
+  auto chunks = [&](int count, auto f) {
+    int n = warp / nk, c = warp - n * nk;
+    while (n < count) {
+      f(n, c * 32 + lane);
+      c += warps;
+      while (c >= nk) c -= nk, ++n;
+    }
+  };
   auto take_in = [&](uint32_t job) {
     const int np = (int)(job & 63u);
     const uint16_t *pair = o.order + (job >> 6 & 2047u);
@@ -404,14 +414,14 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
                      "l"(p.h_up + (int64_t)pair[n] * p.up_pitch + 16 * q) : "memory");
       }
     }
-    for (int i = warp; i < np * nk; i += warps) {
-      const int n = i / nk, u = (i - n * nk) * 32 + lane, from = pair[n];
+    chunks(np, [&](int n, int u) {
+      const int from = pair[n];
       const void *v = DOWN ? (const void *)(p.h + (int64_t)from * p.cols)
                            : (const void *)(static_cast<const __nv_bfloat16 *>(a.x) + (int64_t)(from / a.top_k) * a.x_stride);
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                    ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(unit_at(n, u)))),
                    "l"(static_cast<const uint4 *>(v) + (u < wide ? u : 0)), "r"(u < wide ? 16 : 0) : "memory");
-    }
+    });
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // (x before the weights, which take longer; h is not there yet)
@@ -455,8 +465,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
         atomicMin(&xtop[par * 32 + n], (int)(int8_t)(low & 0xFFu));
       }
     } else {
-      for (int i = warp; i < np * nk; i += warps) {
-        const int n = i / nk, u = (i - n * nk) * 32 + lane;
+      chunks(np, [&](int n, int u) {
         const uint4 r = *unit_at(n, u);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
         uint32_t m = 0u;  // (magnitudes of bf16 are in the order of their bits, NaN above infinity)
@@ -464,11 +473,10 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
         for (int b = 0; b < 4; ++b) m = __vmaxu2(m, w[b] & 0x7FFF7FFFu);
         const unsigned top = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
         if (lane == 0) atomicMax(&xtop[par * 32 + n], (int)(top << 16));
-      }
+      });
     }
     __syncthreads();
-    for (int i = warp; i < np * nk; i += warps) {
-      const int n = i / nk, u = (i - n * nk) * 32 + lane;
+    chunks(np, [&](int n, int u) {
       const int up = DOWN ? xtop[par * 32 + n] : f16_up((unsigned)xtop[par * 32 + n]);
       if (u == 0) xdown[par * 32 + n] = pow2(-up);
       // h: 2^(up of the vector - up of the unit), at least 2^-126, where nothing is left of 16 bits
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
         w[b] = *reinterpret_cast<const uint32_t *>(&y);
       }
       *to = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    });
     if (tid < 32) xtop[(par ^ 1) * 32 + tid] = DOWN ? INT_MAX : INT_MIN;
     __syncthreads();
 
@@ -770,6 +778,7 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
     warps = 8;
     fit(kMoeSmem);
   }
+  p.share = (uint32_t)((uint64_t{1} << 32) / (uint32_t)ctas);
   const size_t smem = (size_t)moe_smem(p.group, p.cols, down, warps, loads, a.experts, p.pairs);
   return with_kernel(p.group <= 8 ? 1 : 4, down, a.gated, loads,
                      [&](auto *k) { return launch_dependent(k, ctas, warps * 32, smem, p, st); });
