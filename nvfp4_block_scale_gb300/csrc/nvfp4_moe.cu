@@ -61,7 +61,7 @@ struct MoeLaunch {
   int group;          // pairs of a job at most
   int steps;          // of 256 columns
   int tiles;          // of a job
-  int job_cost;       // of a job besides its tiles: its vectors' way, mostly (3.5 us of 32 at 61 tokens)
+  int job_cost;       // of a job besides its tiles and vectors
   int more_cost;      // of a tile for each further n-tile, in eighths of a tile's
   uint32_t share;     // of the cost, of a CTA: 2^32 / CTAs
   int64_t cols;       // of this launch's matrices
@@ -104,9 +104,13 @@ static_assert(kMaxExperts <= 1024 && kMoeSlicePairs <= 2048, "a job's fields");
 // A tile's cost: its weights' way, and a part of that for each further n-tile of pairs.
 // Measured: 61 tokens 2048 x 768, 8 of 128 (kWide): a tile of 9 .. 16 pairs took
 // 1.44 times one of up to 8; 256 tokens 2064 x 1424, 6 of 60 (kAny): 1.2, and
-// 1.4 with a third n-tile.
+// 1.4 with a third n-tile.  (Weighing the pairs within an n-tile too made 33 tokens
+// 7168 x 2048, 8 of 256 slower, 645 -> 652 us.)
 __device__ __forceinline__ int moe_tile_cost(const MoeLaunch &p, int pairs) { return 8 + p.more_cost * ((pairs - 1) / 8); }
-__device__ __forceinline__ int moe_job_cost(const MoeLaunch &p, int pairs) { return p.job_cost + p.tiles * moe_tile_cost(p, pairs); }
+// A job's besides its tiles: a vector's way into shared memory takes more than half
+// as long as a tile (0.37 us and 0.4 at 2048 columns, 1.2 and 1.4 at 7168).
+__device__ __forceinline__ int moe_begin_cost(const MoeLaunch &p, int pairs) { return p.job_cost + 5 * pairs; }
+__device__ __forceinline__ int moe_job_cost(const MoeLaunch &p, int pairs) { return moe_begin_cost(p, pairs) + p.tiles * moe_tile_cost(p, pairs); }
 
 // The plan: the pairs that have an expert by expert, ascending, so that every
 // CTA cuts an expert's into the same jobs; the jobs, and the cost of those
@@ -263,11 +267,11 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
                    at1 = blockIdx.x + 1 == gridDim.x ? (uint32_t)cost : __umulhi((blockIdx.x + 1) * p.share, (uint32_t)cost);
     for (int j = tid; j <= total; j += threads) {  // one j holds each place
       const uint32_t from = (uint32_t)o.start[j], to = j < total ? (uint32_t)o.start[j + 1] : ~0u;
-      const int c = j < total ? moe_tile_cost(p, (int)(o.jobs[j] & 63u)) : 1;
+      const int np = (int)(o.jobs[max(min(j, total - 1), 0)] & 63u), begin = moe_begin_cost(p, np), c = moe_tile_cost(p, np);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t at = i ? at1 : at0;
-        if (from <= at && at < to) bound[i][0] = j, bound[i][1] = j < total ? max((int)(at - from) - p.job_cost, 0) / c : 0;
+        if (from <= at && at < to) bound[i][0] = j, bound[i][1] = j < total ? max((int)(at - from) - begin, 0) / c : 0;
       }
     }
     __syncthreads();
@@ -762,7 +766,7 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
   const int loads = down ? loads_of(a.down) : std::max(loads_of(a.up), a.gated ? loads_of(a.gate) : (int)kWide);
   // Pairs that a job should take: few experts have more than three times the mean and four.
   const int wanted = std::min({p.pairs, 32, 4 + 3 * p.pairs / a.experts});
-  p.job_cost = std::min(576 / p.steps, p.tiles);
+  p.job_cost = std::min(368 / p.steps, p.tiles);
   p.more_cost = loads == kWide ? 3 : 2;
   // Little work: one small CTA per SM, so that the next launch's CTAs find room beside
   // it (1 token 2048 x 768, 8 of 128: 22.1 -> 20.6 us).
