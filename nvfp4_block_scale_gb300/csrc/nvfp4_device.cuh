@@ -345,6 +345,11 @@ __device__ __forceinline__ float cand_err_m2p(float s, float m2P, float R) {
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Another CTA's shared memory is there once that CTA has begun: every CTA of a cluster
+// arrives at its start and waits (for nothing, by then) before its first access to another's.
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.arrive.relaxed.aligned;"); }
+__device__ __forceinline__ void cluster_wait_begun() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // Checked build (-DNVFP4_CHECKED).  The hot-path kernels test the index of
 // each global-memory and table access against its buffer's extent before

@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __grid_consta
   const int tokens = (int)min((int64_t)G, a.tokens - t0);
   const int e0 = rank * p.per, mine = max(0, min(p.per, a.experts - e0));
   double *const logits = sums + max(p.splits * p.per * G, a.experts);
+  cluster_begun();
   pdl_wait();
   pdl_launch_dependents();
 
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(const __grid_consta
     if (lane % kLanes == 0) sums[((size_t)s * p.per + e) * G + lane / kLanes] = d[0];
   }
   __syncthreads();
+  cluster_wait_begun();
   // ---- every logit to the CTA of its token
   for (int i = tid; i < mine * tokens; i += kRouteThreads) {
     const int e = i / tokens, g = i - e * tokens;
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
   uint32_t *const token_any = reinterpret_cast<uint32_t *>(token_part + p.splits * kTcTokens);  // [splits][kTcTokens]
   float *const scores = reinterpret_cast<float *>(token_any + p.splits * kTcTokens);            // [2][experts]
   if (tid == 0) doubtful = 0;
+  cluster_begun();
   pdl_wait();
   pdl_launch_dependents();
 
@@ -426,6 +429,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
     }
   }
   __syncthreads();
+  cluster_wait_begun();
   // ---- every logit to the CTA of its token, every row's norm to all
   for (int i = tid; i < mine * kTcTokens; i += kTcThreads) {
     const int e = i / kTcTokens, t = i - e * kTcTokens;

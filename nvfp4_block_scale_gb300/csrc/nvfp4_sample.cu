@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   uint32_t *slice_count = reinterpret_cast<uint32_t *>(slice_mass + 2 * bins);         // [2][bins]
   float *vals = reinterpret_cast<float *>(CUTS ? (void *)(slice_count + 2 * bins) : (void *)slice_mass);
   const int row = blockIdx.x / ctas;
+  cluster_begun();
   const int first = rank * p.seg, n = max(0, min(p.seg, a.vocabulary - first));
   const T *logits = static_cast<const T *>(a.logits) + (int64_t)row * a.stride + first;
 
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   };
   top = 0;
   for (int w = 0; w < kSampleWarps; ++w) top = max(top, sh.warp_sum[w]);
+  cluster_wait_begun();
   tell(top, 0, 0, 0);
   for (int r = 0; r < ctas; ++r) top = max(top, sh.box[turn][r][0]);
   const bool writes = rank == 0 && tid == 0;
