@@ -826,6 +826,8 @@ def moe(experts: Experts, x, ids, weights, activation="silu", residual=None, out
     if out is None:
         out = _empty((tokens, hidden), torch.bfloat16, experts.device, stream)
     yp, ys = _rows_of(out, tokens, hidden, "out")
+    if not experts.device == x.device == out.device == (x if residual is None else residual).device:
+        raise ValueError("x, residual and out must be on the experts' device")
     wp, wb = _space(workspace, experts.device)
     _check((_lib or load()).nvfp4_moe(experts.desc, xp, xs, tokens, top_k, ids.data_ptr(), weights.data_ptr(),
                                       ACTIVATIONS[activation], rp, rs, yp, ys, wp, wb, _on(experts.device, stream)),
@@ -864,6 +866,7 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None
         raise ValueError(f"uniform must be a contiguous fp32 tensor [{rows}] on the logits' device")
     tp, t = _setting(temperature, 1.0, rows, torch.float32, device, "temperature")
     kp, k = _setting(top_k, 0, rows, torch.int32, device, "top_k")
+    k = max(min(k, vocabulary), 0)
     pp, p = _setting(top_p, 1.0, rows, torch.float32, device, "top_p")
     mp, m = _setting(min_p, 0.0, rows, torch.float32, device, "min_p")
     token = _empty((rows,), torch.int32, device, stream)

@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
     const int e = i / kTcCtas, r = i - e * kTcCtas;
     float n = 0.0f;
     for (int s = 0; s < p.splits; ++s) n += row_part[s * rows + e];
-    cluster.map_shared_rank(row_norm, r)[e0 + e] = sqrtf(n);
+    cluster.map_shared_rank(row_norm, r)[e0 + e] = sqrtf(n + 0x1p-100f);  // (an upper bound where squares underflow)
   }
   cluster.sync();
 
@@ -470,7 +470,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
     // (squares that may have underflowed bound nothing; a token of zeros has exact logits)
     norm = norm > 0x1p-100f ? sqrtf(norm) * kBand<R> : INFINITY;
     // how far arithmetic may have moved an expert's score (a sigmoid's slope is at most 1/4)
-    auto off = [&](int o, float s) {
+    auto off = [&](int o, float s) {  // (a bias of -inf or inf leaves nothing open)
+      if (fabsf(s) == INFINITY) return 0.0f;
       return norm * row_norm[o] * (a.sigmoid ? 0.25f : 1.0f) + 0x1p-21f * (fabsf(s) + (a.sigmoid ? 1.0f : 0.0f));
     };
     // those that may be among the chosen reach up to where the last of these may have come from

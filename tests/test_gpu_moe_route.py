@@ -107,6 +107,32 @@ def test_tokens_of_zeros_and_tiny_ones():
     _check(x.to(torch.bfloat16), torch.cat((r[:64], r[:64])), 5, "sigmoid", False, torch.zeros(128))
 
 
+@pytest.mark.parametrize("tokens", [3, 200])
+def test_experts_that_a_bias_masks(tokens):
+    """A bias of -inf is below everything, one of inf above; of equal ones the lower first."""
+    g = torch.Generator().manual_seed(14)
+    x = torch.randn((tokens, 256), generator=g).to(torch.bfloat16)
+    r = (0.1 * torch.randn((96, 256), generator=g)).to(torch.bfloat16)
+    bias = 0.1 * torch.randn(96, generator=g)
+    bias[torch.randperm(96, generator=g)[:70]] = -float("inf")
+    _check(x, r, 8, "sigmoid", True, bias)
+    _check(x, r, 30, "sigmoid", True, bias)  # (26 of them are not masked)
+    bias[torch.randperm(96, generator=g)[:3]] = float("inf")
+    _check(x, r, 8, "sigmoid", False, bias)
+
+
+def test_rows_whose_squares_underflow():
+    """Rows of 2^-75 whose products cancel to 2^-20 of their terms: experts that the tensor cores leave open, which
+    norms of zero would not show."""
+    g = torch.Generator().manual_seed(15)
+    x = torch.randn((130, 256), generator=g).to(torch.bfloat16)
+    x[:, 128:] = -x[:, :128]
+    r = torch.randn((64, 128), generator=g).to(torch.bfloat16)
+    r = torch.cat((r, r), 1)
+    r[:, 3], r[:, 131] = 2.0 ** -14 * torch.randn(64, generator=g), 0.0
+    _check(x, (r.float() * 2.0 ** -75).to(torch.bfloat16), 12)
+
+
 def test_equal_scores_go_to_the_lower_expert():
     x = torch.randn((4, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
     row = torch.randn((1, 64), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)

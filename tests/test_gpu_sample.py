@@ -34,6 +34,12 @@ def _check(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     return token
 
 
+def test_a_top_k_past_32_bits_keeps_all():
+    x, u = torch.zeros((1, 100)), torch.tensor([0.995])
+    for k in (100, 2 ** 31, 2 ** 32 + 5, -2 ** 40):
+        assert nv.sample(x.cuda(), u.cuda(), top_k=k).tolist() == [99]
+
+
 def _logits(rows, vocabulary, kind, seed, spread=2.5):
     g = torch.Generator().manual_seed(seed)
     return (spread * torch.randn((rows, vocabulary), generator=g)).to(kind), torch.rand(rows, generator=g)

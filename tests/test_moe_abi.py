@@ -122,6 +122,34 @@ def test_struct_layouts_match_the_header():
     assert ctypes.sizeof(nv.nvfp4_sampling) == 48
 
 
+class _Elsewhere:
+    """What the binding looks at of a tensor on a device that this machine need not have."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+
+    def stride(self):
+        return (self.shape[1], 1)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.mark.parametrize("what", ["x", "residual", "out", "ids", "weights"])
+def test_moe_refuses_operands_on_another_device(what):
+    experts = nv.Experts.__new__(nv.Experts)
+    experts.experts, experts.hidden, experts.inner, experts.device = 4, 64, 64, torch.device("cuda:0")
+    on = {n: "cuda:1" if n == what else "cuda:0" for n in ("x", "residual", "out", "ids", "weights")}
+    t = {n: _Elsewhere((2, 64), torch.bfloat16, on[n]) for n in ("x", "residual", "out")}
+    t["ids"], t["weights"] = _Elsewhere((2, 2), torch.int32, on["ids"]), _Elsewhere((2, 2), torch.float32, on["weights"])
+    with pytest.raises(ValueError, match="experts' device"):
+        nv.moe(experts, t["x"], t["ids"], t["weights"], residual=t["residual"], out=t["out"])
+
+
 def test_bindings_refuse_host_tensors():
     cpu = torch.zeros((2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
