@@ -10,10 +10,16 @@
 // polynomial), sums of them are 64-bit integers, whose order does not matter,
 // and u times a sum is formed in 128 bits.
 //
-// Bound: reading the logits for many rows, and about 50 instructions a token;
-// for few rows latency, a dozen dependent phases of a cluster.
+// Bound: latency, a dozen dependent phases of a cluster (reading and the largest, a
+// histogram, its slices, the cut, the sum), and the instructions of a token: about 40 for
+// its weight, 50 more for a cut by mass.  Measured (bytes are the logits'): 1 x 32000 bf16,
+// top-k 50 and top-p 0.9: 15 us; 7 x 262144 fp32, top-p 0.9: 42 us; 61 x 128256 bf16,
+// every row with cuts of its own: 66 us; 256 x 151003 fp32, min-p 0.02: 102 us, 1.5 TB/s.
+// (Tried for the third: bf16 in shared memory and clusters of half the size, one wave
+// instead of two, 75 us; CTAs of 1024 threads, 72; comparing values before bins are
+// computed, 71.)
 //
-// Work split: a cluster of 1 to 8 CTAs per row, each with its run of the row in
+// Work split: a cluster of 1 to 16 CTAs per row, each with its run of the row in
 // shared memory as fp32 (what does not fit is read again), so a row is read
 // once.  A thread owns a run of consecutive tokens, of odd length, which spreads
 // its threads over the banks and keeps index order in thread order.
@@ -21,9 +27,10 @@
 // A cut (the k-th token, or the one that reaches top_p) is found through a
 // histogram of counts and masses over 2048 ranges of the exponent, whose
 // slices the cluster's CTAs add up; the tokens of the range that holds the
-// cut (a handful to some hundreds) meet in one CTA, where each counts what
-// comes before it.  A range with too many of them is split again, by value and
-// index.  Without top-k and top-p there is no histogram: two passes.
+// cut (a handful to some hundreds) meet in one CTA, which sorts them (each
+// counts those before it) and sums in order.  A range with too many of them is
+// split again, by value and index.  Without top-k and top-p there is no
+// histogram: two passes.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -40,7 +47,7 @@ namespace cg = cooperative_groups;
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
 constexpr int kSampleMaxCtas = 16;  // of a cluster (8 where a device cannot place more)
 constexpr int kBins = 2048;
-constexpr int kList = kSampleThreads;  // tokens that one CTA ranks, one per thread
+constexpr int kList = kSampleThreads;  // tokens that one CTA ranks
 constexpr int kShortK = 256;           // top-k up to which one CTA finishes the row
 constexpr int kOneBits = 42;      // a weight of 1
 constexpr int kSampleSmem = 226 * 1024;
@@ -112,6 +119,7 @@ struct alignas(16) SampleShared {
 };
 struct SampleList {  // over the histogram
   uint64_t key[kList], mass[kList];
+  uint64_t sorted_key[kList], sorted_mass[kList];
 };
 static_assert(sizeof(SampleList) <= sizeof(SampleShared<true>::hist), "the list lies over the histogram");
 // The slices' totals (for the first histogram and for a finer one), then the values.
@@ -320,7 +328,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       if (hi) atomicAdd(&sh.hist[2][bin], hi);
     }
   };
-  auto bin_of = [&](float v) { return min(kBins - 1, (int)(power(v) * (-(float)kBins / (kOneBits + 2)))); };
+  // Three quarters of the bins for the first 22 of the 44 octaves, where a cut by mass
+  // lies: its weight is at least (1 - top_p) / vocabulary of the largest.
+  auto bin_of = [&](float v) {
+    const float x = -power(v);
+    return (int)fminf(fminf(x * (0.75f * kBins / 22.0f), fmaf(x, 0.25f * kBins / 22.0f, 0.5f * kBins)), (float)(kBins - 1));
+  };
 
   struct Totals {
     uint64_t mass;
@@ -373,6 +386,56 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     *inside = (uint32_t)f[3];
     return Totals{f[0], (uint32_t)f[1]};
   };
+  // Puts a list in descending order of its keys (all different): an element's place is the
+  // number of larger ones, counted by as many threads as there are for each.
+  auto sort_list = [&](SampleList &l, int count) {
+    const int share = min(9 - (32 - __clz(max(count - 1, 0))), 5), e = tid >> share;  // log2 of an element's threads
+    const bool there = e < count;
+    const uint64_t key = there ? l.key[e] : 0;
+    int place = 0;
+    if (there) {
+#pragma unroll 4
+      for (int j = tid & ((1 << share) - 1); j < count; j += 1 << share) place += l.key[j] > key;
+    }
+    for (int o = 1; o < 1 << share; o <<= 1) place += __shfl_xor_sync(~0u, place, o);
+    if (there && (tid & ((1 << share) - 1)) == 0) l.sorted_key[place] = key, l.sorted_mass[place] = l.mass[e];
+    __syncthreads();
+  };
+  static_assert(kSampleThreads == 512 && kList == 512, "2^9 threads and elements");
+  // The sum of the masses of the threads before this one, and of all.
+  auto block_scan = [&](uint64_t v, uint64_t *all) {
+    uint64_t in = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t up = __shfl_up_sync(~0u, in, o);
+      if (lane >= o) in += up;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp_sum[warp] = in;
+    __syncthreads();
+    uint64_t before = in - v, sum = 0;
+    for (int w = 0; w < kSampleWarps; ++w) {
+      if (w == warp) before += sum;
+      sum += sh.warp_sum[w];
+    }
+    *all = sum;
+    return before;
+  };
+  // This thread's tokens of which `is` holds to the list of CTA 0 (which lies over its histogram, by
+  // then spent); what does not fit is left out.
+  auto gather = [&](auto is) {
+    if (rank == 0 && tid == 0) sh.listed = 0;
+    cluster.sync();
+    SampleList *list = reinterpret_cast<SampleList *>(cluster.map_shared_rank(&sh.hist[0][0], 0));
+    uint32_t *listed = cluster.map_shared_rank(&sh.listed, 0);
+    for (int i = t0; i < t1; ++i) {
+      const float v = get(i);
+      if (!is(v, i)) continue;
+      const uint32_t at = atomicAdd(listed, 1u);
+      if (at < kList) list->key[at] = key_of(v, i), list->mass[at] = weight(v);
+    }
+    cluster.sync();
+  };
   // The first token in order with which the count or mass reaches goal, and both up to and with it.
   auto find = [&](bool mass, uint64_t goal, uint64_t *key) {
     int bin;
@@ -410,30 +473,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       high = hk - ((uint64_t)at << down);  // (keys of finite values are above 2^54, a bin's width is at most 2^53)
       low = high - ((1ull << down) - 1);
     }
-    // the range's tokens to CTA 0
-    if (rank == 0 && tid == 0) sh.listed = 0;
-    cluster.sync();
-    SampleList *list = reinterpret_cast<SampleList *>(cluster.map_shared_rank(&sh.hist[0][0], 0));
-    uint32_t *listed = cluster.map_shared_rank(&sh.listed, 0);
-    for (int i = t0; i < t1; ++i) {
-      const float v = get(i);
-      if (!in_range(v, i)) continue;
-      const uint32_t at = atomicAdd(listed, 1u);
-      if (at < kList) list->key[at] = key_of(v, i), list->mass[at] = weight(v);  // (there are `inside` of them)
-    }
-    cluster.sync();
+    gather(in_range);  // (there are `inside` of them)
     if (rank == 0) {
       const int count = min((int)inside, kList);
-      const SampleList &l = *reinterpret_cast<const SampleList *>(&sh.hist[0][0]);
-      if (tid < count) {
-        const uint64_t k = l.key[tid];
-        Totals ahead = b;
-        for (int j = 0; j < count; ++j)
-          if (l.key[j] > k) ahead.mass += l.mass[j], ++ahead.count;
-        const uint64_t upto = mass ? ahead.mass + l.mass[tid] : (uint64_t)ahead.count + 1;
-        if ((mass ? ahead.mass : ahead.count) < goal && upto >= goal)
-          sh.found[0] = k, sh.found[1] = ahead.mass + l.mass[tid], sh.found[2] = ahead.count + 1;
-      }
+      SampleList &l = *reinterpret_cast<SampleList *>(&sh.hist[0][0]);
+      sort_list(l, count);
+      const uint64_t own = tid < count ? l.sorted_mass[tid] : 0;
+      uint64_t all;
+      const Totals ahead = {b.mass + block_scan(own, &all), b.count + (uint32_t)tid};
+      const uint64_t upto = mass ? ahead.mass + own : (uint64_t)ahead.count + 1;
+      if (tid < count && (mass ? ahead.mass : ahead.count) < goal && upto >= goal)
+        sh.found[0] = l.sorted_key[tid], sh.found[1] = ahead.mass + own, sh.found[2] = ahead.count + 1;
       __syncthreads();
     }
     tell(sh.found[0], sh.found[1], sh.found[2], 0);
@@ -470,53 +520,27 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       count = find_bin(0, Totals{0, 0}, false, (uint64_t)top_k, &last, &inside).count + inside;
     }
     if (count <= kList) {
-      if (rank == 0 && tid == 0) sh.listed = 0;
-      cluster.sync();
-      SampleList *list = reinterpret_cast<SampleList *>(cluster.map_shared_rank(&sh.hist[0][0], 0));
-      uint32_t *listed = cluster.map_shared_rank(&sh.listed, 0);
-      for (int i = t0; i < t1; ++i) {
-        const float v = get(i);
-        if (!alive(v) || bin_of(v) > last) continue;
-        const uint32_t at = atomicAdd(listed, 1u);
-        if (at < kList) list->key[at] = key_of(v, i), list->mass[at] = weight(v);  // (there are `count` of them)
-      }
-      cluster.sync();
+      gather([&](float v, int) { return alive(v) && bin_of(v) <= last; });  // (there are `count` of them)
       if (rank > 0) return;
       SampleList &l = *reinterpret_cast<SampleList *>(&sh.hist[0][0]);
-      auto block_sum = [&](uint64_t v) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-        __syncthreads();
-        if (lane == 0) sh.warp_sum[warp] = v;
-        __syncthreads();
-        v = 0;
-        for (int w = 0; w < kSampleWarps; ++w) v += sh.warp_sum[w];
-        return v;
-      };
-      const bool there = tid < (int)count;
-      const uint64_t key = there ? l.key[tid] : 0, mass = there ? l.mass[tid] : 0;
-      Totals ahead = {0, 0};
-      if (there)
-        for (int j = 0; j < (int)count; ++j)
-          if (l.key[j] > key) ahead.mass += l.mass[j], ++ahead.count;
-      uint64_t w = there && ahead.count < (uint32_t)top_k ? mass : 0;
-      if (by_mass) {  // (the largest token stays whatever top_p)
-        const uint64_t goal = max(uint64_t{1}, share_of(block_sum(w), top_p > 0.0f ? top_p : 0.0f, true));
-        if (ahead.mass >= goal) w = 0;
-      }
+      sort_list(l, (int)count);
+      // (top-k, top-p and min-p each keep the first in order)
+      const int keep = min((int)count, top_k);
+      const uint64_t key = tid < keep ? l.sorted_key[tid] : 0;
+      uint64_t w = tid < keep ? l.sorted_mass[tid] : 0, total;
+      const uint64_t ahead = block_scan(w, &total);
+      if (by_mass && ahead >= max(uint64_t{1}, share_of(total, top_p > 0.0f ? top_p : 0.0f, true))) w = 0;  // (the largest stays)
       if (w < least) w = 0;
-      const uint64_t total = block_sum(w), goal = share_of(total, u, false);  // (its barriers: every key and mass has been read)
-      if (there) l.mass[tid] = w;
-      __syncthreads();
-      if (w) {
-        const uint32_t mine = (uint32_t)key;  // smaller indices have larger ones
-        uint64_t before = 0;
-        for (int j = 0; j < (int)count; ++j)
-          if ((uint32_t)l.key[j] > mine) before += l.mass[j];
-        if (before <= goal && before + w > goal) {
-          const uint32_t vb = (uint32_t)(key >> 32);
-          write((int)~mine, __uint_as_float(vb >> 31 ? vb & 0x7FFFFFFFu : ~vb), total);
-        }
+      // those that stay by index: their keys' halves change places
+      if (tid < keep) l.key[tid] = key << 32 | key >> 32, l.mass[tid] = w;
+      const int stay = __syncthreads_count(w != 0);
+      sort_list(l, stay);
+      w = tid < stay ? l.sorted_mass[tid] : 0;
+      const uint64_t before = block_scan(w, &total), goal = share_of(total, u, false);
+      if (w && before <= goal && before + w > goal) {
+        const uint64_t k = l.sorted_key[tid];
+        const uint32_t vb = (uint32_t)k;
+        write((int)~(uint32_t)(k >> 32), __uint_as_float(vb >> 31 ? vb & 0x7FFFFFFFu : ~vb), total);
       }
       return;
     }
@@ -556,20 +580,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     const float v = get(i);
     if (v >= low_v) own += stays(v, i);
   }
-  uint64_t upto = own;  // of this warp's threads, this one's included
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t u = __shfl_up_sync(~0u, upto, o);
-    if (lane >= o) upto += u;
-  }
-  __syncthreads();  // (warp_sum's readers before)
-  if (lane == 31) sh.warp_sum[warp] = upto;
-  __syncthreads();
-  uint64_t sum = 0, before = 0;
-  for (int w = 0; w < kSampleWarps; ++w) {
-    if (w == warp) before = sum;
-    sum += sh.warp_sum[w];
-  }
+  uint64_t sum;
+  uint64_t before = block_scan(own, &sum);
   tell(sum, 0, 0, 0);
   uint64_t total = 0;
   for (int r = 0; r < ctas; ++r) {
@@ -577,17 +589,25 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     total += sh.box[turn][r][0];
   }
   const uint64_t goal = share_of(total, u, false);  // a whole sum is above u * total where it is above this
-  before += upto - own;
-  if (before <= goal && before + own > goal) {  // one thread of the cluster
-    for (int i = t0; i < t1; ++i) {
-      const float v = get(i);
-      if (!(v >= low_v)) continue;
-      before += stays(v, i);
-      if (before > goal) {
-        write(first + i, v, total);
-        break;
-      }
+  const uint32_t here = __ballot_sync(~0u, before <= goal && before + own > goal);
+  if (here == 0) return;
+  // one thread's run, of the whole cluster: its warp goes over it once more
+  const int from = __ffs(here) - 1, first_of = __shfl_sync(~0u, t0, from), last_of = __shfl_sync(~0u, t1, from);
+  before = __shfl_sync(~0u, before, from);
+  for (int i0 = first_of; i0 < last_of; i0 += 32) {
+    const int i = i0 + lane;
+    const float v = i < last_of ? get(i) : -INFINITY;
+    const uint64_t w = v >= low_v && i < last_of ? stays(v, i) : 0;
+    uint64_t upto = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t up = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += up;
     }
+    upto += before;
+    if (upto - w <= goal && upto > goal) write(first + i, v, total);
+    before = __shfl_sync(~0u, upto, 31);
+    if (before > goal) break;
   }
 }
 
@@ -597,8 +617,8 @@ int g_sample_ctas = 8;  // of a cluster at most
 
 template <typename T, bool CUTS>
 cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
-  // As few CTAs per row as let two of them share an SM (three, of twice as many, took 133
-  // us instead of 124 on 256 x 151003); more, down to 2048 tokens each, while that
+  // As few CTAs per row as let two of them share an SM (three, of twice as many, took 7 %
+  // longer on 256 x 151003, half as many that read a third of their row again 58 %); more, down to 2048 tokens each, while that
   // leaves SMs idle.
   int ctas = 1;
   const int64_t share = 112 * 1024;
