@@ -4,19 +4,31 @@
 //   y[t]   = bf16( residual[t] + sum_s weights[t][s] alpha_d sum_j q Delta h[t,s][j] ).
 //
 // Bound: reading once the weights of every expert that some token names
-// (0.5625 B each); a token's share of x, h and y is small beside them.
+// (0.5625 B each); a token's share of x, h and y is small beside them.  Measured
+// with cold weights, and the rate at which those came (a copy reads and writes
+// 6.77 TB/s):
+//   33 tokens 7168 x 2048, 8 of 256       612 us   6.0 TB/s
+//    5 tokens 4096 x 14336, 2 of 8        121      4.1
+//   61 tokens 2048 x 768, 8 of 128         79      3.8
+//   256 tokens 2064 x 1424, 6 of 60       187      1.1  (no gate; 26 pairs an expert, 96 TFLOP/s)
+//    1 token 2048 x 768, 8 of 128          17      1.2
+// What the largest leaves is the plan, the first fetches (4 to 6 us a launch) and
+// CTAs that end apart (5 to 10); with less work those weigh more, with many pairs an
+// expert their vectors' way into shared memory and the MMAs' four n-tiles.
 //
 // Three launches, each waiting for the one before through a programmatic
-// dependency: gate and up with the activation (h, fp32, to the workspace), down
-// (each slot's product, fp32, to the workspace), and the sum over a token's
-// slots in slot order.  No atomics take part in a sum and no CTA waits for
-// another, so a workspace may hold anything and results repeat bit for bit.
+// dependency: gate and up with the activation (h, f16 with a power of two for each
+// 8 entries, to the workspace), down (each slot's product, fp32, to the workspace),
+// and the sum over a token's slots in slot order.  No atomics take part in a sum and
+// no CTA waits for another, so a workspace may hold anything and results repeat bit
+// for bit.
 //
 // Jobs: every CTA sorts the call's (token, slot) pairs by expert in shared
 // memory; an expert with n pairs makes ceil(n / N) jobs of up to N pairs.  The
-// row tiles of all jobs, job after job, are cut into one contiguous range per
-// SM, and the units (16 rows by 256 columns) of a range's part of one job into 16
-// contiguous runs, one per warp.  A warp that does a whole tile finishes it
+// row tiles of all jobs, job after job, are cut by measured costs into one
+// contiguous range per CTA (two of 8 warps on an SM, or one of 16 where the vectors
+// leave no room for two), and the units (16 rows by 256 columns) of a range's part of
+// one job into contiguous runs, one per warp.  A warp that does a whole tile finishes it
 // from its registers; sums of a tile cut between warps meet in shared memory, in
 // warp order.  Codes come by asynchronous copies, kMoeDepth units ahead, across
 // tiles and jobs.
@@ -103,7 +115,7 @@ __device__ __forceinline__ uint32_t moe_job(int expert, int at, int n) { return 
 static_assert(kMaxExperts <= 1024 && kMoeSlicePairs <= 2048, "a job's fields");
 // A tile's cost: its weights' way, and a part of that for each further n-tile of pairs.
 // Measured: 61 tokens 2048 x 768, 8 of 128 (kWide): a tile of 9 .. 16 pairs took
-// 1.44 times one of up to 8; 256 tokens 2064 x 1424, 6 of 60 (kAny): 1.2, and
+// 1.44 times one of up to 8; 256 tokens 2064 x 1424, 6 of 60 (rows on 8 bytes): 1.2, and
 // 1.4 with a third n-tile.  (Weighing the pairs within an n-tile too made 33 tokens
 // 7168 x 2048, 8 of 256 slower, 645 -> 652 us.)
 __device__ __forceinline__ int moe_tile_cost(const MoeLaunch &p, int pairs) { return 8 + p.more_cost * ((pairs - 1) / 8); }
@@ -769,7 +781,7 @@ cudaError_t launch_product(MoeLaunch p, bool down, int sms, cudaStream_t st) {
   p.job_cost = std::min(368 / p.steps, p.tiles);
   p.more_cost = loads == kWide ? 3 : 2;
   // Little work: one small CTA per SM, so that the next launch's CTAs find room beside
-  // it (1 token 2048 x 768, 8 of 128: 22.1 -> 20.6 us).
+  // it (1 token 2048 x 768, 8 of 128: 7 % less time than with two).
   const bool little = (int64_t)std::min(p.pairs, a.experts) * p.tiles * p.steps <= (int64_t)64 * sms;
   int warps = 8, ctas = little ? sms : 2 * sms;
   auto fit = [&](int64_t room) { p.group = moe_group(wanted, p.cols, down, warps, loads, a.experts, p.pairs, room); };
