@@ -105,7 +105,7 @@ __host__ __device__ constexpr int moe_up_pitch(int64_t cols) { return (int)((col
 // Shared memory: the vectors (with h's exponents), the warps' units in flight
 // and partial sums, the vectors' scales, the plan.
 __host__ __device__ constexpr int64_t moe_smem(int group, int64_t cols, bool down, int warps, int loads, int experts, int pairs) {
-  return (cols + 255) / 256 * 512 * group + (down ? (int64_t)group * moe_up_pitch(cols) : 0) +
+  return (cols + 255) / 256 * 512 * (group | 1) + (down ? (int64_t)group * moe_up_pitch(cols) : 0) +
          (int64_t)warps * (kMoeDepth * moe_slot(loads) + (group + 7) / 8 * 512) + 512 +
          (pairs > kMoeFewPairs ? (int64_t)experts * 8 : 0) + ((int64_t)pairs + 1) * 14 + 64;
 }
@@ -119,9 +119,9 @@ static_assert(kMaxExperts <= 1024 && kMoeSlicePairs <= 2048, "a job's fields");
 // 1.4 with a third n-tile.  (Weighing the pairs within an n-tile too made 33 tokens
 // 7168 x 2048, 8 of 256 slower, 645 -> 652 us.)
 __device__ __forceinline__ int moe_tile_cost(const MoeLaunch &p, int pairs) { return 8 + p.more_cost * ((pairs - 1) / 8); }
-// A job's besides its tiles: a vector's way into shared memory takes more than half
-// as long as a tile (0.37 us and 0.4 at 2048 columns, 1.2 and 1.4 at 7168).
-__device__ __forceinline__ int moe_begin_cost(const MoeLaunch &p, int pairs) { return p.job_cost + 5 * pairs; }
+// A job's besides its tiles: a vector's way into shared memory takes about a third of a
+// tile's time (256 tokens 2064 x 1424, 6 of 60: a weight of 0 181 us, 3 176, 5 178).
+__device__ __forceinline__ int moe_begin_cost(const MoeLaunch &p, int pairs) { return p.job_cost + 3 * pairs; }
 __device__ __forceinline__ int moe_job_cost(const MoeLaunch &p, int pairs) { return moe_begin_cost(p, pairs) + p.tiles * moe_tile_cost(p, pairs); }
 
 // The plan: the pairs that have an expert by expert, ascending, so that every
@@ -236,11 +236,11 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   const MoeArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cq = lane & 3;
   const int threads = blockDim.x, warps = threads >> 5, warps_bits = 31 - __clz(warps);  // (8 or 16)
-  const int nk = p.steps, N = p.group, NB = (N + 7) / 8;
+  const int nk = p.steps, N = p.group, NB = (N + 7) / 8, P = N | 1;  // P: vectors' places (odd, see `chunks`)
   constexpr bool WIDE = LOADS == kWide;
   constexpr int kSlot = moe_slot(LOADS), kScales = moe_code_slot(LOADS);  // of a slot: its bytes, where its scales begin
-  uint4 *xs = dsm;                                                        // [nk][8][N][4] 16-byte units of f16
-  uint4 *slots = dsm + (size_t)nk * 32 * N;                               // [warps][depth][kSlot / 16]: units in flight
+  uint4 *xs = dsm;                                                        // [nk][8][P][4] 16-byte units of f16
+  uint4 *slots = dsm + (size_t)nk * 32 * P;                               // [warps][depth][kSlot / 16]: units in flight
   float4 *own = reinterpret_cast<float4 *>(slots + warps * kMoeDepth * (kSlot / 16));  // [warps][NB][32]
   slots += warp * kMoeDepth * (kSlot / 16);
   int8_t *ups = reinterpret_cast<int8_t *>(own + warps * NB * 32);        // [N][up_pitch]
@@ -408,12 +408,15 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
   // what lies in memory, bf16 or f16 of eighths, to their places.
   const int wide = (int)(p.cols / 8);  // units of a vector (nk * 32 with those past the end)
   // unit u: step u / 32, lane quarter (u / 8) % 4, pair of k-steps u % 8
-  auto unit_at = [&](int n, int u) { return xs + (((u >> 5) * 8 + (u & 7)) * N + n) * 4 + ((u >> 3) & 3); };
-  // this warp's chunks of 32 units of n vectors: (vector, chunk)
+  auto unit_at = [&](int n, int u) { return xs + (((u >> 5) * 8 + (u & 7)) * P + n) * 4 + ((u >> 3) & 3); };
+  // This warp's chunks of 32 units of `count` vectors: (vector, the lane's unit).  Eight
+  // lanes in a row have two pairs of k-steps of four lane quarters: with P odd their places are
+  // in different banks (in the order of u, eight met in one: 5 tokens 4096 x 14336, 2 of 8,
+  // took 122 us instead of 105).
   auto chunks = [&](int count, auto f) {
     int n = warp / nk, c = warp - n * nk;
     while (n < count) {
-      f(n, c * 32 + lane);
+      f(n, c * 32 + ((lane & 3) << 3 | lane >> 2));
       c += warps;
       while (c >= nk) c -= nk, ++n;
     }
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
 #pragma unroll
       for (int nt = 0; nt < A; ++nt) {
         xl[nt] = xs + min(8 * nt + g, np - 1) * 4 + cq;
-        xk[nt] = xl[nt] + ck * 32 * N;
+        xk[nt] = xl[nt] + ck * 32 * P;
       }
       [[maybe_unused]] const int chunk0 = g * 8 + ((2 * cq) ^ g), chunk1 = g * 8 + ((2 * cq + 1) ^ g);
       [[maybe_unused]] const int odd_at = g * 144 + (g & 1 ? back : 0) + 32 * cq;
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
             }
 #pragma unroll
             for (int nt = 0; nt < A; ++nt) {
-              const uint4 xb = xk[nt][(half * 4 + jj) * (4 * N)];
+              const uint4 xb = xk[nt][(half * 4 + jj) * (4 * P)];
               mma_f16(acc[nt], w[0][0], w[1][0], w[0][1], w[1][1], xb.x, xb.y);
               mma_f16(acc[nt], w[0][2], w[1][2], w[0][3], w[1][3], xb.z, xb.w);
             }
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
         __syncwarp();
         fetch();  // into the place just read
 #pragma unroll
-        for (int nt = 0; nt < A; ++nt) xk[nt] += 32 * N;
+        for (int nt = 0; nt < A; ++nt) xk[nt] += 32 * P;
         if (++ck == nk) {  // the tile's last step
           if (mine) finish_tile(r.t0 + ct);
           else put_own();
