@@ -8,13 +8,13 @@
 // with cold weights, and the rate at which those came (a copy reads and writes
 // 6.77 TB/s):
 //   33 tokens 7168 x 2048, 8 of 256       612 us   6.0 TB/s
-//    5 tokens 4096 x 14336, 2 of 8        121      4.1
+//    5 tokens 4096 x 14336, 2 of 8        105      4.7
 //   61 tokens 2048 x 768, 8 of 128         79      3.8
-//   256 tokens 2064 x 1424, 6 of 60       187      1.1  (no gate; 26 pairs an expert, 96 TFLOP/s)
+//   256 tokens 2064 x 1424, 6 of 60       164      1.2  (no gate; 26 pairs an expert, 110 TFLOP/s)
 //    1 token 2048 x 768, 8 of 128          17      1.2
 // What the largest leaves is the plan, the first fetches (4 to 6 us a launch) and
 // CTAs that end apart (5 to 10); with less work those weigh more, with many pairs an
-// expert their vectors' way into shared memory and the MMAs' four n-tiles.
+// expert the MMAs of their n-tiles and their vectors' way into shared memory.
 //
 // Three launches, each waiting for the one before through a programmatic
 // dependency: gate and up with the activation (h, f16 with a power of two for each
@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
     if (tid < 32) xtop[(par ^ 1) * 32 + tid] = DOWN ? INT_MAX : INT_MIN;
     __syncthreads();
 
-    // ---- the run, with as many n-tiles as the job's pairs fill
+    // ---- the run, with as many n-tiles as the job's pairs fill (three and four by one
+    // form of four: 256 tokens 2064 x 1424, 6 of 60 took 177 us instead of 164)
     auto products = [&](auto tiles_of_pairs) {
       constexpr int A = decltype(tiles_of_pairs)::value;
       const Run r = run_of(j, warp);
@@ -680,6 +681,7 @@ __global__ void __launch_bounds__(kMoeMaxWarps * 32, 1) k_moe(const __grid_const
     if (np <= 8) products(std::integral_constant<int, 1>());
     else if constexpr (NT > 1) {
       if (np <= 16) products(std::integral_constant<int, 2>());
+      else if (np <= 24) products(std::integral_constant<int, 3>());
       else products(std::integral_constant<int, 4>());
     }
   }
