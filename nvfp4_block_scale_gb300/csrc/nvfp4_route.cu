@@ -13,8 +13,8 @@
 // and the router's first bytes are 3); from about 64 tokens on the 7 fp32 operations a
 // product, so many tokens take the tensor cores, and those operations only where the
 // tensor cores leave the order of two experts open (61 tokens 4096, 2 of 8: 8.5 us;
-// 256 x 7168, 8 of 256: 47 us, 20 TFLOP/s, where the operations for all took 266; about
-// half of it is products, half the choice, the doubtful experts and the weights).
+// 256 x 7168, 8 of 256: 47 us, 20 TFLOP/s, where the operations for all took 266; 17 to
+// 25 of them are loads and products, 5 the choice, up to 8 the doubtful experts).
 //
 // Work split: a cluster of 8 or 16 CTAs takes G tokens; each CTA has its
 // share of the experts, its warps an expert each, or a range of an expert's
