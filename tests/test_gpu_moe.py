@@ -1,6 +1,5 @@
 """The experts' products against the plain 64-bit form, within the bound that
 moe_ref derives."""
-import numpy as np
 import pytest
 import torch
 
@@ -53,6 +52,17 @@ def test_products(shape, gated):
     tokens, hidden, inner, n, k = shape
     host = moe_ref.experts(n, hidden, inner, gated, seed=sum(shape))
     x, ids, w, r = _inputs(tokens, hidden, n, k, 7)
+    _check(host, x, ids, w, "silu", r, _run(host, x, ids, w, "silu", r))
+
+
+# around the edges of what one MMA, a tile of several and a job take; columns in whole steps, and rows of codes on 8 bytes
+@pytest.mark.parametrize("hidden,inner", [(512, 256), (272, 144)])
+@pytest.mark.parametrize("pairs", [2, 7, 8, 9, 16, 17, 23, 24, 25, 31, 32, 33, 57, 65])
+def test_pairs_of_an_expert(pairs, hidden, inner):
+    host = moe_ref.experts(2, hidden, inner, pairs % 2 == 1, seed=pairs)
+    x, ids, w, r = _inputs(pairs + 3, hidden, 2, 1, pairs)
+    ids[:] = 1
+    ids[torch.randperm(pairs + 3, generator=torch.Generator().manual_seed(pairs))[:pairs]] = 0
     _check(host, x, ids, w, "silu", r, _run(host, x, ids, w, "silu", r))
 
 

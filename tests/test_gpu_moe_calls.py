@@ -4,13 +4,11 @@ step of them together."""
 import os
 import sys
 
-import numpy as np
 import pytest
 import torch
 
 import moe_ref
 import nvfp4_block_scale_gb300 as nv
-from decode_ref import within
 from test_gpu_moe import _check, _cuda, _inputs
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))

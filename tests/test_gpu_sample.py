@@ -1,5 +1,4 @@
 """Sampling against its definition in 64 bits: the tokens have to be equal."""
-import numpy as np
 import pytest
 import torch
 
