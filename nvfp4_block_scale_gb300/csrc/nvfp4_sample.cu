@@ -13,11 +13,11 @@
 // Bound: latency, a dozen dependent phases of a cluster (reading and the largest, a
 // histogram, its slices, the cut, the sum), and the instructions of a token: about 40 for
 // its weight, 50 more for a cut by mass.  Measured (bytes are the logits'): 1 x 32000 bf16,
-// top-k 50 and top-p 0.9: 15 us; 7 x 262144 fp32, top-p 0.9: 42 us; 61 x 128256 bf16,
-// every row with cuts of its own: 66 us; 256 x 151003 fp32, min-p 0.02: 102 us, 1.5 TB/s.
+// top-k 50 and top-p 0.9: 15 us; 7 x 262144 fp32, top-p 0.9: 38 us; 61 x 128256 bf16,
+// every row with cuts of its own: 65 us; 256 x 151003 fp32, min-p 0.02: 102 us, 1.5 TB/s.
 // (Tried for the third: bf16 in shared memory and clusters of half the size, one wave
-// instead of two, 75 us; CTAs of 1024 threads, 72; comparing values before bins are
-// computed, 71.)
+// instead of two, took 14 % longer; CTAs of 1024 threads 9 %; comparing values before bins
+// are computed 7 %.)
 //
 // Work split: a cluster of 1 to 16 CTAs per row, each with its run of the row in
 // shared memory as fp32 (what does not fit is read again), so a row is read
@@ -129,8 +129,11 @@ constexpr uint64_t kNoCut = 0;  // keeps every token
 
 // CUTS: some row may have a top_k or top_p.  Without (known from the values for
 // all rows) the kernel is a third as long and needs no histogram.
-template <typename T, bool CUTS>
-__global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_constant__ SampleLaunch p) {
+// PER_SM: CTAs that may share an SM.  With cuts, two leave 64 registers a thread, which is
+// too few (7 x 262144: 41.7 us, alone on an SM 39.1), but 61 rows of 128256 take 90 us
+// instead of 66 with one CTA to an SM.
+template <typename T, bool CUTS, int PER_SM>
+__global__ void __launch_bounds__(kSampleThreads, PER_SM) k_sample(const __grid_constant__ SampleLaunch p) {
   constexpr int kVec = 16 / sizeof(T);
   extern __shared__ __align__(16) uint8_t dsm[];
   SampleShared<CUTS> &sh = *reinterpret_cast<SampleShared<CUTS> *>(dsm);
@@ -428,6 +431,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     cluster.sync();
     SampleList *list = reinterpret_cast<SampleList *>(cluster.map_shared_rank(&sh.hist[0][0], 0));
     uint32_t *listed = cluster.map_shared_rank(&sh.listed, 0);
+#pragma unroll 4
     for (int i = t0; i < t1; ++i) {
       const float v = get(i);
       if (!is(v, i)) continue;
@@ -640,7 +644,9 @@ cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_sample<T, CUTS>, p);
+  if constexpr (CUTS)
+    if ((int64_t)a.rows * ctas <= sms) return cudaLaunchKernelEx(&cfg, k_sample<T, CUTS, 1>, p);
+  return cudaLaunchKernelEx(&cfg, k_sample<T, CUTS, 2>, p);
 }
 
 }  // namespace
@@ -657,10 +663,12 @@ cudaError_t prepare_sample_kernels() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e;
   };
-  cudaError_t e = prepare(k_sample<float, true>);
-  if (e == cudaSuccess) e = prepare(k_sample<float, false>);
-  if (e == cudaSuccess) e = prepare(k_sample<__nv_bfloat16, true>);
-  if (e == cudaSuccess) e = prepare(k_sample<__nv_bfloat16, false>);
+  cudaError_t e = prepare(k_sample<float, true, 1>);
+  if (e == cudaSuccess) e = prepare(k_sample<float, true, 2>);
+  if (e == cudaSuccess) e = prepare(k_sample<float, false, 2>);
+  if (e == cudaSuccess) e = prepare(k_sample<__nv_bfloat16, true, 1>);
+  if (e == cudaSuccess) e = prepare(k_sample<__nv_bfloat16, true, 2>);
+  if (e == cudaSuccess) e = prepare(k_sample<__nv_bfloat16, false, 2>);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -673,7 +681,7 @@ cudaError_t prepare_sample_kernels() {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, k_sample<float, true>, &cfg) != cudaSuccess) cudaGetLastError();  // (8 then)
+  if (cudaOccupancyMaxActiveClusters(&clusters, k_sample<float, true, 1>, &cfg) != cudaSuccess) cudaGetLastError();  // (8 then)
   g_sample_ctas = clusters > 0 ? kSampleMaxCtas : 8;
   return cudaSuccess;
 }
