@@ -157,7 +157,16 @@ __device__ __forceinline__ int choose(const RouteArgs &a, uint64_t *keys, int la
 __device__ __forceinline__ void weigh(const RouteArgs &a, int64_t t, const double *l, int e, int lane) {
   const double m = l[__shfl_sync(~0u, e, 0)];  // softmax: the first choice has the largest logit
   float w = 0.0f, z = 1.0f;
-  if (lane < a.top_k) w = a.sigmoid ? sigmoid((float)l[e]) : expf((float)(l[e] - m));
+  if (a.sigmoid) {
+    // exp(min(l, 0)) / (1 + exp(-|l|)).  Of a sum the exponentials' largest cancels, so that the
+    // weights of logits below -87, whose sigmoids fp32 does not hold, still have one.
+    const float v = (float)l[e];
+    float most = 0.0f;
+    if (a.renormalize) most = -__uint_as_float(__reduce_min_sync(~0u, lane >= a.top_k ? ~0u : v < 0.0f ? __float_as_uint(-v) : 0u));
+    if (lane < a.top_k) w = __fdiv_rn(expf((float)(fmin(l[e], 0.0) - (double)most)), 1.0f + expf(-fabsf(v)));
+  } else if (lane < a.top_k) {
+    w = expf((float)(l[e] - m));
+  }
   if (a.renormalize) {
     z = w;
   } else if (!a.sigmoid) {

@@ -154,3 +154,34 @@ def test_strides_streams_and_repeats():
     for p, q in zip(a + a, b + c):
         assert torch.equal(p, q)
     assert nv.moe_route(x[:0], r, 4)[0].shape == (0, 4)
+
+
+def _exact_logits(tokens, experts, level, kind, seed):
+    """Operands whose logits, `level` give or take a few tens, every order of fp32 sums forms exactly: multiples of
+    1/8 (of level / 64) below 2^11."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.ones((tokens, 128))
+    x[:, 64:] = 2.0 * torch.randint(0, 2, (tokens, 64), generator=g) - 1.0
+    r = torch.full((experts, 128), level / 64)
+    r[:, 64:] = torch.randint(-8, 9, (experts, 64), generator=g) / 8
+    assert torch.equal(r.to(torch.bfloat16).float(), r)
+    return x.to(torch.bfloat16), r.to(kind)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("level", [-300.0, -120.0, -95.0, -20.0])
+@pytest.mark.parametrize("tokens", [3, 200])
+def test_sigmoid_weights_of_strongly_negative_logits(tokens, level, kind):
+    """Sigmoids too small for fp32: what they are of their sum is not."""
+    x, r = _exact_logits(tokens, 64, level, kind, 17)
+    bias = torch.randn(64, generator=torch.Generator().manual_seed(18))
+    for k, b, renormalize in ((8, None, True), (8, bias, True), (1, None, True), (1, bias, True), (8, bias, False)):
+        ids, w = nv.moe_route(x.cuda(), r.cuda(), k, "sigmoid", renormalize, None if b is None else b.cuda(), 2.5)
+        torch.cuda.synchronize()
+        wi, ww = _want(x, r, k, "sigmoid", renormalize, b, 2.5)
+        assert np.array_equal(ids.cpu().numpy(), wi)
+        # two exponentials good to 2 ulp (2^-22 each), a sum of 8 (5 roundings deep), at most four more roundings, and
+        # what fp32 ends at: 2 ulp of an exponential there and three roundings, times 2.5
+        assert np.all(np.abs(w.double().cpu().numpy() - ww) <= 2.0 ** -20 * ww + 1e-44)
+        if k == 1 and renormalize:
+            assert bool((w == 2.5).all())
