@@ -476,11 +476,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_moe_route_tc(const __grid_con
   int e = 0;
   if (has) {
     const float *score = scores + (size_t)warp * a.experts;
-    e = choose(a, keys + (size_t)warp * a.experts, lane);
+    uint64_t *const key = keys + (size_t)warp * a.experts;
     float norm = 0.0f;
     uint32_t any = 0u;
     for (int s = 0; s < p.splits; ++s) norm += token_part[s * kTcTokens + t], any |= token_any[s * kTcTokens + t];
-    // (squares that may have underflowed bound nothing; a token of zeros has exact logits)
+    if (!any && a.bias) {  // a token of zeros: its logits are exact, and so are its scores in fp64
+      for (int o = lane; o < a.experts; o += 32) key[o] = score_key(0.5 + (double)a.bias[o]);
+      __syncwarp();
+    }
+    e = choose(a, key, lane);
+    // (squares that may have underflowed bound nothing)
     norm = norm > 0x1p-100f ? sqrtf(norm) * kBand<R> : INFINITY;
     // how far arithmetic may have moved an expert's score (a sigmoid's slope is at most 1/4)
     auto off = [&](int o, float s) {  // (a bias of -inf or inf leaves nothing open)

@@ -185,3 +185,21 @@ def test_sigmoid_weights_of_strongly_negative_logits(tokens, level, kind):
         assert np.all(np.abs(w.double().cpu().numpy() - ww) <= 2.0 ** -20 * ww + 1e-44)
         if k == 1 and renormalize:
             assert bool((w == 2.5).all())
+
+
+@pytest.mark.parametrize("tokens", [5, 72, 130])
+@pytest.mark.parametrize("neighbours", [False, True])
+def test_tokens_of_zeros_choose_by_biases_closer_than_fp32_tells_apart(tokens, neighbours):
+    """0.5 + bias in fp32 merges biases of some 1e-8; beside a token in doubt or not, the fp64 scores decide."""
+    g = torch.Generator().manual_seed(19)
+    experts = 128
+    bias = 1e-8 * torch.randperm(experts, generator=g).float()
+    r = torch.randn((experts, 256), generator=g).to(torch.bfloat16)
+    x = torch.zeros((tokens, 256), dtype=torch.bfloat16)
+    x[::3] = -0.0
+    if neighbours:  # every other group of eight tokens: experts in pairs of equal logits
+        r[64:] = r[:64]
+        live = (torch.arange(tokens) // 8) % 2 == 1
+        x[live] = torch.randn((int(live.sum()), 256), generator=g).to(torch.bfloat16)
+    _check(x, r, 8, "sigmoid", True, bias)
+    _check(x, r.float(), 8, "sigmoid", False, bias)
