@@ -635,10 +635,14 @@ int nvfp4_ffma_probe(int packed, int64_t rounds, float *sink, int64_t sink_float
  *     outputs come out NaN.  Every copy and MMA already issued still
  *     completes before the CTA exits (those waits keep their normal limits).
  *     tries < 0 restores the normal limits.
- * Both return an nvfp4_status.
+ *   nvfp4_test_small_clusters(on): 1 makes nvfp4_moe_route and nvfp4_sample
+ *     take clusters of 8 CTAs at most, as on a device that places none of 16;
+ *     0 restores the device's own limit.
+ * Each returns an nvfp4_status.
  */
 int nvfp4_test_fail_allocations(int count);
 int nvfp4_test_first_wait_tries(int64_t tries);
+int nvfp4_test_small_clusters(int on);
 
 /*
  * Checked build.  The library compiled with -DNVFP4_CHECKED

@@ -145,6 +145,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.nvfp4_test_fail_allocations.restype = ci
     L.nvfp4_test_first_wait_tries.argtypes = [i64]
     L.nvfp4_test_first_wait_tries.restype = ci
+    L.nvfp4_test_small_clusters.argtypes = [ci]
+    L.nvfp4_test_small_clusters.restype = ci
     L.nvfp4_checked_build.argtypes = []
     L.nvfp4_checked_build.restype = ci
     L.nvfp4_check_take.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
@@ -276,6 +278,11 @@ def nvfp4_test_fail_allocations(count) -> int:
 def nvfp4_test_first_wait_tries(tries) -> int:
     """Test hook: the first bounded device wait gives up after `tries` polls (< 0: normal)."""
     return load().nvfp4_test_first_wait_tries(int(tries))
+
+
+def nvfp4_test_small_clusters(on) -> int:
+    """Test hook: moe_route and sample take clusters of 8 CTAs at most (1), or of the device's own limit (0)."""
+    return load().nvfp4_test_small_clusters(int(on))
 
 
 def nvfp4_checked_build() -> int:

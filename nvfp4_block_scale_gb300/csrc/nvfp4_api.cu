@@ -45,6 +45,7 @@ struct DevInfo {
   int sms = 0;
   int l2 = 0;  // L2 bytes
   int occ[kKernCount] = {};
+  int route_ctas = 0, sample_ctas = 0;  // of a cluster at most
   cudaMemPool_t pool = nullptr;
   // second streams (with their fork/join events) of the pipelined grouped
   // quantization: a caller takes one that no other call holds and that is not
@@ -64,9 +65,11 @@ std::mutex g_mu;
 DevInfo g_dev[kMaxDevices];
 
 // test hooks (nvfp4_test_*): allocations left to fail, and the first-wait
-// limit passed to the kernels with bounded waits (< 0: normal)
+// limit passed to the kernels with bounded waits (< 0: normal), and whether
+// clusters keep to the size that every device places
 std::atomic<int> g_fail_allocs{0};
 std::atomic<long> g_first_wait{-1};
+std::atomic<bool> g_small_clusters{false};
 
 // Scratch from the library's pool on `stream` (or a failure the test hook asked for).
 cudaError_t pool_alloc(void **p, size_t bytes, cudaMemPool_t pool, cudaStream_t stream) {
@@ -83,14 +86,16 @@ int first_tries() {
   return fw < 0 ? -1 : (int)std::min<long>(fw, INT32_MAX);
 }
 
+int most_ctas(int placed) { return g_small_clusters.load() ? std::min(placed, 8) : placed; }
+
 int map_cuda(cudaError_t e) {
   if (e == cudaSuccess) return NVFP4_OK;
   if (e == cudaErrorMemoryAllocation) return NVFP4_ERR_OUT_OF_MEMORY;
   return NVFP4_ERR_CUDA;
 }
 
-// Per-device facts, queried once: SM count, occupancy of every kernel and a
-// library-owned memory pool that keeps its memory (release threshold = max),
+// Per-device facts, queried once: SM count, occupancy of every kernel, the largest
+// clusters and a library-owned memory pool that keeps its memory (release threshold = max),
 // so steady-state scratch allocations never reach the driver.
 int device_info(DevInfo **out) {
   int dev = 0;
@@ -119,8 +124,8 @@ int device_info(DevInfo **out) {
       if (e == cudaSuccess) e = prepare_linear_tc_kernels();
       if (e == cudaSuccess) e = prepare_attention_kernels();
       if (e == cudaSuccess) e = prepare_moe_kernels();
-      if (e == cudaSuccess) e = prepare_route_kernels();
-      if (e == cudaSuccess) e = prepare_sample_kernels();
+      if (e == cudaSuccess) e = prepare_route_kernels(&d.route_ctas);
+      if (e == cudaSuccess) e = prepare_sample_kernels(&d.sample_ctas);
       if (e != cudaSuccess) return map_cuda(e);
       cudaMemPoolProps props = {};
       props.allocType = cudaMemAllocationTypePinned;
@@ -792,7 +797,7 @@ int nvfp4_moe_route(const void *x, int64_t x_stride, int64_t tokens, const void 
   const RouteArgs a = {x, x_stride, tokens, router, fp32, router_stride, hidden, experts, top_k, bias,
                        scoring == NVFP4_SCORE_SIGMOID, renormalize != 0, scale, ids, weights};
   TraceScope tr(kTrMoeRoute, stream);
-  return map_cuda(launch_route(a, d->sms, stream));
+  return map_cuda(launch_route(a, d->sms, most_ctas(d->route_ctas), stream));
 }
 
 int64_t nvfp4_moe_workspace_bytes(const nvfp4_experts *experts, int64_t tokens, int top_k) {
@@ -866,7 +871,7 @@ int nvfp4_sample(const void *logits, int dtype, int64_t stride, int64_t rows, in
                         s.min_p, s.top_k, s.temperature_all, s.top_p_all, s.min_p_all, s.top_k_all, uniform, token,
                         logprob};
   TraceScope tr(kTrSample, stream);
-  return map_cuda(launch_sample(a, d->sms, stream));
+  return map_cuda(launch_sample(a, d->sms, most_ctas(d->sample_ctas), stream));
 }
 
 int64_t nvfp4_swizzled_scales_bytes(int64_t rows, int64_t cols) {
@@ -933,6 +938,12 @@ int nvfp4_test_fail_allocations(int count) {
 
 int nvfp4_test_first_wait_tries(int64_t tries) {
   g_first_wait.store(tries < 0 ? -1L : (long)std::min<int64_t>(tries, int64_t(1) << 30));
+  return NVFP4_OK;
+}
+
+int nvfp4_test_small_clusters(int on) {
+  if (on != 0 && on != 1) return NVFP4_ERR_INVALID_ARG;
+  g_small_clusters.store(on != 0);
   return NVFP4_OK;
 }
 

@@ -197,10 +197,11 @@ bool moe_fits(int64_t hidden, int64_t inner, int experts, int pairs);
 size_t moe_workspace_bytes(int64_t hidden, int64_t inner, int pairs);
 cudaError_t prepare_moe_kernels();
 cudaError_t launch_moe(const MoeArgs &a, int sms, void *ws, cudaStream_t st);
-cudaError_t prepare_route_kernels();
-cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st);
-cudaError_t prepare_sample_kernels();
-cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t st);
+// *ctas: of a cluster at most, by what the device can place (8 or 16)
+cudaError_t prepare_route_kernels(int *ctas);
+cudaError_t launch_route(const RouteArgs &a, int sms, int most_ctas, cudaStream_t st);
+cudaError_t prepare_sample_kernels(int *ctas);
+cudaError_t launch_sample(const SampleArgs &a, int sms, int most_ctas, cudaStream_t st);
 int64_t ffma_probe_fmas_per_thread(int packed, int64_t rounds);
 cudaError_t launch_ffma_probe(int packed, int64_t rounds, int grid, float *sink, cudaStream_t st);
 int ffma_probe_threads();

@@ -564,8 +564,6 @@ auto with_route(bool fp32, int g, F f) {
   return fp32 ? pick(0.0f) : pick(__nv_bfloat16());
 }
 
-int g_route_ctas = 8;  // of a cluster for few tokens
-
 size_t route_smem(const RouteLaunch &p, int g) {
   return ((size_t)std::max(p.splits * p.per * g, p.a.experts) + (size_t)p.a.experts) * sizeof(double);
 }
@@ -578,7 +576,7 @@ size_t route_tc_smem(const RouteLaunch &p) {
 
 }  // namespace
 
-cudaError_t prepare_route_kernels() {
+cudaError_t prepare_route_kernels(int *ctas) {
   // splits * rows <= 128 rows of 16 tokens, and 1024 experts
   const int most = (128 * kTcTokens + 4 * kMaxExperts) * 8 + (3 * kMaxExperts + 128 + kTcWarps * 2 * kTcTokens) * 4;
   cudaError_t e = cudaFuncSetAttribute(k_moe_route_tc<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -599,11 +597,11 @@ cudaError_t prepare_route_kernels() {
   cfg.numAttrs = 1;
   int clusters = 0;
   if (cudaOccupancyMaxActiveClusters(&clusters, k_moe_route<float, 1>, &cfg) != cudaSuccess) cudaGetLastError();  // (8 then)
-  g_route_ctas = clusters > 0 ? kRouteMaxCtas : 8;
+  *ctas = clusters > 0 ? kRouteMaxCtas : 8;
   return cudaSuccess;
 }
 
-cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st) {
+cudaError_t launch_route(const RouteArgs &a, int sms, int most_ctas, cudaStream_t st) {
   RouteLaunch p = {a, 0, 1};
   // The tensor cores where they fill their tiles.  Measured (us, then the other kernel's):
   // 7168, 256 experts: 16 tokens 30 and 33, 64 33 and 53, 256 39 and 266; 2048, 128
@@ -619,7 +617,7 @@ cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t st) {
     // through L2 is shared by a cluster's tokens, but a lane's work is theirs together
     g = 1, threads = kRouteThreads;
     // (1 token 7168, 256 experts: 23 us with clusters of 8, 14 with 16; 2048, 128 experts: 7.9 and 6.6)
-    if (a.experts >= 32 && a.tokens * kRouteMaxCtas <= sms) ctas = g_route_ctas;
+    if (a.experts >= 32 && a.tokens * kRouteMaxCtas <= sms) ctas = most_ctas;
     p.per = (a.experts + ctas - 1) / ctas;
     p.splits = std::max(1, std::min<int>(kRouteWarps / p.per, (int)(a.hidden / 256)));
     while (g < 8 && (a.tokens + g - 1) / g * ctas > 2 * sms) g *= 2;

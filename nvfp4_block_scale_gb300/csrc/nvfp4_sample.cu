@@ -617,10 +617,8 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) k_sample(const __grid_
 
 namespace {
 
-int g_sample_ctas = 8;  // of a cluster at most
-
 template <typename T, bool CUTS>
-cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
+cudaError_t sample_launch(const SampleArgs &a, int sms, int most_ctas, cudaStream_t st) {
   // As few CTAs per row as let two of them share an SM (three, of twice as many, took 7 %
   // longer on 256 x 151003, half as many that read a third of their row again 58 %); more, down to 2048 tokens each, while that
   // leaves SMs idle.
@@ -628,7 +626,7 @@ cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
   const int64_t share = 112 * 1024;
   auto fixed = [&](int c) { return (int64_t)sizeof(SampleShared<CUTS>) + sample_slices(CUTS, c); };
   auto seg = [&](int c) { return (a.vocabulary + c - 1) / c; };
-  while (ctas < g_sample_ctas && (seg(ctas) > (share - fixed(ctas)) / 4 - 8 || ((int64_t)a.rows * ctas < sms && seg(ctas) > 2048)))
+  while (ctas < most_ctas && (seg(ctas) > (share - fixed(ctas)) / 4 - 8 || ((int64_t)a.rows * ctas < sms && seg(ctas) > 2048)))
     ctas *= 2;
   SampleLaunch p = {a, seg(ctas), 0, 0};
   p.run = (p.seg + kSampleThreads - 1) / kSampleThreads | 1;
@@ -651,13 +649,13 @@ cudaError_t sample_launch(const SampleArgs &a, int sms, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_sample(const SampleArgs &a, int sms, cudaStream_t st) {
+cudaError_t launch_sample(const SampleArgs &a, int sms, int most_ctas, cudaStream_t st) {
   const bool cuts = a.top_k || a.top_p || (a.top_k_all > 0 && a.top_k_all < a.vocabulary) || a.top_p_all < 1.0f;
-  if (a.fp32) return cuts ? sample_launch<float, true>(a, sms, st) : sample_launch<float, false>(a, sms, st);
-  return cuts ? sample_launch<__nv_bfloat16, true>(a, sms, st) : sample_launch<__nv_bfloat16, false>(a, sms, st);
+  if (a.fp32) return cuts ? sample_launch<float, true>(a, sms, most_ctas, st) : sample_launch<float, false>(a, sms, most_ctas, st);
+  return cuts ? sample_launch<__nv_bfloat16, true>(a, sms, most_ctas, st) : sample_launch<__nv_bfloat16, false>(a, sms, most_ctas, st);
 }
 
-cudaError_t prepare_sample_kernels() {
+cudaError_t prepare_sample_kernels(int *ctas) {
   auto prepare = [](auto *k) {
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -682,7 +680,7 @@ cudaError_t prepare_sample_kernels() {
   cfg.numAttrs = 1;
   int clusters = 0;
   if (cudaOccupancyMaxActiveClusters(&clusters, k_sample<float, true, 1>, &cfg) != cudaSuccess) cudaGetLastError();  // (8 then)
-  g_sample_ctas = clusters > 0 ? kSampleMaxCtas : 8;
+  *ctas = clusters > 0 ? kSampleMaxCtas : 8;
   return cudaSuccess;
 }
 

@@ -277,3 +277,30 @@ def test_a_step_of_them_together(shape):
     # every tensor between two operators is rounded to bf16, as in the decoder layer's test; the tokens follow from the
     # logits that the plain layer gets too, but for those roundings: see moe_layer.run
     assert worst <= 2.0 ** -6 and tokens == want and us > 0
+
+
+def test_clusters_of_eight():
+    """As on a device that places none of sixteen: the same tokens and experts, and weights within what a sum's order moves."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((3, 2048), generator=g, device="cuda").to(torch.bfloat16)
+    router = 0.03 * torch.randn((128, 2048), generator=g, device="cuda")
+    u = torch.rand(3, generator=g, device="cuda")
+    logits = [(2.5 * torch.randn((3, v), generator=g, device="cuda")).to(kind) for v in (32000, 262144, 1 << 20)
+              for kind in (torch.bfloat16, torch.float32)]
+    settings = (dict(), dict(top_k=40), dict(top_k=2000, top_p=0.9), dict(top_p=0.9, temperature=1.5), dict(min_p=0.05))
+
+    def calls():
+        routed = [nv.moe_route(x, r, 8, s) for r in (router, router.to(torch.bfloat16)) for s in ("softmax", "sigmoid")]
+        return routed, [nv.sample(t, u, return_logprob=True, **s) for t in logits for s in settings]
+
+    routed, sampled = calls()
+    assert nv.nvfp4_test_small_clusters(1) == 0
+    try:
+        routed8, sampled8 = calls()
+    finally:
+        nv.nvfp4_test_small_clusters(0)
+    for a, b in zip(sampled, sampled8):  # (sums of whole numbers)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for (i, w), (i8, w8) in zip(routed, routed8):
+        # logits to 2^-46 of |x| |r| (at most 2^7) become weights with the same few fp32 roundings
+        assert torch.equal(i, i8) and bool(((w - w8).abs() <= 2.0 ** -20 * w).all())

@@ -1,6 +1,8 @@
 """The entry points of the mixture-of-experts layer and of sampling on the
 host: what they refuse, with which status, before touching the device."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -158,3 +160,16 @@ def test_bindings_refuse_host_tensors():
         nv.sample(cpu, torch.zeros(2))
     with pytest.raises(ValueError):
         nv.Experts(*(tuple(torch.zeros((2, 32, n), dtype=torch.uint8) for n in (32, 4)) + (torch.ones(2),) for _ in range(2)))
+
+
+def test_what_a_device_places_is_kept_by_device():
+    """No kernel file holds a variable of its own (of one device's, another's call would read it, and threads race for it)."""
+    csrc = os.path.join(os.path.dirname(nv.__file__), "csrc")
+    for name in ("nvfp4_route.cu", "nvfp4_sample.cu", "nvfp4_moe.cu"):
+        text = open(os.path.join(csrc, name)).read()
+        assert re.findall(r"^(?:static )?(?:std::\w+<\w+>|int|bool|size_t|int64_t|uint\w+_t) \w+ *(?:=|\{[^}]*\};|;|\[)", text, re.M) == []
+
+
+def test_small_clusters_are_asked_for_by_a_truth_value():
+    assert nv.nvfp4_test_small_clusters(2) == INVALID and nv.nvfp4_test_small_clusters(-1) == INVALID
+    assert nv.nvfp4_test_small_clusters(1) == 0 and nv.nvfp4_test_small_clusters(0) == 0
