@@ -853,7 +853,8 @@ int nvfp4_moe(const nvfp4_experts *experts, const void *x, int64_t x_stride, int
 int nvfp4_sample(const void *logits, int dtype, int64_t stride, int64_t rows, int64_t vocabulary,
                  const nvfp4_sampling *sampling, const float *uniform, int32_t *token, float *logprob, cudaStream_t stream) {
   if ((dtype != NVFP4_DTYPE_BF16 && dtype != NVFP4_DTYPE_FP32) || rows < 0 || rows > (int64_t(1) << 27) ||
-      vocabulary < 0 || vocabulary > kMaxVocabulary || stride < vocabulary || stride >= kMaxElems)
+      vocabulary < 0 || vocabulary > kMaxVocabulary || stride < vocabulary || stride >= kMaxElems ||
+      stride > INT64_MAX / 4 / std::max<int64_t>(1, rows))
     return NVFP4_ERR_INVALID_ARG;
   if (rows > 0 && ((vocabulary > 0 && !logits) || !uniform || !token)) return NVFP4_ERR_INVALID_ARG;
   nvfp4_sampling s = {};

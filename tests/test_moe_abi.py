@@ -173,3 +173,8 @@ def test_what_a_device_places_is_kept_by_device():
 def test_small_clusters_are_asked_for_by_a_truth_value():
     assert nv.nvfp4_test_small_clusters(2) == INVALID and nv.nvfp4_test_small_clusters(-1) == INVALID
     assert nv.nvfp4_test_small_clusters(1) == 0 and nv.nvfp4_test_small_clusters(0) == 0
+
+
+def test_sample_refuses_rows_past_every_address():
+    for rows, stride in ((1 << 27, 1 << 39), (1 << 27, 1 << 35), (1 << 24, 1 << 38)):
+        assert _sample(rows=rows, stride=stride) == INVALID
