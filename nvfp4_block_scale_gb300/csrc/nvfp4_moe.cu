@@ -88,7 +88,9 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 // The power of two (its exponent) that brings a largest magnitude of these bits
-// into [2^14, 2^15); for an infinity or a NaN one that leaves it what it is.
+// into [2^14, 2^15), or up to 2^126; for an infinity or a NaN one that leaves it what it is.
+// (2^126 is enough: it brings bf16's smallest, 2^-133, to 2^-7, which f16 holds with all of
+// bf16's bits, and half of f16's last step, 2^-25, back to 2^-151, below fp32's own 2^-150.)
 __device__ __forceinline__ int f16_up(unsigned top) { return min(14 + 127 - (int)(top >> 23), 126); }
 
 // How a unit's codes and scales reach shared memory, by what their rows' addresses allow:

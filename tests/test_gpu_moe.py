@@ -85,3 +85,68 @@ def test_slots_without_an_expert_and_named_twice():
         assert torch.equal(y[0].cpu(), (residual if residual is not None else torch.zeros_like(r))[0])
     empty = torch.full_like(ids, -1)
     assert torch.equal(_run(host, x, empty, w, "silu", r).cpu(), r)
+
+
+# vectors so long that a job takes three pairs, or one; so long that one fits only beside eight warps' units (rows of codes
+# in whole words and on any byte; of x, of h)
+@pytest.mark.parametrize("shape", [(12, 48, 14336, 2, 2), (16, 14336, 32, 2, 2), (9, 16, 49152, 3, 2), (5, 49152, 16, 2, 2),
+                                   (2, 16, 73728, 2, 2), (2, 16, 73744, 2, 2), (2, 73744, 16, 2, 2)])
+def test_long_vectors(shape):
+    tokens, hidden, inner, n, k = shape
+    host = moe_ref.experts(n, hidden, inner, tokens % 2 == 0, seed=sum(shape))
+    x, ids, w, r = _inputs(tokens, hidden, n, k, 13)
+    _check(host, x, ids, w, "silu", r, _run(host, x, ids, w, "silu", r))
+
+
+def test_longest_vectors_that_every_call_takes():
+    """49152 columns with the most experts and pairs that a launch has.  The experts are one expert's tensors 1024
+    times (0 bytes apart), so that a token's slots sum to its product times the sum of their weights."""
+    host = moe_ref.experts(1, 16, 49152, False, 23)
+    x, _, _, _ = _inputs(64, 16, 1024, 1, 24)
+    g = torch.Generator().manual_seed(25)
+    ids = torch.stack([torch.randperm(1024, generator=g)[:32] for _ in range(64)]).int()
+    w = torch.rand((64, 32), generator=g) + 0.1
+    up, down = (tuple(t.cuda().expand(1024, *t.shape[1:]) for t in m) for m in host[:2])
+    y = nv.moe(nv.Experts(up, down), x.cuda(), ids.cuda(), w.cuda())
+    want, err = moe_ref.moe(*host, x.double().numpy(), torch.zeros((64, 1), dtype=torch.int32).numpy(),
+                            w.double().sum(1, keepdim=True).numpy(), "silu")
+    # (31 more slots of one sign: as many more roundings of the slots' sum)
+    assert within(y.double().cpu().numpy(), want, err + 31 * 2.0 ** -24 * (abs(want) + err))
+
+
+def test_entries_down_to_the_smallest_bf16():
+    """Vectors whose largest entry is 2^-95 or less enter the products exactly: bf16 ends at 2^-133.  The largest meets
+    weights of 0, so that the others are what the output shows."""
+    host = moe_ref.experts(2, 128, 64, False, 26)
+    up, down, _ = host
+    up[0][:, :, 0] &= 0xF0  # (a byte's lower half is the even column)
+    host = (up[0], up[1], up[2] * 2.0 ** 100), (down[0], down[1], down[2] * 2.0 ** 30), None
+    g = torch.Generator().manual_seed(27)
+    x = torch.randint(-127, 128, (8, 128), generator=g).double() * 2.0 ** -133
+    x[:, 0] = torch.tensor([2.0 ** e for e in (-95, -100, -110, -112, -113, -120, -126, -133)], dtype=torch.float64)
+    exact = x.numpy().copy()
+    x = x.to(torch.bfloat16)
+    assert (x.double().numpy() == exact).all()
+    ids, w = torch.arange(8).int()[:, None] % 2, torch.ones((8, 1))
+    y = _run(host, x, ids, w, "none")
+    _check(host, x, ids, w, "none", None, y)
+    assert bool((y != 0).any(1).all())
+
+
+def test_products_between_that_fp32_hardly_holds():
+    """h around 2^-130: f16 of eight's common power of two ends no higher than fp32 itself."""
+    host = moe_ref.experts(2, 64, 128, False, 28)
+    up, down, _ = host
+    up, down = (up[0], up[1], up[2] * 2.0 ** -120), (down[0], down[1], down[2] * 2.0 ** 110)
+    g = torch.Generator().manual_seed(29)
+    x = (torch.randn((6, 64), generator=g) * 2.0 ** torch.tensor([0.0, -4, -8, -10, -12, 4])[:, None]).to(torch.bfloat16)
+    ids, w = torch.arange(6).int()[:, None] % 2, torch.ones((6, 1))
+    y = _run((up, down, None), x, ids, w, "none").double().cpu().numpy()
+    for t in range(6):
+        mats = [(moe_ref.weights(m[0][t % 2].numpy(), m[1][t % 2].numpy()), float(m[2][t % 2])) for m in (up, down)]
+        xt = x[t].double().numpy()
+        h, eh = moe_ref._product(*mats[0], xt, 0.0 * xt + 2.0 ** -39 * abs(xt).max())
+        # fp32's own end, twice, and that of f16 under 2^126: 2^-150, 2^-150 and 2^-151
+        eh = eh + 2.0 ** -12 * (abs(h) + eh) + 2.0 ** -38 * (abs(h) + eh).max() + 2.5 * 2.0 ** -150
+        want, err = moe_ref._product(*mats[1], h, eh)
+        assert within(y[t], want, err + 3 * 2.0 ** -24 * (abs(want) + err))
