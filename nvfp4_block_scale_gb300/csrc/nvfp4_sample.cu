@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) k_sample(const __grid_
       int at;
       b = find_bin(1, b, mass, goal, &at, &inside);
       high = hk - ((uint64_t)at << down);  // (keys of finite values are above 2^54, a bin's width is at most 2^53)
-      low = high - ((1ull << down) - 1);
+      low = max(high - ((uint64_t{1} << down) - 1), lk);  // (the last bin reaches below lk, where the next range's tokens are)
     }
     gather(in_range);  // (there are `inside` of them)
     if (rank == 0) {

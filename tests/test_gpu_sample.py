@@ -162,3 +162,28 @@ def test_largest_vocabulary():
         _check(x, u, **s)
     with pytest.raises(nv.Nvfp4Error):
         nv.sample(torch.zeros((1, (1 << 20) + 1), device="cuda"), u[:1].cuda())
+
+
+def test_cuts_at_the_end_of_a_range():
+    """A cut among the last tokens of a range that is split again, tokens of the next range right behind them.  Values two
+    steps of fp32 apart: a range of the exponent is 83300 of them wide, a finer one 64."""
+    v, rows = 120000, 34
+    g = torch.Generator().manual_seed(11)
+    line = 1.0 - 2.0 ** -23 * torch.arange(v, dtype=torch.float64)
+    x = torch.stack([line[torch.randperm(v, generator=g)] for _ in range(rows)]).float()
+    u = torch.rand(rows, generator=g)
+    edge = int((22 / (0.75 * 2048 * 1.4426950408889634)) * 2.0 ** 23)
+    k = edge - 132 + 8 * torch.arange(rows, dtype=torch.int32)
+    _check(x, u, top_k=k)
+    w = torch.exp(line - 1.0)
+    _check(x, u, top_p=((w.cumsum(0) - 0.5 * w)[k.long() - 1] / w.sum()).float())  # (half a token before the k-th's end)
+
+
+def test_top_p_of_a_large_top_k_of_nearly_equal_weights():
+    """Every weight is 1 in 42 bits, so the cuts go by count: 5795 tokens, then 5216 of them."""
+    g = torch.Generator().manual_seed(447325616)
+    x = 0.5 * torch.randn((7, 64418), generator=g)
+    x[torch.rand(x.shape, generator=g) < 0.1] = -INF
+    u = torch.rand(7, generator=g)
+    for _ in range(3):
+        _check(x.to(torch.bfloat16), u, temperature=1e30, top_k=5795, top_p=0.9)
