@@ -412,7 +412,7 @@ int nvfp4_moe_route(const void *x, int64_t x_stride, int64_t tokens, const void 
  *   nvfp4_linear.  x enters in f16, each vector scaled by a power of two: its
  *   entries are exact down to 2^-31 of its largest, and those below are off by at
  *   most 2^-39 of it.  h is rounded to the 11 bits of f16 under such
- *   scales (off by at most 2^-12 of an entry or 2^-38 of the vector's largest, or,
+ *   scales (off by at most 2^-11 of an entry or 2^-38 of the vector's largest, or,
  *   where that is below what fp32 holds, 2^-151).  A
  *   slot whose id is outside [0, experts) adds nothing: padding tokens of a
  *   captured batch carry -1.  An expert may be named any number of times, by

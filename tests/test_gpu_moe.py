@@ -1,5 +1,6 @@
 """The experts' products against the plain 64-bit form, within the bound that
 moe_ref derives."""
+import numpy as np
 import pytest
 import torch
 
@@ -133,20 +134,44 @@ def test_entries_down_to_the_smallest_bf16():
     assert bool((y != 0).any(1).all())
 
 
+def _one_slot(host, e, x, act):
+    """(y, bound) of one token's only slot, of weight 1, as moe_ref.moe, with f16's own half step for h: 11 bits are 2^-11
+    of a value at most (of 1 + 2^-11, say, whose neighbours are 1 and 1 + 2^-10); and fp32's end, twice, and that of f16
+    under 2^126: 2^-150, 2^-150 and 2^-151."""
+    up, down, gate = (None if m is None else (moe_ref.weights(m[0][e].numpy(), m[1][e].numpy()), float(m[2][e])) for m in host)
+    ex = np.full(len(x), 2.0 ** -39 * np.abs(x).max())
+    h, eh = moe_ref._product(*up, x, ex)
+    if gate is not None:
+        g, eg = moe_ref._product(*gate, x, ex)
+        a, ea = moe_ref.activation(g, act), 1.13 * eg + 2.0 ** -20 * np.abs(g)
+        h, eh = a * h, ea * np.abs(h) + np.abs(a) * eh + ea * eh
+    else:
+        h, eh = moe_ref.activation(h, act), 1.13 * eh + 2.0 ** -20 * np.abs(h)
+    eh = eh + 2.0 ** -24 * np.abs(h)
+    eh = eh + 2.0 ** -11 * (np.abs(h) + eh) + 2.0 ** -38 * (np.abs(h) + eh).max() + 2.5 * 2.0 ** -150
+    y, err = moe_ref._product(*down, h, eh)
+    return y, err + 3 * 2.0 ** -24 * (np.abs(y) + err)
+
+
 def test_products_between_that_fp32_hardly_holds():
     """h around 2^-130: f16 of eight's common power of two ends no higher than fp32 itself."""
-    host = moe_ref.experts(2, 64, 128, False, 28)
-    up, down, _ = host
-    up, down = (up[0], up[1], up[2] * 2.0 ** -120), (down[0], down[1], down[2] * 2.0 ** 110)
+    up, down, _ = moe_ref.experts(2, 64, 128, False, 28)
+    host = (up[0], up[1], up[2] * 2.0 ** -120), (down[0], down[1], down[2] * 2.0 ** 110), None
     g = torch.Generator().manual_seed(29)
     x = (torch.randn((6, 64), generator=g) * 2.0 ** torch.tensor([0.0, -4, -8, -10, -12, 4])[:, None]).to(torch.bfloat16)
     ids, w = torch.arange(6).int()[:, None] % 2, torch.ones((6, 1))
-    y = _run((up, down, None), x, ids, w, "none").double().cpu().numpy()
+    y = _run(host, x, ids, w, "none").double().cpu().numpy()
     for t in range(6):
-        mats = [(moe_ref.weights(m[0][t % 2].numpy(), m[1][t % 2].numpy()), float(m[2][t % 2])) for m in (up, down)]
-        xt = x[t].double().numpy()
-        h, eh = moe_ref._product(*mats[0], xt, 0.0 * xt + 2.0 ** -39 * abs(xt).max())
-        # fp32's own end, twice, and that of f16 under 2^126: 2^-150, 2^-150 and 2^-151
-        eh = eh + 2.0 ** -12 * (abs(h) + eh) + 2.0 ** -38 * (abs(h) + eh).max() + 2.5 * 2.0 ** -150
-        want, err = moe_ref._product(*mats[1], h, eh)
-        assert within(y[t], want, err + 3 * 2.0 ** -24 * (abs(want) + err))
+        assert within(y[t], *_one_slot(host, t % 2, x[t].double().numpy(), "none"))
+
+
+@pytest.mark.parametrize("hidden,inner", [(16, 16), (32, 16), (48, 32), (16, 96), (64, 80)])
+@pytest.mark.parametrize("act,gated", [("none", True), ("relu", True), ("gelu_tanh", True), ("silu", False)])
+def test_small_layers(hidden, inner, act, gated):
+    """So few columns that single roundings of h show in an output."""
+    host = moe_ref.experts(30, hidden, inner, gated, hidden + inner)
+    x, _, _, _ = _inputs(240, hidden, 30, 1, 31)
+    ids, w = torch.arange(240).int()[:, None] % 30, torch.ones((240, 1))
+    y = _run(host, x, ids, w, act).double().cpu().numpy()
+    for t in range(240):
+        assert within(y[t], *_one_slot(host, t % 30, x[t].double().numpy(), act))
