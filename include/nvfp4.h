@@ -383,7 +383,10 @@ int nvfp4_paged_attention(const nvfp4_kv_cache *cache, const void *q, int64_t q_
  *   and a NaN is below every number.  ids are in descending order of the score.
  *   Weights are fp32; those of many tokens (128 or more, or 16 with 8192 scores
  *   among them) follow logits of fp32 accuracy (off by 2^-18 of ||x|| ||router[e]||
- *   at most, 2^-16 with an fp32 router).  Results repeat bit for bit.
+ *   at most, 2^-16 with an fp32 router), so a token's weights may differ that much
+ *   between a small and a large batch.  Products and their sums are
+ *   formed in fp32: a token and expert whose |x router| sum to 2^127 or more
+ *   have no logit (NaN).  Results repeat bit for bit.
  * Arguments:
  *   x       device, bf16, 16-byte aligned, [tokens][hidden], rows x_stride
  *           elements apart (>= hidden, a multiple of 8).  x and router finite.
@@ -483,7 +486,9 @@ int nvfp4_moe(const nvfp4_experts *experts, const void *x, int64_t x_stride, int
  *   they are never chosen; a row without others gives token -1, logprob -inf.
  *   Infinite logits share their row evenly.
  *   Weights are whole numbers of 2^-42, off by at most 2^-30 of themselves or one
- *   unit, their sums and every comparison of sums exact, so results repeat bit for bit.
+ *   unit (so a token is never chosen whose w is below 2^-42, or whose l lies so far
+ *   below m that fp32 does not hold l - m), their sums and every comparison of sums
+ *   exact, so results repeat bit for bit.
  * Arguments:
  *   logits  device, bf16 or fp32 (dtype), aligned to its type, [rows][vocabulary],
  *           rows stride elements apart (>= vocabulary).

@@ -3,11 +3,11 @@
 //   h[t,s] = act(alpha_g sum_c q Delta x[t][c]) * (alpha_u sum_c q Delta x[t][c]),  expert ids[t][s]
 //   y[t]   = bf16( residual[t] + sum_s weights[t][s] alpha_d sum_j q Delta h[t,s][j] ).
 //
-// Bound: reading once the weights of every expert that some token names
+// Floor: reading once the weights of every expert that some token names
 // (0.5625 B each); a token's share of x, h and y is small beside them.  Measured
-// with cold weights, and the rate at which those came (a copy reads and writes
+// with cold weights, and those weights' bytes over the time (a copy reads and writes
 // 6.77 TB/s):
-//   33 tokens 7168 x 2048, 8 of 256       612 us   6.0 TB/s
+//   33 tokens 7168 x 2048, 8 of 256  612 to 646 us   5.7 to 6.0 TB/s (by the box)
 //    5 tokens 4096 x 14336, 2 of 8        105      4.7
 //   61 tokens 2048 x 768, 8 of 128         79      3.8
 //   256 tokens 2064 x 1424, 6 of 60       164      1.2  (no gate; 26 pairs an expert, 110 TFLOP/s)
@@ -15,6 +15,14 @@
 // What the largest leaves is the plan, the first fetches (4 to 6 us a launch) and
 // CTAs that end apart (5 to 10); with less work those weigh more, with many pairs an
 // expert the MMAs of their n-tiles and their vectors' way into shared memory.
+//
+// An expert's weights are gone over once for each of its jobs, and a job's pairs are
+// limited by its vectors, which lie whole in shared memory: 32 up to about 1500 columns,
+// 24 to 29 at 2048, 13 to 16 at 4096, 7 to 9 at 7168, 3 to 5 at 14336.  So many pairs on wide
+// experts fetch, form and multiply the same weights again (in brackets how many times):
+//   4096 x 14336, 2 of 8:  5 tokens 107 us (1.07 times)    16 tokens 214 (1.2)
+//                          33       292    (1.9)           64        478 (2.9)    256  1645 (10.3)
+//   256 tokens 7168 x 2048, 8 of 256: 2046 us (1.4); 4096 x 2048, 6 of 64: 477 (2.0)
 //
 // Three launches, each waiting for the one before through a programmatic
 // dependency: gate and up with the activation (h, f16 with a power of two for each

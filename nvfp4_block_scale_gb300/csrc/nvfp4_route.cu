@@ -12,7 +12,7 @@
 // Bound: latency for a few tokens (1 token 2048, 8 of 128: 6.4 us, of which a launch
 // and the router's first bytes are 3); from about 64 tokens on the 7 fp32 operations a
 // product, so many tokens take the tensor cores, and those operations only where the
-// tensor cores leave the order of two experts open (61 tokens 4096, 2 of 8: 8.5 us;
+// tensor cores leave the order of two experts open (61 tokens 4096, 2 of 8: 8.3 us;
 // 256 x 7168, 8 of 256: 47 us, 20 TFLOP/s, where the operations for all took 266; 17 to
 // 25 of them are loads and products, 5 the choice, up to 8 the doubtful experts).
 //
@@ -603,10 +603,16 @@ cudaError_t prepare_route_kernels(int *ctas) {
 
 cudaError_t launch_route(const RouteArgs &a, int sms, int most_ctas, cudaStream_t st) {
   RouteLaunch p = {a, 0, 1};
-  // The tensor cores where they fill their tiles.  Measured (us, then the other kernel's):
-  // 7168, 256 experts: 16 tokens 30 and 33, 64 33 and 53, 256 39 and 266; 2048, 128
-  // experts: 31 tokens 15 and 11, 64 17 and 15, 128 15 and 20; 4096, 60 experts: 64 tokens
-  // 16 and 15, 128 12 and 20; 4096, 8 experts: 64 tokens 11 and 10, 128 11 and 11, 256 14 and 28.
+  // The tensor cores where there are many scores.  Measured with a bf16 router, softmax (us, then the
+  // other kernel's), where the rule takes them: 64 tokens 7168, 256 experts 31 and 53; 32 tokens 31 and 34;
+  // 128 tokens 2048, 128 experts 16 and 20; 128 tokens 4096, 60 experts 17 and 20; 256 tokens 4096, 8 experts
+  // 14 and 28; 64 tokens 4096, 128 experts 18 and 19; and where it does not: 31 tokens 2048, 128 experts 13
+  // and 11; 64 tokens 4096, 60 experts 16 and 14; 64 tokens 4096, 8 experts 11 and 9.  It looks at tokens and
+  // scores alone, since the accuracy of the weights goes by it, and so takes the slower kernel near its edges:
+  // 64 tokens 2048, 128 experts 16 and 15 (1024: 15 and 11), 128 tokens 4096, 8 experts 12 and 10 (256, 32
+  // experts: 9 and 6), and the other way 16 tokens 7168, 256 experts 28 and 33, 127 tokens 4096, 64 experts 17
+  // and 20.  With an fp32 router both take longer: 64 tokens 7168, 256 experts 45 and 62; 64 tokens 4096, 128
+  // experts 24 and 22; 128 tokens 4096, 8 experts 17 and 11.
   const bool tc = a.tokens >= 128 || (a.tokens >= 16 && a.tokens * a.experts >= 8192);
   int g = kTcTokens, ctas = kTcCtas, threads = kTcThreads;
   p.per = (a.experts + ctas - 1) / ctas;
